@@ -77,6 +77,13 @@ enum {
    violation (see dsatopk_paged). */
 #define DSATOPK_MAX_SEQ_LEN 131072
 
+/* Element types of the serving operators' inputs. */
+enum {
+    DSATOPK_BF16 = 0, /* bfloat16 */
+    DSATOPK_FP16 = 1, /* IEEE half */
+    DSATOPK_FP8 = 2   /* e4m3 without infinities (OCP), scores only */
+};
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char* dsatopk_status_string(int status);
 
@@ -270,6 +277,115 @@ int dsatopk_paged_noalloc(const float* scores, int64_t score_stride, const int32
                           const int32_t* row_starts, const int32_t* page_table,
                           int64_t page_table_stride, int32_t page_size, int32_t num_rows,
                           int32_t k, int32_t* out, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The serving operators around the selection: page maps, indexer scores and
+ * latent attention. The conventions above hold for them too (device
+ * pointers, asynchronous, no allocation, only kernel launches). Strides are
+ * in elements; a tensor's last dimension is contiguous. Every call reads
+ * inputs at its stated bounds only: page numbers and slots outside a cache
+ * are treated as absent.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * dsatopk_page_maps - the pages, cache slots and top-k row arguments of a
+ * serving step, from its request lengths.
+ *
+ *   seq_lens      int32 [num_requests]: tokens of each request after the
+ *                 step; negative values are read as 0.
+ *   new_lens      int32 [num_requests]: those of them that the step adds,
+ *                 clamped to [0, seq_len]. NULL: min(1, seq_len).
+ *   page_table    int32 [num_requests, page_table_width], rows
+ *                 page_table_stride apart. Request r's entries below
+ *                 ceil((seq_len - new_len) / page_size) are the pages that
+ *                 it holds. The following ones, up to ceil(seq_len /
+ *                 page_size), are WRITTEN with pages of the free list: the
+ *                 list's pages go to the requests in order, each request's
+ *                 in order.
+ *   page_size     power of two in [1, 2^20].
+ *   free_pages    int32 [num_free].
+ *   num_tokens    rows of the outputs below. A step of fewer tokens leaves
+ *                 empty rows behind them; tokens past num_tokens get neither
+ *                 a row nor a page.
+ *
+ * Written, all of them, tokens of request 0 first, each request's in order:
+ *   token_starts  int32 [num_requests + 1]: first token of each request.
+ *   slots         int32 [num_tokens]: page * page_size + offset, where the
+ *                 token's cache entry goes; -1 for an empty row, a page
+ *                 past the table's width, one that the free list did not have
+ *                 (its table entry is then -1), or a slot past 2^31 - 1.
+ *   table_rows    int32 [num_tokens]: the token's request (0 for empty rows).
+ *   row_lens      int32 [num_tokens]: the token's position + 1, which is its
+ *                 causal window (0 for empty rows). With table_rows these
+ *                 are the row arguments of dsatopk_paged_packed,
+ *                 dsatopk_scores_paged and dsatopk_attend_paged.
+ *   counts        int32 [2]: tokens of the step, pages that they open. More
+ *                 tokens than num_tokens, or more pages than num_free: the
+ *                 step did not fit.
+ *
+ * Device-side precondition: the step's tokens and pages, over all requests,
+ * are below 2^31.
+ * Errors: DSATOPK_ERR_INVALID_ARG, DSATOPK_ERR_HIP.
+ */
+int dsatopk_page_maps(const int32_t* seq_lens, const int32_t* new_lens, int32_t num_requests,
+                      int32_t* page_table, int64_t page_table_stride, int32_t page_table_width,
+                      int32_t page_size, const int32_t* free_pages, int32_t num_free,
+                      int32_t num_tokens, int32_t* token_starts, int32_t* slots,
+                      int32_t* table_rows, int32_t* row_lens, int32_t* counts, void* stream);
+
+/*
+ * dsatopk_scores_paged - the indexer's scores over a paged key cache:
+ *
+ *   out[b, j] = key_scale[j] * sum_h weights[b, h] * max(0, q[b, h] . key[j])
+ *
+ * for j in [0, min(seq_lens[b], columns, page_table_width * page_size)),
+ * with key[j] the key at page_table[table_rows[b]][j / page_size], offset
+ * j % page_size. Other columns of out are not written.
+ *
+ *   q             type [num_rows, num_heads, head_dim], strides
+ *                 q_row_stride, q_head_stride.
+ *   weights       float [num_rows, num_heads], rows weight_stride apart.
+ *   keys          type [num_pages, page_size, head_dim], strides
+ *                 key_page_stride, key_token_stride.
+ *   key_scales    float [num_pages, page_size], pages scale_page_stride
+ *                 apart, or NULL (ones).
+ *   type          DSATOPK_BF16, DSATOPK_FP16 or DSATOPK_FP8 (q and keys).
+ *   num_heads     1 .. 128; head_dim 64 or 128.
+ *   seq_lens      int32 [num_rows]; negative values are read as 0.
+ *   table_rows    int32 [num_rows] or NULL (row b reads table row b).
+ *   out           float [num_rows, >= columns], rows out_stride apart; a
+ *                 top-k's score buffer (for it: 16-byte aligned, out_stride
+ *                 a multiple of 4).
+ *   columns       at most 2^30.
+ *
+ * A page outside [0, num_pages) reads as keys of score 0. Products are
+ * exact, sums are fp32.
+ * Errors: DSATOPK_ERR_INVALID_ARG, DSATOPK_ERR_ALIGNMENT (q or keys not
+ * 16-byte aligned, or one of their strides no multiple of 16 bytes),
+ * DSATOPK_ERR_HIP. num_rows == 0 is a no-op.
+ */
+int dsatopk_scores_paged(const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                         const float* weights, int64_t weight_stride, const void* keys,
+                         int64_t num_pages, int64_t key_page_stride, int64_t key_token_stride,
+                         const float* key_scales, int64_t scale_page_stride, int32_t type,
+                         int32_t num_heads, int32_t head_dim, const int32_t* seq_lens,
+                         const int32_t* page_table, int64_t page_table_stride,
+                         int32_t page_table_width, int32_t page_size, const int32_t* table_rows,
+                         int32_t num_rows, float* out, int64_t out_stride, int64_t columns,
+                         void* stream);
+
+/*
+ * dsatopk_scores_ragged - the same over flattened keys [num_keys, head_dim]
+ * (rows key_stride apart; key_scales float [num_keys] or NULL): out[b, c] for
+ * the columns c of row b's window [row_starts[b], row_starts[b] +
+ * seq_lens[b]), as dsatopk_ragged reads them, cut at columns and num_keys.
+ */
+int dsatopk_scores_ragged(const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                          const float* weights, int64_t weight_stride, const void* keys,
+                          int64_t num_keys, int64_t key_stride, const float* key_scales,
+                          int32_t type, int32_t num_heads, int32_t head_dim,
+                          const int32_t* seq_lens, const int32_t* row_starts, int32_t num_rows,
+                          float* out, int64_t out_stride, int64_t columns, void* stream);
 
 #ifdef __cplusplus
 }

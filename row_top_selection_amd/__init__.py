@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 from pathlib import Path
+from typing import NamedTuple
 
 LIB_PATH = Path(__file__).resolve().parent / "libdsatopk.so"
 
@@ -27,7 +28,8 @@ STATUS = {
 NOALLOC_MAX_ROWS = 262144
 
 EXPORTS = ("dsatopk_status_string", "dsatopk_plan_bytes", "dsatopk_plan", "dsatopk_plan_error",
-           "dsatopk_paged", "dsatopk_paged_packed", "dsatopk_ragged", "dsatopk_paged_noalloc")
+           "dsatopk_paged", "dsatopk_paged_packed", "dsatopk_ragged", "dsatopk_paged_noalloc",
+           "dsatopk_page_maps", "dsatopk_scores_paged", "dsatopk_scores_ragged")
 
 
 class DsatopkError(RuntimeError):
@@ -70,6 +72,15 @@ def _lib():
         lib.dsatopk_ragged.restype = ctypes.c_int
         lib.dsatopk_paged_noalloc.argtypes = [P, i64, P, P, P, i64, i32, i32, i32, P, P]
         lib.dsatopk_paged_noalloc.restype = ctypes.c_int
+        lib.dsatopk_page_maps.argtypes = [P, P, i32, P, i64, i32, i32, P, i32, i32, P, P, P, P, P,
+                                          P]
+        lib.dsatopk_page_maps.restype = ctypes.c_int
+        lib.dsatopk_scores_paged.argtypes = [P, i64, i64, P, i64, P, i64, i64, i64, P, i64, i32,
+                                             i32, i32, P, P, i64, i32, i32, P, i32, P, i64, i64, P]
+        lib.dsatopk_scores_paged.restype = ctypes.c_int
+        lib.dsatopk_scores_ragged.argtypes = [P, i64, i64, P, i64, P, i64, i64, P, i32, i32, i32,
+                                              P, P, i32, P, i64, i64, P]
+        lib.dsatopk_scores_ragged.restype = ctypes.c_int
         _handle = lib
     return _handle
 
@@ -267,4 +278,187 @@ def paged_noalloc(scores, seq_lens, page_table, page_size: int, k: int, row_star
         page_table.stride(0), int(page_size), rows, int(k), _ptr(out), _stream(stream))
     if st != 0:
         raise DsatopkError(st, "dsatopk_paged_noalloc")
+    return out
+
+
+class PageMaps(NamedTuple):
+    """What ``page_maps`` writes beside the page table."""
+
+    token_starts: "torch.Tensor"  # int32 [requests + 1]
+    slots: "torch.Tensor"         # int32 [num_tokens], -1: none
+    table_rows: "torch.Tensor"    # int32 [num_tokens]
+    row_lens: "torch.Tensor"      # int32 [num_tokens]
+    counts: "torch.Tensor"        # int32 [2]: tokens, pages opened
+
+
+def _table(page_table, like, name="page_table"):
+    import torch
+
+    if page_table.dtype != torch.int32:
+        raise ValueError(f"{name} must be int32")
+    if page_table.dim() != 2 or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError(f"{name} must be [rows, width] with contiguous columns")
+    if not page_table.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if like is not None:
+        _on(page_table, like, name)
+    return page_table
+
+
+def _row_stride(t):
+    """Elements between t's rows (at least a row: what one row's stride says does not matter)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _stride(t, dim):
+    """t's stride; 0 where one entry makes it meaningless."""
+    return t.stride(dim) if t.shape[dim] > 1 else 0
+
+
+def page_maps(seq_lens, page_table, page_size: int, free_pages, num_tokens: int, new_lens=None,
+              out=None, stream=None):
+    """The pages, slots and top-k row arguments of a serving step.
+
+    Requests of ``seq_lens`` tokens after the step, ``new_lens`` of them new
+    (None: one each), take the pages that they lack from ``free_pages``:
+    these are written into ``page_table`` in place. Returns ``PageMaps``,
+    whose ``slots``, ``table_rows`` and ``row_lens`` have ``num_tokens`` rows
+    (empty ones behind the step's tokens). ``out``: a ``PageMaps`` to write
+    into."""
+    import torch
+
+    n, t = int(seq_lens.shape[0]), int(num_tokens)
+    _vec_i32(seq_lens, n, "seq_lens")
+    _vec_i32(new_lens, n, "new_lens", seq_lens)
+    _table(page_table, seq_lens)
+    if page_table.shape[0] != n:
+        raise ValueError("page_table must have one row per request")
+    _vec_i32(free_pages, int(free_pages.shape[0]), "free_pages", seq_lens)
+    if t < 0:
+        raise ValueError("num_tokens must not be negative")
+    if out is None:
+        sizes = (n + 1, t, t, t, 2)
+        # one allocation, its parts at 16-byte boundaries
+        whole = torch.empty(sum((s + 3) // 4 * 4 for s in sizes), dtype=torch.int32,
+                            device=seq_lens.device)
+        parts, at = [], 0
+        for s in sizes:
+            parts.append(whole[at:at + s])
+            at += (s + 3) // 4 * 4
+        out = PageMaps(*parts)
+    else:
+        for name, size in zip(PageMaps._fields, (n + 1, t, t, t, 2)):
+            _vec_i32(getattr(out, name), size, name, seq_lens)
+    st = _lib().dsatopk_page_maps(
+        _ptr(seq_lens), _ptr(new_lens), n, _ptr(page_table), _row_stride(page_table),
+        page_table.shape[1], int(page_size), _ptr(free_pages), free_pages.shape[0], t,
+        *(_ptr(getattr(out, name)) for name in ("token_starts", "slots", "table_rows", "row_lens",
+                                                "counts")), _stream(stream))
+    if st != 0:
+        raise DsatopkError(st, "dsatopk_page_maps")
+    return out
+
+
+def _element_type(t, name, fp8=False):
+    """The library's number for t's element type."""
+    import torch
+
+    types = {torch.bfloat16: 0, torch.float16: 1}
+    if fp8:
+        types[torch.float8_e4m3fn] = 2
+    if t.dtype not in types:
+        raise ValueError(f"{name} must be one of {', '.join(str(d) for d in types)}")
+    return types[t.dtype]
+
+
+def _tensor(t, dims, like, name):
+    """A device tensor of ``dims`` dimensions with a contiguous last one."""
+    if t.dim() != dims or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name} must have {dims} dimensions, the last one contiguous")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if like is not None:
+        _on(t, like, name)
+    return t
+
+
+def _score_args(q, weights, keys, key_scales, key_dims):
+    import torch
+
+    _tensor(q, 3, None, "q")
+    rows, heads, dim = q.shape
+    _tensor(weights, 2, q, "weights")
+    if weights.dtype != torch.float32 or tuple(weights.shape) != (rows, heads):
+        raise ValueError(f"weights must be float32 of shape ({rows}, {heads})")
+    _tensor(keys, key_dims, q, "keys")
+    kind = _element_type(q, "q", fp8=True)
+    if keys.dtype != q.dtype or keys.shape[-1] != dim:
+        raise ValueError("keys must have q's type and head dimension")
+    if key_scales is not None:
+        _tensor(key_scales, key_dims - 1, q, "key_scales")
+        if key_scales.dtype != torch.float32 or key_scales.shape != keys.shape[:-1]:
+            raise ValueError("key_scales must be float32, one per key")
+    return kind, int(rows), int(heads), int(dim)
+
+
+def _score_out(out, rows, columns, like):
+    import torch
+
+    if out is None:
+        # a top-k's score buffer: row stride a multiple of 4
+        return torch.empty((rows, max(4, (columns + 3) // 4 * 4)), dtype=torch.float32,
+                           device=like.device)
+    _tensor(out, 2, like, "out")
+    if out.dtype != torch.float32 or out.shape[0] != rows:
+        raise ValueError(f"out must be float32 with {rows} rows")
+    return out
+
+
+def scores_paged(q, weights, keys, seq_lens, page_table, key_scales=None, table_rows=None,
+                 out=None, stream=None):
+    """Indexer scores over a paged key cache, as ``paged`` reads them.
+
+    ``q`` [rows, heads, dim] and ``keys`` [pages, page_size, dim] in
+    bfloat16, float16 or float8_e4m3fn, ``weights`` float32 [rows, heads],
+    ``key_scales`` float32 [pages, page_size] or None. Column j < seq_len of
+    row b of ``out`` gets key_scale[j] * sum_h weights[b, h] * max(0, q[b, h]
+    . key[j]); other columns are not written. Returns ``out`` (allocated with
+    a column per table position when None)."""
+    kind, rows, heads, dim = _score_args(q, weights, keys, key_scales, 3)
+    _vec_i32(seq_lens, rows, "seq_lens", q)
+    _vec_i32(table_rows, rows, "table_rows", q)
+    _table(page_table, q)
+    if table_rows is None and page_table.shape[0] != rows:
+        raise ValueError("page_table must have one row per query row without table_rows")
+    page_size = int(keys.shape[1])
+    out = _score_out(out, rows, page_table.shape[1] * page_size, q)
+    st = _lib().dsatopk_scores_paged(
+        _ptr(q), _stride(q, 0), _stride(q, 1), _ptr(weights), _stride(weights, 0), _ptr(keys),
+        keys.shape[0], _stride(keys, 0), _stride(keys, 1), _ptr(key_scales),
+        0 if key_scales is None else _stride(key_scales, 0), kind, heads, dim, _ptr(seq_lens),
+        _ptr(page_table), _row_stride(page_table), page_table.shape[1], page_size,
+        _ptr(table_rows), rows, _ptr(out), _row_stride(out), out.shape[1], _stream(stream))
+    if st != 0:
+        raise DsatopkError(st, "dsatopk_scores_paged")
+    return out
+
+
+def scores_ragged(q, weights, keys, seq_lens, row_starts, key_scales=None, out=None,
+                  stream=None):
+    """Indexer scores over flattened keys [tokens, dim], as ``ragged`` reads
+    them: row b's window is columns row_starts[b] .. row_starts[b] +
+    seq_lens[b] - 1 of ``out``; other columns are not written. Arguments as
+    for ``scores_paged``, ``key_scales`` float32 [tokens]."""
+    kind, rows, heads, dim = _score_args(q, weights, keys, key_scales, 2)
+    _vec_i32(seq_lens, rows, "seq_lens", q)
+    _vec_i32(row_starts, rows, "row_starts", q)
+    if row_starts is None:
+        raise ValueError("row_starts is required")
+    out = _score_out(out, rows, keys.shape[0], q)
+    st = _lib().dsatopk_scores_ragged(
+        _ptr(q), _stride(q, 0), _stride(q, 1), _ptr(weights), _stride(weights, 0), _ptr(keys),
+        keys.shape[0], _stride(keys, 0), _ptr(key_scales), kind, heads, dim, _ptr(seq_lens),
+        _ptr(row_starts), rows, _ptr(out), _row_stride(out), out.shape[1], _stream(stream))
+    if st != 0:
+        raise DsatopkError(st, "dsatopk_scores_ragged")
     return out

@@ -3,35 +3,49 @@ from __future__ import annotations
 
 import os
 import subprocess
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 from pathlib import Path
 
 PKG = Path(__file__).resolve().parent
 ROOT = PKG.parent
-SOURCES = [PKG / "csrc" / "dsatopk.hip"]
-HEADERS = [PKG / "csrc" / "select_device.h", ROOT / "include" / "dsatopk.h"]
+SOURCES = [PKG / "csrc" / name for name in (
+    "dsatopk.hip", "page_maps.hip", "index_scores.hip")]
+HEADERS = [PKG / "csrc" / "select_device.h", PKG / "csrc" / "serve_common.h",
+           ROOT / "include" / "dsatopk.h"]
 LIB = PKG / "libdsatopk.so"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 # -packed-fp32-ops: keep the compiler from forming packed fp32 instructions.
 FLAGS = [
-    "-O3", "--offload-arch=gfx950", "-std=c++17", "-fPIC", "-shared", "-Wall",
+    "-O3", "--offload-arch=gfx950", "-std=c++17", "-fPIC", "-Wall",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-I", str(ROOT / "include"),
 ]
 
 
-def build(force: bool = True, verbose: bool = False) -> Path:
-    """Compile every HIP source into ``libdsatopk.so`` next to this file."""
-    newest = max(p.stat().st_mtime for p in SOURCES + HEADERS)
-    if not force and LIB.exists() and LIB.stat().st_mtime >= newest:
-        return LIB
-    tmp = LIB.with_suffix(".so.tmp%d" % os.getpid())
-    cmd = [HIPCC, *FLAGS, *map(str, SOURCES), "-o", str(tmp)]
+def _run(cmd, verbose):
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"hipcc failed ({res.returncode}):\n{res.stderr}")
+
+
+def build(force: bool = True, verbose: bool = False) -> Path:
+    """Compile every HIP source into ``libdsatopk.so`` next to this file
+    (the sources side by side, then one link)."""
+    newest = max(p.stat().st_mtime for p in SOURCES + HEADERS)
+    if not force and LIB.exists() and LIB.stat().st_mtime >= newest:
+        return LIB
+    tmp = LIB.with_suffix(".so.tmp%d" % os.getpid())
+    with tempfile.TemporaryDirectory() as d:
+        objects = [Path(d) / (p.stem + ".o") for p in SOURCES]
+        cmds = [[HIPCC, *FLAGS, "-c", str(p), "-o", str(o)] for p, o in zip(SOURCES, objects)]
+        with ThreadPoolExecutor(max_workers=min(8, len(cmds))) as pool:
+            list(pool.map(lambda cmd: _run(cmd, verbose), cmds))
+        _run([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *map(str, objects), "-o",
+              str(tmp)], verbose)
     os.replace(tmp, LIB)
     return LIB
 

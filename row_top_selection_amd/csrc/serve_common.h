@@ -1,0 +1,149 @@
+// serve_common.h - what the serving operators' kernels share: matrix
+// instruction wrappers, asynchronous copies from memory to LDS, LDS swizzle,
+// and the host's argument checks.
+#ifndef DSATOPK_SERVE_COMMON_H_
+#define DSATOPK_SERVE_COMMON_H_
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "dsatopk.h"
+
+namespace dsatopk_serve {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 fp16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 fp16x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 fp16x8 __attribute__((ext_vector_type(8)));
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+using lds_u32 = __attribute__((address_space(3))) uint32_t;
+using lds_i16x4 = __attribute__((address_space(3))) i16x4;
+using global_u32 = const __attribute__((address_space(1))) uint32_t;
+
+constexpr int kWave = 64;
+
+// A 16-bit float type's matrix instructions. In all of them lane l holds
+// row (A) or column (B) l % 32 (l % 16), and along the contraction the
+// lane group l / 32 (l / 16) holds consecutive elements; the result has
+// column l % 32 (l % 16) and rows 8 * (i / 4) + 4 * (l / 32) + i % 4
+// (4 * (l / 16) + i) in its i-th register.
+struct Bf16 {
+  using x4 = bf16x4;
+  using x8 = bf16x8;
+  static __device__ __forceinline__ f32x16 mma32(u32x4 a, u32x4 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ f32x4 mma16(u32x4 a, u32x4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ f32x4 mma16_half(u32x2 a, u32x2 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(i16x4, a),
+                                                     __builtin_bit_cast(i16x4, b), c, 0, 0, 0);
+  }
+  // Two floats, each rounded to nearest even, in one word.
+  static __device__ __forceinline__ uint32_t pack(float x, float y) {
+    bf16x2 v = {(__bf16)x, (__bf16)y};
+    return __builtin_bit_cast(uint32_t, v);
+  }
+};
+
+struct Fp16 {
+  using x4 = fp16x4;
+  using x8 = fp16x8;
+  static __device__ __forceinline__ f32x16 mma32(u32x4 a, u32x4 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(fp16x8, a),
+                                                  __builtin_bit_cast(fp16x8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ f32x4 mma16(u32x4 a, u32x4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(fp16x8, a),
+                                                  __builtin_bit_cast(fp16x8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ f32x4 mma16_half(u32x2 a, u32x2 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x16f16(__builtin_bit_cast(fp16x4, a),
+                                                 __builtin_bit_cast(fp16x4, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ uint32_t pack(float x, float y) {
+    fp16x2 v = {(_Float16)x, (_Float16)y};
+    return __builtin_bit_cast(uint32_t, v);
+  }
+};
+
+// 16 bytes a lane from memory straight into LDS: lane l's bytes go to
+// lds + 16 * l (lds is the wave's, the global address each lane's own).
+// Completion is counted with the vector loads (wait_copies).
+__device__ __forceinline__ void copy_to_lds(const void* global, char* lds) {
+  __builtin_amdgcn_global_load_lds((global_u32*)(uintptr_t)global, (lds_u32*)lds, 16, 0, 0);
+}
+
+// Until every load and copy of this wave has arrived.
+__device__ __forceinline__ void wait_copies() {
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt 0, the other counters unbounded
+}
+
+// Copies of all waves visible to all waves (each waits for its own first).
+__device__ __forceinline__ void copies_barrier() {
+  wait_copies();
+  __syncthreads();
+}
+
+// Four 16-bit elements down a column of an LDS tile: the 16 lanes of a
+// group point at 4 rows x 4 chunks of 8 bytes (lane i: row i / 4, chunk
+// i % 4), and lane i gets column i of those 16, rows 0 .. 3.
+__device__ __forceinline__ u32x2 read_columns(const char* lds) {
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)lds));
+}
+
+// Where row t of an LDS tile keeps its 16-byte chunk c (rows of 16 chunks or
+// a multiple): chunk c ^ swizzle(t). Eight rows after each other have eight
+// different values modulo 8, so lanes that read one chunk of consecutive
+// rows use different banks; rows 4a .. 4a + 3 differ in bits 1 and 2, so
+// a column read's 4 rows x 2 chunks do as well.
+__device__ __forceinline__ constexpr int swizzle(int t) {
+  return ((t & 3) << 1) | ((t >> 2) & 1) | (t & 8);
+}
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// The value of lane ^ 32.
+__device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32); }
+
+// Bytes that stand in for cache entries which a call may not read (no page,
+// past a row's end).
+constexpr int kZeroBytes = 2048;
+static __device__ __align__(256) const uint32_t zero_words[kZeroBytes / 4] = {};
+__device__ __forceinline__ const char* zero_row() {
+  return reinterpret_cast<const char*>(zero_words);
+}
+
+inline bool pow2(int64_t v) { return v >= 1 && (v & (v - 1)) == 0; }
+
+inline int log2_of(int64_t v) {
+  int b = 0;
+  while ((int64_t(1) << b) < v) ++b;
+  return b;
+}
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+template <class P>
+int launch(void (*fn)(P), dim3 grid, dim3 block, P p, void* stream) {
+  void* args[] = {&p};
+  return hipLaunchKernel(reinterpret_cast<const void*>(fn), grid, block, args, 0,
+                         (hipStream_t)stream) == hipSuccess
+             ? DSATOPK_OK
+             : DSATOPK_ERR_HIP;
+}
+
+}  // namespace dsatopk_serve
+
+#endif  // DSATOPK_SERVE_COMMON_H_
