@@ -65,7 +65,9 @@ enum {
     /* the HIP runtime reported an error (no device, launch failure). */
     DSATOPK_ERR_HIP = 4,
     /* dsatopk_paged_noalloc: num_rows above DSATOPK_NOALLOC_MAX_ROWS. */
-    DSATOPK_ERR_TOO_LARGE = 5
+    DSATOPK_ERR_TOO_LARGE = 5,
+    /* workspace missing or smaller than dsatopk_attend_bytes(...). */
+    DSATOPK_ERR_WORKSPACE_TOO_SMALL = 6
 };
 
 /* Largest k (runtime value; one build serves every k). The pages bound the
@@ -386,6 +388,72 @@ int dsatopk_scores_ragged(const void* q, int64_t q_row_stride, int64_t q_head_st
                           int32_t type, int32_t num_heads, int32_t head_dim,
                           const int32_t* seq_lens, const int32_t* row_starts, int32_t num_rows,
                           float* out, int64_t out_stride, int64_t columns, void* stream);
+
+/*
+ * dsatopk_attend_selected, dsatopk_attend_paged - latent attention in its
+ * absorbed form: all heads of a query row read one cached vector per token,
+ *
+ *   s[b, h, j] = scale * sum over latent_dim + rope_dim of q[b, h] * c[j]
+ *   out[b, h]  = sum_j softmax_j(s[b, h, j]) * c[j][0 : latent_dim]
+ *   lse[b, h]  = log(sum_j exp(s[b, h, j]))        (natural logarithm)
+ *
+ * over the tokens j that row b reads:
+ *   selected   the slots of row b of `slots` (page * page_size + offset, as
+ *              dsatopk_paged and dsatopk_paged_packed emit them; in any
+ *              order; slots outside the cache, -1 among them, are skipped);
+ *   paged      positions 0 .. min(seq_lens[b], page_table_width * page_size)
+ *              - 1 of page table row table_rows[b] (row b when NULL); tokens
+ *              of a page outside the cache are skipped.
+ * A row that reads no token gets zeros and lse -inf.
+ *
+ *   q             type [num_rows, num_heads, latent_dim + rope_dim], strides
+ *                 q_row_stride, q_head_stride.
+ *   cache         type [num_pages, page_size, latent_dim + rope_dim], strides
+ *                 page_stride, token_stride; latent part first.
+ *   page_size     power of two in [1, 2^20].
+ *   type          DSATOPK_BF16 or DSATOPK_FP16.
+ *   num_heads     1 .. 1024; latent_dim 256 or 512; rope_dim 64.
+ *   scale         finite and above 0.
+ *   slots         int32 [num_rows, k], rows slot_stride apart.
+ *   max_seq_len   an upper bound on seq_lens. It sets how the tokens are
+ *                 split over workgroups (and the workspace's size); longer
+ *                 rows are read whole all the same.
+ *   out           type [num_rows, num_heads, latent_dim], contiguous.
+ *   lse           float [num_rows, num_heads] or NULL.
+ *   workspace     at least dsatopk_attend_bytes(num_rows, num_heads,
+ *                 latent_dim, k or max_seq_len) bytes, 16-byte aligned
+ *                 (NULL where that is 0). Calls that overlap must not share
+ *                 one.
+ *
+ * Scores, softmax and sums are fp32; the softmax's weights are rounded to
+ * `type` before the second product. The order of the sums is fixed: the
+ * same inputs give the same bits.
+ *
+ * Errors: DSATOPK_ERR_INVALID_ARG, DSATOPK_ERR_ALIGNMENT (q, cache or
+ * workspace not 16-byte aligned, out not 8-byte aligned, a stride of q or
+ * cache no multiple of 8 elements), DSATOPK_ERR_WORKSPACE_TOO_SMALL,
+ * DSATOPK_ERR_HIP. num_rows == 0 is a no-op.
+ */
+size_t dsatopk_attend_bytes(int32_t num_rows, int32_t num_heads, int32_t latent_dim,
+                            int64_t max_tokens);
+
+int dsatopk_attend_selected(const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                            const void* cache, int64_t num_pages, int64_t page_stride,
+                            int64_t token_stride, int32_t page_size, int32_t type,
+                            int32_t num_heads, int32_t latent_dim, int32_t rope_dim, float scale,
+                            const int32_t* slots, int64_t slot_stride, int32_t k,
+                            int32_t num_rows, void* out, float* lse, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+int dsatopk_attend_paged(const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                         const void* cache, int64_t num_pages, int64_t page_stride,
+                         int64_t token_stride, int32_t page_size, int32_t type, int32_t num_heads,
+                         int32_t latent_dim, int32_t rope_dim, float scale,
+                         const int32_t* seq_lens, const int32_t* page_table,
+                         int64_t page_table_stride, int32_t page_table_width,
+                         const int32_t* table_rows, int64_t max_seq_len, int32_t num_rows,
+                         void* out, float* lse, void* workspace, size_t workspace_bytes,
+                         void* stream);
 
 #ifdef __cplusplus
 }

@@ -23,13 +23,15 @@ STATUS = {
     3: "DSATOPK_ERR_PLAN_TOO_SMALL",
     4: "DSATOPK_ERR_HIP",
     5: "DSATOPK_ERR_TOO_LARGE",
+    6: "DSATOPK_ERR_WORKSPACE_TOO_SMALL",
 }
 
 NOALLOC_MAX_ROWS = 262144
 
 EXPORTS = ("dsatopk_status_string", "dsatopk_plan_bytes", "dsatopk_plan", "dsatopk_plan_error",
            "dsatopk_paged", "dsatopk_paged_packed", "dsatopk_ragged", "dsatopk_paged_noalloc",
-           "dsatopk_page_maps", "dsatopk_scores_paged", "dsatopk_scores_ragged")
+           "dsatopk_page_maps", "dsatopk_scores_paged", "dsatopk_scores_ragged",
+           "dsatopk_attend_bytes", "dsatopk_attend_selected", "dsatopk_attend_paged")
 
 
 class DsatopkError(RuntimeError):
@@ -81,6 +83,15 @@ def _lib():
         lib.dsatopk_scores_ragged.argtypes = [P, i64, i64, P, i64, P, i64, i64, P, i32, i32, i32,
                                               P, P, i32, P, i64, i64, P]
         lib.dsatopk_scores_ragged.restype = ctypes.c_int
+        f32 = ctypes.c_float
+        lib.dsatopk_attend_bytes.argtypes = [i32, i32, i32, i64]
+        lib.dsatopk_attend_bytes.restype = sz
+        lib.dsatopk_attend_selected.argtypes = [P, i64, i64, P, i64, i64, i64, i32, i32, i32, i32,
+                                                i32, f32, P, i64, i32, i32, P, P, P, sz, P]
+        lib.dsatopk_attend_selected.restype = ctypes.c_int
+        lib.dsatopk_attend_paged.argtypes = [P, i64, i64, P, i64, i64, i64, i32, i32, i32, i32,
+                                             i32, f32, P, P, i64, i32, P, i64, i32, P, P, P, sz, P]
+        lib.dsatopk_attend_paged.restype = ctypes.c_int
         _handle = lib
     return _handle
 
@@ -462,3 +473,96 @@ def scores_ragged(q, weights, keys, seq_lens, row_starts, key_scales=None, out=N
     if st != 0:
         raise DsatopkError(st, "dsatopk_scores_ragged")
     return out
+
+
+def _attend_args(q, cache, latent_dim, out, lse, workspace, max_tokens):
+    import torch
+
+    _tensor(q, 3, None, "q")
+    _tensor(cache, 3, q, "cache")
+    rows, heads, dim = q.shape
+    kind = _element_type(q, "q")
+    if cache.dtype != q.dtype or cache.shape[-1] != dim:
+        raise ValueError("cache must have q's type and last dimension")
+    shape = (rows, heads, int(latent_dim))
+    if out is None:
+        out = torch.empty(shape, dtype=q.dtype, device=q.device)
+    elif out.dtype != q.dtype or tuple(out.shape) != shape or not out.is_contiguous():
+        raise ValueError(f"out must be a contiguous {q.dtype} tensor of shape {shape}")
+    else:
+        _on(out, q, "out")
+    if lse is None:
+        lse = torch.empty((rows, heads), dtype=torch.float32, device=q.device)
+    elif lse.dtype != torch.float32 or tuple(lse.shape) != (rows, heads) or not lse.is_contiguous():
+        raise ValueError(f"lse must be a contiguous float32 tensor of shape ({rows}, {heads})")
+    else:
+        _on(lse, q, "lse")
+    if workspace is None:
+        need = attend_bytes(rows, heads, latent_dim, max_tokens)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor")
+    else:
+        _on(workspace, q, "workspace")
+    head = (_ptr(q), _stride(q, 0), _stride(q, 1), _ptr(cache), cache.shape[0], _stride(cache, 0),
+            _stride(cache, 1), cache.shape[1], kind, heads, int(latent_dim), dim - int(latent_dim))
+    tail = (_ptr(out), _ptr(lse), _ptr(workspace), 0 if workspace is None else workspace.numel())
+    return out, lse, rows, head, tail
+
+
+def attend_bytes(num_rows: int, num_heads: int, latent_dim: int, max_tokens: int) -> int:
+    """Workspace bytes of ``attend_selected`` (max_tokens: k) and
+    ``attend_paged`` (max_tokens: max_seq_len)."""
+    return int(_lib().dsatopk_attend_bytes(int(num_rows), int(num_heads), int(latent_dim),
+                                           int(max_tokens)))
+
+
+def attend_selected(q, cache, slots, latent_dim: int, scale: float, out=None, lse=None,
+                    workspace=None, stream=None):
+    """Absorbed latent attention over selected cache slots.
+
+    ``q`` [rows, heads, latent_dim + 64] and ``cache`` [pages, page_size,
+    latent_dim + 64] in bfloat16 or float16; ``slots`` int32 [rows, k] as
+    ``paged`` returns them (-1: none). Returns ``(out, lse)``: q's type
+    [rows, heads, latent_dim], and float32 [rows, heads]. ``workspace``: uint8
+    of ``attend_bytes(rows, heads, latent_dim, k)`` (allocated when None)."""
+    import torch
+
+    _tensor(slots, 2, q, "slots")
+    if slots.dtype != torch.int32 or slots.shape[0] != q.shape[0]:
+        raise ValueError("slots must be int32 with one row per query row")
+    k = int(slots.shape[1])
+    out, lse, rows, head, tail = _attend_args(q, cache, latent_dim, out, lse, workspace, k)
+    st = _lib().dsatopk_attend_selected(*head, float(scale), _ptr(slots), _row_stride(slots), k,
+                                        rows, *tail, _stream(stream))
+    if st != 0:
+        raise DsatopkError(st, "dsatopk_attend_selected")
+    return out, lse
+
+
+def attend_paged(q, cache, seq_lens, page_table, latent_dim: int, scale: float, table_rows=None,
+                 max_seq_len=None, out=None, lse=None, workspace=None, stream=None):
+    """Absorbed latent attention over the first ``seq_lens`` positions of each
+    row's page table. Arguments as for ``attend_selected`` and ``paged``;
+    ``max_seq_len`` bounds ``seq_lens`` (the table's width when None) and
+    sets how rows are split."""
+    _tensor(q, 3, None, "q")
+    n = int(q.shape[0])
+    _vec_i32(seq_lens, n, "seq_lens", q)
+    _vec_i32(table_rows, n, "table_rows", q)
+    _table(page_table, q)
+    if table_rows is None and page_table.shape[0] != n:
+        raise ValueError("page_table must have one row per query row without table_rows")
+    _tensor(cache, 3, q, "cache")
+    if max_seq_len is None:
+        max_seq_len = page_table.shape[1] * cache.shape[1]
+    out, lse, rows, head, tail = _attend_args(q, cache, latent_dim, out, lse, workspace,
+                                              int(max_seq_len))
+    st = _lib().dsatopk_attend_paged(*head, float(scale), _ptr(seq_lens), _ptr(page_table),
+                                     _row_stride(page_table), page_table.shape[1],
+                                     _ptr(table_rows), int(max_seq_len), rows, *tail,
+                                     _stream(stream))
+    if st != 0:
+        raise DsatopkError(st, "dsatopk_attend_paged")
+    return out, lse

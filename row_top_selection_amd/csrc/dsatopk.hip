@@ -3365,11 +3365,12 @@ const char* dsatopk_status_string(int status) {
   switch (status) {
     case DSATOPK_OK: return "ok";
     case DSATOPK_ERR_INVALID_ARG: return "invalid argument";
-    case DSATOPK_ERR_ALIGNMENT: return "scores not 16-byte aligned or stride not a multiple of 4";
+    case DSATOPK_ERR_ALIGNMENT: return "a pointer or stride is not aligned as the call needs (scores: 16 bytes, stride a multiple of 4)";
     case DSATOPK_ERR_PLAN_TOO_SMALL: return "plan buffer too small";
     case DSATOPK_ERR_HIP: return "HIP runtime error";
     case DSATOPK_ERR_TOO_LARGE:
       return "num_rows above DSATOPK_NOALLOC_MAX_ROWS (the static scratch of dsatopk_paged_noalloc)";
+    case DSATOPK_ERR_WORKSPACE_TOO_SMALL: return "workspace missing or too small";
     default: return "unknown status";
   }
 }

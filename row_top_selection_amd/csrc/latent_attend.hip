@@ -1,0 +1,669 @@
+// latent_attend.hip - latent attention in its absorbed form
+// (dsatopk_attend_selected and dsatopk_attend_paged in include/dsatopk.h).
+//
+// Every head of query row b attends to the same cached vectors c[j] =
+// (latent, rotary part):
+//
+//   s[h, j] = scale * q[b, h] . c[j],   out[b, h] = sum_j softmax(s[h, :])[j] * latent(c[j])
+//
+// over the tokens j that the row reads: its selected slots, or the first
+// seq_len positions of its page table's row. A cached vector is read once
+// for both products and for all heads of the workgroup.
+//
+// Both products are computed transposed: S' = C Q' has a head in each lane
+// (column) and tokens in its registers (rows), so the softmax's maximum and
+// sum are reductions inside a lane but for one or two lane exchanges, and
+// the rounded weights are, register for register, the B operand of O' =
+// latent' P' (the order of tokens along that contraction is free, and is
+// taken as S' leaves it). O' has a head in each lane too: rescaling it is a
+// multiplication by the lane's own factor, done only where a row's maximum
+// grows by more than 2^8 over the one in use. The A operand of O' needs the
+// tile by columns; the LDS column reads give it from the same tile that the
+// rows were read from.
+//
+// A workgroup of four waves takes one row, up to 128 heads and a range of
+// tokens (split over workgroups when there are few rows; a second kernel
+// joins the parts), 64 tokens a tile, copied to LDS ahead of their use
+// without passing through registers. The waves are WH groups of heads by WT
+// groups of a tile's tokens; token groups keep sums of their own and join
+// them at the end. The vectors of 64 tokens fill 72 KB of LDS: two tiles,
+// one workgroup and one wave per SIMD with up to 512 registers, of which the
+// sums take 256 for 32 heads a wave.
+//
+// Weights are rounded to the inputs' 16-bit type for the second product
+// (off by at most 2^-8 or 2^-11 of each, of either sign); scores, maxima, sums and
+// both products' accumulators are fp32.
+
+#include "serve_common.h"
+
+namespace dsatopk_serve {
+namespace {
+
+constexpr int kBlock = 256;
+constexpr int kTile = 64;  // tokens
+constexpr int kRope = 64;
+constexpr int kRopeBytes = kRope * 2;
+constexpr int kCopyTokens = kTile / 4;  // a wave's share of a tile's copies
+constexpr float kGrow = 8.0f;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct AttendParams {
+  const char* q;
+  int64_t q_row, q_head;  // bytes
+  const char* cache;
+  int64_t page, token;  // bytes
+  int64_t num_pages;
+  const int32_t* slots;  // selected form: [rows, slot_stride], the first `selected` of a row
+  int64_t slot_stride;
+  const int32_t* seq_lens;  // paged form
+  const int32_t* table;
+  int64_t table_stride;
+  const int32_t* table_rows;
+  int32_t table_width, page_bits;
+  int32_t rows, heads, selected, blocks, splits;
+  float scale2;  // scale * log2 e
+  char* out;
+  float* lse;
+  float* part;   // [rows, splits, heads, latent], then [rows, splits, heads, 2]
+  float* state;
+};
+
+template <int kHeads, int kWH, int kWT, int kLatent_>
+struct Plan {
+  static constexpr int kHB = kHeads;  // heads a wave: 16 or 32
+  static constexpr int kLatent = kLatent_;
+  static constexpr int kRow = kLatent * 2;           // bytes of a latent vector
+  static constexpr int kBuffer = kTile * (kRow + kRopeBytes);
+  static constexpr int kTokens = kTile / kWT;        // a wave's of a tile
+  static constexpr int kAcc = kHB * kHB / 64;        // registers of one
+  static constexpr int kSteps = kLatent * kHB / 512; // contraction steps over the latent part
+  static constexpr int kRopeSteps = kRope * kHB / 512;
+  static constexpr int kBlocks = kLatent / kHB;      // output blocks
+  static constexpr int kGroups = 64 / kHB;           // lane groups: 2 or 4
+};
+
+template <int kAcc>
+struct Acc;
+template <>
+struct Acc<16> {
+  using type = f32x16;
+};
+template <>
+struct Acc<4> {
+  using type = f32x4;
+};
+
+template <class T>
+__device__ __forceinline__ f32x16 mma(u32x4 a, u32x4 b, f32x16 c) {
+  return T::mma32(a, b, c);
+}
+template <class T>
+__device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
+  return T::mma16(a, b, c);
+}
+
+// Largest (sum) over the lanes that hold the same head.
+template <int kHB>
+__device__ __forceinline__ float head_max(float x) {
+  if constexpr (kHB == 16) x = fmaxf(x, __shfl_xor(x, 16));
+  return fmaxf(x, __shfl_xor(x, 32));
+}
+template <int kHB>
+__device__ __forceinline__ float head_sum(float x) {
+  if constexpr (kHB == 16) x += __shfl_xor(x, 16);
+  return x + __shfl_xor(x, 32);
+}
+
+// Copies 16 tokens' vectors into a tile's rows 16 * wave ..; `at` is the
+// address of token lane % 16. Chunk c of token t goes to c ^ swizzle(t).
+template <class P>
+__device__ __forceinline__ void copy_tokens(char* tile, uint64_t at, int wave, int lane) {
+  constexpr int kChunks = P::kRow / 16;
+  constexpr int kPer = 64 / kChunks;  // tokens a copy
+  const uint32_t lo = (uint32_t)at, hi = (uint32_t)(at >> 32);
+#pragma unroll
+  for (int t = 0; t < kCopyTokens; t += kPer) {
+    uint64_t base = ((uint64_t)__builtin_amdgcn_readlane(hi, t) << 32) |
+                    (uint32_t)__builtin_amdgcn_readlane(lo, t);
+    int chunk = lane ^ swizzle(t);
+    if constexpr (kPer == 2) {
+      const uint64_t second = ((uint64_t)__builtin_amdgcn_readlane(hi, t + 1) << 32) |
+                              (uint32_t)__builtin_amdgcn_readlane(lo, t + 1);
+      if (lane >= 32) base = second;
+      chunk = (lane & 31) ^ (lane >= 32 ? swizzle(t + 1) : swizzle(t));
+    }
+    copy_to_lds(reinterpret_cast<const char*>(base) + chunk * 16,
+                tile + (wave * kCopyTokens + t) * P::kRow);
+  }
+#pragma unroll
+  for (int t = 0; t < kCopyTokens; t += 8) {
+    const int mine = t + (lane >> 3);
+    const uint64_t base = ((uint64_t)(uint32_t)__shfl((int)hi, mine) << 32) |
+                          (uint32_t)__shfl((int)lo, mine);
+    const int chunk = (lane & 7) ^ (swizzle(mine) & 7);
+    copy_to_lds(reinterpret_cast<const char*>(base) + P::kRow + chunk * 16,
+                tile + kTile * P::kRow + (wave * kCopyTokens + t) * kRopeBytes);
+  }
+}
+
+// A wave's running state.
+template <class P>
+struct State {
+  typename Acc<P::kAcc>::type o[P::kBlocks];
+  float top, sum;  // the reference maximum (log2), this lane's part of the sum
+};
+
+// Scores, weights and sums of kGo consecutive products' tokens (kGo * kHB of
+// them) from tile row `from` on, and first the next tile's copies if `more`:
+// the two buffers are told apart so that no read of one waits for the
+// other's copies. `valid`: a bit for each token. Returns false, with `st`
+// untouched and the scores' maximum in `top`, if that is too far above the
+// reference in use.
+template <class T, class P, int kGo>
+__device__ __forceinline__ bool attend_tokens(State<P>& st, const u32x4 (&q)[P::kSteps + P::kRopeSteps],
+                                              const char* __restrict__ cur, char* __restrict__ next,
+                                              bool more, uint64_t next_at, int wave, int from,
+                                              uint64_t valid, int lane, float scale2, float& top) {
+  constexpr int kHB = P::kHB;
+  if (more) copy_tokens<P>(next, next_at, wave, lane);
+  using acc_t = typename Acc<P::kAcc>::type;
+  const int col = lane % kHB, group = lane / kHB;
+  acc_t s[kGo];
+  {
+    const int swz = swizzle(col);  // rows `from` on: `from` is a multiple of 16
+    constexpr int kPer = 16 / P::kGroups;  // steps whose chunks share their upper bits
+    const char* row = cur + (from + col) * P::kRow;
+    const char* rope = cur + kTile * P::kRow + (from + col) * kRopeBytes;
+#pragma unroll
+    for (int x = 0; x < kGo; ++x) s[x] = acc_t{};
+    // Reads go kAhead steps before the products that take them, and no
+    // further: registers are what a wave of 32 heads has least of.
+    constexpr int kAhead = 4, kAll = P::kSteps + P::kRopeSteps;
+    auto read = [&](int i, int x) {
+      if (i < P::kSteps)
+        return *reinterpret_cast<const u32x4*>(
+            row + (((P::kGroups * (i % kPer) + group) ^ swz) << 4) + (i / kPer) * 256 + x * kHB * P::kRow);
+      return *reinterpret_cast<const u32x4*>(
+          rope + (((P::kGroups * (i - P::kSteps) + group) ^ (swz & 7)) << 4) + x * kHB * kRopeBytes);
+    };
+    u32x4 a[kAhead][kGo];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+      for (int x = 0; x < kGo; ++x) a[i][x] = read(i, x);
+#pragma unroll
+    for (int i = 0; i < kAll; ++i) {
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int x = 0; x < kGo; ++x) {
+        s[x] = mma<T>(a[i % kAhead][x], q[i], s[x]);
+        if (i + kAhead < kAll) a[i % kAhead][x] = read(i + kAhead, x);
+      }
+    }
+  }
+  // register i of a product holds its token 8 * (i / 4) + 4 * group + i % 4
+  constexpr uint32_t kAll = kGo * kHB == 32 ? ~0u : (1u << (kGo * kHB)) - 1;
+  if ((uint32_t)valid != kAll) {
+    const uint32_t mine = (uint32_t)valid >> (4 * group);
+#pragma unroll
+    for (int x = 0; x < kGo; ++x)
+#pragma unroll
+      for (int i = 0; i < P::kAcc; ++i)
+        if (!((mine >> (x * kHB + 8 * (i / 4) + i % 4)) & 1)) s[x][i] = -INFINITY;
+  }
+  top = s[0][0];
+#pragma unroll
+  for (int x = 0; x < kGo; ++x)
+#pragma unroll
+    for (int i = 0; i < P::kAcc; ++i) top = fmaxf(top, s[x][i]);
+  top = head_max<kHB>(top) * scale2;
+  if (__any(top > st.top + kGrow)) return false;
+  const float ref = st.top == -INFINITY ? 0.0f : st.top;
+#pragma unroll
+  for (int x = 0; x < kGo; ++x)
+#pragma unroll
+    for (int i = 0; i < P::kAcc; ++i) {
+      s[x][i] = exp2_fast(fmaf(s[x][i], scale2, -ref));
+      st.sum += s[x][i];
+    }
+
+  // sums: lane i of 16 points at row i / 4, 8 bytes i % 4 of a 4 x 32 byte block
+  const int in = lane & 15;
+  if constexpr (kHB == 32) {
+    const int half = lane >> 5, side = (lane >> 4) & 1;
+    const int tok = 4 * half + (in >> 2);
+    const int swz = swizzle(tok);
+    int at[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      at[j] = (from + tok) * P::kRow + (((4 * j + 2 * side + ((in & 3) >> 1)) ^ swz) << 4) + 8 * (in & 1);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const u32x4 w = {T::pack(s[0][8 * k], s[0][8 * k + 1]), T::pack(s[0][8 * k + 2], s[0][8 * k + 3]),
+                       T::pack(s[0][8 * k + 4], s[0][8 * k + 5]), T::pack(s[0][8 * k + 6], s[0][8 * k + 7])};
+      const char* rows = cur + 16 * k * P::kRow;
+      auto read = [&](int b) {
+        const u32x2 lo = read_columns(rows + at[b & 3] + (b >> 2) * 256);
+        const u32x2 hi = read_columns(rows + at[(b & 3) ^ 2] + (b >> 2) * 256 + 8 * P::kRow);
+        return u32x4{lo[0], lo[1], hi[0], hi[1]};
+      };
+      constexpr int kAhead = 4;
+      u32x4 a[kAhead];
+#pragma unroll
+      for (int b = 0; b < kAhead; ++b) a[b] = read(b);
+#pragma unroll
+      for (int b = 0; b < P::kBlocks; ++b) {
+        __builtin_amdgcn_sched_barrier(0);
+        st.o[b] = mma<T>(a[b % kAhead], w, st.o[b]);
+        if (b + kAhead < P::kBlocks) a[b % kAhead] = read(b + kAhead);
+      }
+    }
+  } else {
+    const int tok = 4 * group + (in >> 2);
+    const int swz = swizzle(tok);
+    int at[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      at[j] = (from + tok) * P::kRow + (((2 * j + ((in & 3) >> 1)) ^ swz) << 4) + 8 * (in & 1);
+    if constexpr (kGo == 1) {
+      const u32x2 w = {T::pack(s[0][0], s[0][1]), T::pack(s[0][2], s[0][3])};
+#pragma unroll
+      for (int b = 0; b < P::kBlocks; ++b)
+        st.o[b] = T::mma16_half(read_columns(cur + at[b & 7] + (b >> 3) * 256), w, st.o[b]);
+    } else {
+      const u32x4 w = {T::pack(s[0][0], s[0][1]), T::pack(s[0][2], s[0][3]),
+                       T::pack(s[1][0], s[1][1]), T::pack(s[1][2], s[1][3])};
+#pragma unroll
+      for (int b = 0; b < P::kBlocks; ++b) {
+        const u32x2 lo = read_columns(cur + at[b & 7] + (b >> 3) * 256);
+        const u32x2 hi = read_columns(cur + at[b & 7] + (b >> 3) * 256 + 16 * P::kRow);
+        st.o[b] = mma<T>(u32x4{lo[0], lo[1], hi[0], hi[1]}, w, st.o[b]);
+      }
+    }
+  }
+  return true;
+}
+
+template <class T, int kHeads, int kWH, int kWT, int kLatent, bool kPaged>
+__global__ __launch_bounds__(kBlock, 1) void attend_kernel(AttendParams p) {
+  using P = Plan<kHeads, kWH, kWT, kLatent>;
+  constexpr int kHB = P::kHB;
+  __shared__ __attribute__((aligned(1024))) char tiles[2 * P::kBuffer];
+  __shared__ uint32_t masks[2][4];
+  __shared__ float joined[2][4][kHB];
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wh = wave % kWH, wt = wave / kWH;
+  const uint32_t id = blockIdx.x;
+  const int split = id % p.splits;
+  const int block = (id / p.splits) % p.blocks;
+  const int64_t row = id / p.splits / p.blocks;
+
+  // the tokens of this workgroup
+  int32_t len = p.selected;
+  const int32_t* list;
+  if constexpr (kPaged) {
+    const int64_t most = (int64_t)p.table_width << p.page_bits;
+    len = (int32_t)min((int64_t)max(p.seq_lens[row], 0), most);
+    list = p.table + (p.table_rows ? p.table_rows[row] : row) * p.table_stride;
+  } else {
+    list = p.slots + row * p.slot_stride;
+  }
+  const int32_t tiles_all = (len + kTile - 1) / kTile;
+  const int32_t per = (tiles_all + p.splits - 1) / p.splits;
+  const int32_t first = split * per;
+  const int32_t last = min(first + per, tiles_all);
+
+  // The entry (slot or page) of token lane % 16 of this wave's share of a tile, -1: none.
+  auto entry_of = [&](int32_t tile) {
+    const int32_t j = tile * kTile + wave * kCopyTokens + (lane & 15);
+    if (tile >= last || j >= len) return -1;
+    return list[kPaged ? j >> p.page_bits : j];
+  };
+  // Its address, or that of zeros.
+  auto address_of = [&](int32_t tile, int32_t entry, bool& there) {
+    int64_t page = entry;
+    int32_t in = tile * kTile + wave * kCopyTokens + (lane & 15);
+    if constexpr (!kPaged) {
+      page = entry >> p.page_bits;
+      in = entry;
+    }
+    in &= (1 << p.page_bits) - 1;
+    there = entry >= 0 && page < p.num_pages;
+    const char* at = there ? p.cache + page * p.page + in * p.token : zero_row();
+    return (uint64_t)(uintptr_t)at;
+  };
+
+  State<P> st;
+  st.top = -INFINITY;
+  st.sum = 0.0f;
+#pragma unroll
+  for (int b = 0; b < P::kBlocks; ++b) {
+    st.o[b] = typename Acc<P::kAcc>::type{};
+  }
+
+  const int col = lane % kHB, group = lane / kHB;
+  const int head = (block * kWH + wh) * kHB + col;
+  if (first < last) {
+    int32_t entry = entry_of(first);
+    bool there;
+    uint64_t at = address_of(first, entry, there);
+    uint32_t mask = (uint32_t)__ballot(there) & 0xffff;
+    if (kWT < 4 && lane == 0) masks[0][wave] = mask;
+    copy_tokens<P>(tiles, at, wave, lane);
+    entry = entry_of(first + 1);
+
+    u32x4 q[P::kSteps + P::kRopeSteps];
+    const char* qh = head < p.heads ? p.q + row * p.q_row + head * p.q_head : zero_row();
+#pragma unroll
+    for (int i = 0; i < P::kSteps + P::kRopeSteps; ++i)
+      q[i] = *reinterpret_cast<const u32x4*>(qh + (P::kGroups * i + group) * 16);
+
+    // A pass of the inner loop takes the wave's next kGo * kHB tokens. It has
+    // only products touch the sums, which thereby stay where those keep
+    // them; when a maximum outgrows the reference the loop is left, the sums
+    // are rescaled, and the tokens are taken again.
+    constexpr int kGo = P::kTokens == 16 ? 1 : 32 / kHB;
+    int32_t t = first;
+    int from = P::kTokens;  // past the wave's tokens of the tile before
+    int buf = 1;
+    uint64_t valid = 0;
+    bool more = false;
+    --t;
+    for (;;) {
+      float high = 0.0f;
+      bool done = false;
+      for (;;) {
+        if (from == P::kTokens) {
+          if (++t == last) {
+            done = true;
+            break;
+          }
+          from = 0;
+          buf ^= 1;
+          if constexpr (kWT == 4) {
+            wait_copies();  // a wave copies and reads the same tokens
+            valid = mask;
+          } else {
+            copies_barrier();
+            const uint32_t lo = masks[buf][0] | masks[buf][1] << 16;
+            const uint32_t hi = masks[buf][2] | masks[buf][3] << 16;
+            const uint32_t a = __builtin_amdgcn_readfirstlane(kWT == 2 && wt ? hi : lo);
+            valid = a;
+            if constexpr (kWT == 1) valid |= (uint64_t)__builtin_amdgcn_readfirstlane(hi) << 32;
+          }
+          more = t + 1 < last;
+          if (more) {
+            at = address_of(t + 1, entry, there);
+            mask = (uint32_t)__ballot(there) & 0xffff;
+            if (kWT < 4 && lane == 0) masks[buf ^ 1][wave] = mask;
+            entry = entry_of(t + 2);
+          }
+        }
+        if (!attend_tokens<T, P, kGo>(st, q, tiles + buf * P::kBuffer, tiles + (buf ^ 1) * P::kBuffer,
+                                      more, at, wave, wt * P::kTokens + from, valid >> from, lane,
+                                      p.scale2, high))
+          break;
+        more = false;
+        from += kGo * kHB;
+      }
+      if (done) break;
+      more = false;
+      const float to = fmaxf(st.top, high);
+      const float by = st.top == -INFINITY ? 0.0f : exp2_fast(st.top - to);
+      st.top = to;
+      st.sum *= by;
+#pragma unroll
+      for (int b = 0; b < P::kBlocks; ++b) {
+        st.o[b] *= by;
+      }
+    }
+  }
+  float sum = head_sum<kHB>(st.sum);
+  float top = st.top;
+  if constexpr (kWT > 1) {
+    // join the token groups: each wave's sums to the common maximum, then into group 0
+    constexpr int kRegs = P::kBlocks * P::kAcc;
+    if (lane < kHB) {
+      joined[0][wave][lane] = top;
+      joined[1][wave][lane] = sum;
+    }
+    __syncthreads();
+    float all = -INFINITY, total = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWT; ++w) all = fmaxf(all, joined[0][w * kWH + wh][col]);
+#pragma unroll
+    for (int w = 0; w < kWT; ++w) {
+      const float x = joined[0][w * kWH + wh][col];
+      total += joined[1][w * kWH + wh][col] * (x == -INFINITY ? 0.0f : exp2_fast(x - all));
+    }
+    const float by = top == -INFINITY ? 0.0f : exp2_fast(top - all);
+#pragma unroll
+    for (int b = 0; b < P::kBlocks; ++b) st.o[b] *= by;
+    float* give = reinterpret_cast<float*>(tiles);
+    if (wt > 0) {
+      float* to = give + (size_t)(wave - kWH) * kRegs * 64 + lane;
+#pragma unroll
+      for (int b = 0; b < P::kBlocks; ++b)
+#pragma unroll
+        for (int i = 0; i < P::kAcc; ++i) to[(b * P::kAcc + i) * 64] = st.o[b][i];
+    }
+    __syncthreads();
+    if (wt > 0) return;
+#pragma unroll
+    for (int w = 1; w < kWT; ++w) {
+      const float* from = give + (size_t)(w * kWH + wh - kWH) * kRegs * 64 + lane;
+#pragma unroll
+      for (int b = 0; b < P::kBlocks; ++b)
+#pragma unroll
+        for (int i = 0; i < P::kAcc; ++i) st.o[b][i] += from[(b * P::kAcc + i) * 64];
+    }
+    top = all;
+    sum = total;
+  }
+  if (head >= p.heads) return;
+
+  // register i of block b: element b * kHB + 8 * (i / 4) + 4 * group + i % 4 of the head's vector
+  if (p.splits == 1) {
+    const float by = sum == 0.0f ? 0.0f : 1.0f / sum;
+    char* to = p.out + ((row * p.heads + head) * kLatent + 4 * group) * 2;
+#pragma unroll
+    for (int b = 0; b < P::kBlocks; ++b)
+#pragma unroll
+      for (int i = 0; i < P::kAcc; i += 4)
+        *reinterpret_cast<u32x2*>(to + (b * kHB + 2 * i) * 2) =
+            u32x2{T::pack(st.o[b][i] * by, st.o[b][i + 1] * by),
+                  T::pack(st.o[b][i + 2] * by, st.o[b][i + 3] * by)};
+    if (p.lse && group == 0) p.lse[row * p.heads + head] = (top + log2f(sum)) * kLn2;
+  } else {
+    const int64_t at = (row * p.splits + split) * p.heads + head;
+    if (group == 0) {
+      p.state[at * 2] = top;
+      p.state[at * 2 + 1] = sum;
+    }
+    if (top == -INFINITY && sum == 0.0f) return;  // nothing seen: the join skips it
+    float* to = p.part + at * kLatent + 4 * group;
+#pragma unroll
+    for (int b = 0; b < P::kBlocks; ++b)
+#pragma unroll
+      for (int i = 0; i < P::kAcc; i += 4)
+        *reinterpret_cast<f32x4*>(to + b * kHB + 2 * i) =
+            f32x4{st.o[b][i], st.o[b][i + 1], st.o[b][i + 2], st.o[b][i + 3]};
+  }
+}
+
+// Joins the splits of one row's head: a thread has 4 elements.
+template <class T, int kLatent>
+__global__ __launch_bounds__(kLatent / 4) void join_kernel(AttendParams p) {
+  const int64_t row = blockIdx.x / p.heads;
+  const int head = blockIdx.x % p.heads;
+  const int64_t base = row * p.splits * p.heads + head;
+  float top = -INFINITY;
+  for (int s = 0; s < p.splits; ++s) top = fmaxf(top, p.state[(base + (int64_t)s * p.heads) * 2]);
+  const float ref = top == -INFINITY ? 0.0f : top;
+  f32x4 o = {};
+  float sum = 0.0f;
+  for (int s = 0; s < p.splits; ++s) {
+    const int64_t at = base + (int64_t)s * p.heads;
+    const float x = p.state[at * 2], n = p.state[at * 2 + 1];
+    if (x == -INFINITY && n == 0.0f) continue;
+    const float by = exp2_fast(x - ref);
+    sum += n * by;
+    o += *reinterpret_cast<const f32x4*>(p.part + at * kLatent + threadIdx.x * 4) * by;
+  }
+  const float by = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const int64_t at = row * p.heads + head;
+  *reinterpret_cast<u32x2*>(p.out + (at * kLatent + threadIdx.x * 4) * 2) =
+      u32x2{T::pack(o[0] * by, o[1] * by), T::pack(o[2] * by, o[3] * by)};
+  if (p.lse && threadIdx.x == 0) p.lse[at] = (top + log2f(sum)) * kLn2;
+}
+
+// Heads a workgroup: 16, 32 or 64.
+int head_block(int32_t heads) { return heads <= 16 ? 16 : heads <= 32 ? 32 : 64; }
+
+// Workgroups that the chip runs at once (one per CU).
+constexpr int64_t kSlots = 256;
+
+// Parts of the token axis: enough workgroups for every CU, each with a
+// tile at least.
+int32_t splits_for(int32_t rows, int32_t heads, int64_t tokens) {
+  const int64_t hb = head_block(heads);
+  const int64_t groups = (int64_t)rows * ((heads + hb - 1) / hb);
+  const int64_t tiles = (tokens + kTile - 1) / kTile;
+  int64_t s = groups > 0 ? kSlots / groups : 1;
+  if (s > tiles) s = tiles;
+  return (int32_t)(s < 1 ? 1 : s);
+}
+
+template <class T, int kLatent, bool kPaged>
+int launch_attend(AttendParams p, void* stream) {
+  const int hb = head_block(p.heads);
+  p.blocks = (p.heads + hb - 1) / hb;
+  const dim3 grid((unsigned)((int64_t)p.rows * p.blocks * p.splits));
+  int st;
+  if (hb == 16)
+    st = launch(attend_kernel<T, 16, 1, 4, kLatent, kPaged>, grid, dim3(kBlock), p, stream);
+  else if (hb == 32)
+    st = launch(attend_kernel<T, 16, 2, 2, kLatent, kPaged>, grid, dim3(kBlock), p, stream);
+  else
+    st = launch(attend_kernel<T, 16, 4, 1, kLatent, kPaged>, grid, dim3(kBlock), p, stream);
+  if (st != DSATOPK_OK || p.splits == 1) return st;
+  return launch(join_kernel<T, kLatent>, dim3((unsigned)((int64_t)p.rows * p.heads)),
+                dim3(kLatent / 4), p, stream);
+}
+
+size_t part_floats(int32_t rows, int32_t heads, int32_t latent, int32_t splits) {
+  return splits <= 1 ? 0 : (size_t)rows * splits * heads * (latent + 2);
+}
+
+// Checks and fills what both forms share; `tokens` bounds a row's tokens.
+int check_attend(AttendParams& p, const void* q, int64_t q_row, int64_t q_head, const void* cache,
+                 int64_t num_pages, int64_t page_stride, int64_t token_stride, int32_t page_size,
+                 int32_t type, int32_t heads, int32_t latent, int32_t rope, float scale,
+                 int32_t rows, int64_t tokens, void* out, float* lse, void* workspace,
+                 size_t workspace_bytes) {
+  if (rows < 0 || heads < 1 || heads > 1024 || (latent != 256 && latent != 512) || rope != kRope ||
+      (type != DSATOPK_BF16 && type != DSATOPK_FP16) || !(scale > 0.0f) || !(scale < INFINITY) ||
+      num_pages < 0 || page_stride < 0 || token_stride < 0 || !pow2(page_size) ||
+      page_size > (1 << 20) || q_row < 0 || q_head < 0 || tokens < 0 || tokens > INT32_MAX - kTile)
+    return DSATOPK_ERR_INVALID_ARG;
+  if (rows == 0) return DSATOPK_OK;
+  if (!q || !out || (num_pages && !cache)) return DSATOPK_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(cache) || (reinterpret_cast<uintptr_t>(out) & 7u) ||
+      !aligned4(lse) || q_row % 8 || q_head % 8 || page_stride % 8 || token_stride % 8)
+    return DSATOPK_ERR_ALIGNMENT;
+  p.splits = splits_for(rows, heads, tokens);
+  if (p.splits > 1) {
+    if (!workspace || workspace_bytes < part_floats(rows, heads, latent, p.splits) * sizeof(float))
+      return DSATOPK_ERR_WORKSPACE_TOO_SMALL;
+    if (!aligned16(workspace)) return DSATOPK_ERR_ALIGNMENT;
+    p.part = static_cast<float*>(workspace);
+    p.state = p.part + (size_t)rows * p.splits * heads * latent;
+  }
+  p.q = static_cast<const char*>(q);
+  p.q_row = q_row * 2;
+  p.q_head = q_head * 2;
+  p.cache = static_cast<const char*>(cache);
+  p.page = page_stride * 2;
+  p.token = token_stride * 2;
+  p.num_pages = num_pages;
+  p.page_bits = log2_of(page_size);
+  p.rows = rows;
+  p.heads = heads;
+  p.scale2 = scale * kLog2e;
+  p.out = static_cast<char*>(out);
+  p.lse = lse;
+  return DSATOPK_OK;
+}
+
+template <bool kPaged>
+int run_attend(const AttendParams& p, int32_t type, int32_t latent, void* stream) {
+  if (type == DSATOPK_BF16)
+    return latent == 256 ? launch_attend<Bf16, 256, kPaged>(p, stream)
+                         : launch_attend<Bf16, 512, kPaged>(p, stream);
+  return latent == 256 ? launch_attend<Fp16, 256, kPaged>(p, stream)
+                       : launch_attend<Fp16, 512, kPaged>(p, stream);
+}
+
+}  // namespace
+}  // namespace dsatopk_serve
+
+using namespace dsatopk_serve;
+
+extern "C" {
+
+size_t dsatopk_attend_bytes(int32_t num_rows, int32_t num_heads, int32_t latent_dim,
+                            int64_t max_tokens) {
+  if (num_rows < 1 || num_heads < 1 || latent_dim < 1 || max_tokens < 0) return 0;
+  return part_floats(num_rows, num_heads, latent_dim,
+                     splits_for(num_rows, num_heads, max_tokens)) * sizeof(float);
+}
+
+int dsatopk_attend_selected(const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                            const void* cache, int64_t num_pages, int64_t page_stride,
+                            int64_t token_stride, int32_t page_size, int32_t type,
+                            int32_t num_heads, int32_t latent_dim, int32_t rope_dim, float scale,
+                            const int32_t* slots, int64_t slot_stride, int32_t k,
+                            int32_t num_rows, void* out, float* lse, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  AttendParams p{};
+  if (k < 0 || slot_stride < k) return DSATOPK_ERR_INVALID_ARG;
+  const int st = check_attend(p, q, q_row_stride, q_head_stride, cache, num_pages, page_stride,
+                              token_stride, page_size, type, num_heads, latent_dim, rope_dim,
+                              scale, num_rows, k, out, lse, workspace, workspace_bytes);
+  if (st != DSATOPK_OK || num_rows == 0) return st;
+  if (k && !slots) return DSATOPK_ERR_INVALID_ARG;
+  p.slots = slots;
+  p.slot_stride = slot_stride;
+  p.selected = k;
+  return run_attend<false>(p, type, latent_dim, stream);
+}
+
+int dsatopk_attend_paged(const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                         const void* cache, int64_t num_pages, int64_t page_stride,
+                         int64_t token_stride, int32_t page_size, int32_t type, int32_t num_heads,
+                         int32_t latent_dim, int32_t rope_dim, float scale,
+                         const int32_t* seq_lens, const int32_t* page_table,
+                         int64_t page_table_stride, int32_t page_table_width,
+                         const int32_t* table_rows, int64_t max_seq_len, int32_t num_rows,
+                         void* out, float* lse, void* workspace, size_t workspace_bytes,
+                         void* stream) {
+  AttendParams p{};
+  if (page_table_width < 1 || page_table_stride < page_table_width)
+    return DSATOPK_ERR_INVALID_ARG;
+  const int st = check_attend(p, q, q_row_stride, q_head_stride, cache, num_pages, page_stride,
+                              token_stride, page_size, type, num_heads, latent_dim, rope_dim,
+                              scale, num_rows, max_seq_len, out, lse, workspace, workspace_bytes);
+  if (st != DSATOPK_OK || num_rows == 0) return st;
+  if (!seq_lens || !page_table) return DSATOPK_ERR_INVALID_ARG;
+  p.seq_lens = seq_lens;
+  p.table = page_table;
+  p.table_stride = page_table_stride;
+  p.table_rows = table_rows;
+  p.table_width = page_table_width;
+  return run_attend<true>(p, type, latent_dim, stream);
+}
+
+}  // extern "C"

@@ -87,6 +87,7 @@ __device__ __forceinline__ void copy_to_lds(const void* global, char* lds) {
 // Until every load and copy of this wave has arrived.
 __device__ __forceinline__ void wait_copies() {
   __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt 0, the other counters unbounded
+  asm volatile("" ::: "memory");       // LDS reads stay behind it
 }
 
 // Copies of all waves visible to all waves (each waits for its own first).
