@@ -455,6 +455,56 @@ int dsatopk_attend_paged(const void* q, int64_t q_row_stride, int64_t q_head_str
                          void* out, float* lse, void* workspace, size_t workspace_bytes,
                          void* stream);
 
+/*
+ * dsatopk_attend_expanded - latent attention in its expanded form, for
+ * prompts: keys and values of each head (the latent vectors' projections),
+ * one rotary key for all heads,
+ *
+ *   s[i, h, j] = scale * (q[i, h][0 : nope_dim] . k[j, h] + q[i, h][nope_dim :] . k_rope[j])
+ *   out[i, h]  = sum_j softmax_j(s[i, h, j]) * v[j, h]
+ *   lse[i, h]  = log(sum_j exp(s[i, h, j]))
+ *
+ * over a ragged batch: request r has the queries q_starts[r] .. q_starts[r +
+ * 1] - 1 and the keys k_starts[r] .. k_starts[r + 1] - 1. With `causal`,
+ * query i of a request's n sees its first (keys - n + i + 1) keys: the
+ * queries are the request's last tokens. A query that sees no key gets zeros
+ * and lse -inf.
+ *
+ *   q             type [num_queries, num_heads, nope_dim + rope_dim]
+ *   k             type [num_keys, num_heads, nope_dim]
+ *   v             type [num_keys, num_heads, value_dim]
+ *   k_rope        type [num_keys, rope_dim]
+ *                 (each with its row and head strides; k and v may be parts
+ *                 of one tensor)
+ *   type          DSATOPK_BF16 or DSATOPK_FP16.
+ *   num_heads     1 .. 1024; nope_dim 128, rope_dim 64, value_dim 128.
+ *   scale         finite and above 0.
+ *   q_starts, k_starts  int32 [num_requests + 1], rising; parts past
+ *                 num_queries and num_keys are cut off.
+ *   max_queries   an upper bound on a request's queries (rows past it are
+ *                 not computed).
+ *   out           type [num_queries, num_heads, value_dim], contiguous. Rows
+ *                 of no request are not written.
+ *   lse           float [num_queries, num_heads] or NULL.
+ *
+ * Values must be finite, also those of keys that causality hides from some
+ * queries (their weight is 0, which infinities and NaN turn into NaN). Hidden
+ * keys may hold anything. Rounding as for dsatopk_attend_selected.
+ *
+ * Errors: DSATOPK_ERR_INVALID_ARG, DSATOPK_ERR_ALIGNMENT (an input not
+ * 16-byte aligned or a stride no multiple of 8 elements; out not 8-byte
+ * aligned), DSATOPK_ERR_HIP. No queries: a no-op.
+ */
+int dsatopk_attend_expanded(const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                            const void* k, int64_t k_row_stride, int64_t k_head_stride,
+                            const void* v, int64_t v_row_stride, int64_t v_head_stride,
+                            const void* k_rope, int64_t rope_row_stride, int32_t type,
+                            int32_t num_heads, int32_t nope_dim, int32_t rope_dim,
+                            int32_t value_dim, float scale, int32_t causal,
+                            const int32_t* q_starts, const int32_t* k_starts,
+                            int32_t num_requests, int32_t num_queries, int32_t num_keys,
+                            int32_t max_queries, void* out, float* lse, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -31,7 +31,8 @@ NOALLOC_MAX_ROWS = 262144
 EXPORTS = ("dsatopk_status_string", "dsatopk_plan_bytes", "dsatopk_plan", "dsatopk_plan_error",
            "dsatopk_paged", "dsatopk_paged_packed", "dsatopk_ragged", "dsatopk_paged_noalloc",
            "dsatopk_page_maps", "dsatopk_scores_paged", "dsatopk_scores_ragged",
-           "dsatopk_attend_bytes", "dsatopk_attend_selected", "dsatopk_attend_paged")
+           "dsatopk_attend_bytes", "dsatopk_attend_selected", "dsatopk_attend_paged",
+           "dsatopk_attend_expanded")
 
 
 class DsatopkError(RuntimeError):
@@ -92,6 +93,10 @@ def _lib():
         lib.dsatopk_attend_paged.argtypes = [P, i64, i64, P, i64, i64, i64, i32, i32, i32, i32,
                                              i32, f32, P, P, i64, i32, P, i64, i32, P, P, P, sz, P]
         lib.dsatopk_attend_paged.restype = ctypes.c_int
+        lib.dsatopk_attend_expanded.argtypes = [P, i64, i64, P, i64, i64, P, i64, i64, P, i64, i32,
+                                                i32, i32, i32, i32, f32, i32, P, P, i32, i32, i32,
+                                                i32, P, P, P]
+        lib.dsatopk_attend_expanded.restype = ctypes.c_int
         _handle = lib
     return _handle
 
@@ -475,6 +480,25 @@ def scores_ragged(q, weights, keys, seq_lens, row_starts, key_scales=None, out=N
     return out
 
 
+def _attend_out(out, lse, q, shape):
+    """Attention's results: out (q's type) of ``shape``, lse (float32) of its first two."""
+    import torch
+
+    if out is None:
+        out = torch.empty(shape, dtype=q.dtype, device=q.device)
+    elif out.dtype != q.dtype or tuple(out.shape) != shape or not out.is_contiguous():
+        raise ValueError(f"out must be a contiguous {q.dtype} tensor of shape {shape}")
+    else:
+        _on(out, q, "out")
+    if lse is None:
+        lse = torch.empty(shape[:2], dtype=torch.float32, device=q.device)
+    elif lse.dtype != torch.float32 or tuple(lse.shape) != shape[:2] or not lse.is_contiguous():
+        raise ValueError(f"lse must be a contiguous float32 tensor of shape {shape[:2]}")
+    else:
+        _on(lse, q, "lse")
+    return out, lse
+
+
 def _attend_args(q, cache, latent_dim, out, lse, workspace, max_tokens):
     import torch
 
@@ -484,19 +508,7 @@ def _attend_args(q, cache, latent_dim, out, lse, workspace, max_tokens):
     kind = _element_type(q, "q")
     if cache.dtype != q.dtype or cache.shape[-1] != dim:
         raise ValueError("cache must have q's type and last dimension")
-    shape = (rows, heads, int(latent_dim))
-    if out is None:
-        out = torch.empty(shape, dtype=q.dtype, device=q.device)
-    elif out.dtype != q.dtype or tuple(out.shape) != shape or not out.is_contiguous():
-        raise ValueError(f"out must be a contiguous {q.dtype} tensor of shape {shape}")
-    else:
-        _on(out, q, "out")
-    if lse is None:
-        lse = torch.empty((rows, heads), dtype=torch.float32, device=q.device)
-    elif lse.dtype != torch.float32 or tuple(lse.shape) != (rows, heads) or not lse.is_contiguous():
-        raise ValueError(f"lse must be a contiguous float32 tensor of shape ({rows}, {heads})")
-    else:
-        _on(lse, q, "lse")
+    out, lse = _attend_out(out, lse, q, (rows, heads, int(latent_dim)))
     if workspace is None:
         need = attend_bytes(rows, heads, latent_dim, max_tokens)
         if need:
@@ -565,4 +577,40 @@ def attend_paged(q, cache, seq_lens, page_table, latent_dim: int, scale: float, 
                                      _stream(stream))
     if st != 0:
         raise DsatopkError(st, "dsatopk_attend_paged")
+    return out, lse
+
+
+def attend_expanded(q, k, v, k_rope, q_starts, k_starts, max_queries: int, scale: float,
+                    causal: bool = True, out=None, lse=None, stream=None):
+    """Expanded latent attention over a ragged batch of prompts.
+
+    ``q`` [queries, heads, 192], ``k`` and ``v`` [keys, heads, 128] and
+    ``k_rope`` [keys, 64] in bfloat16 or float16 (k and v may be parts of one
+    tensor); ``q_starts`` and ``k_starts`` int32 [requests + 1];
+    ``max_queries`` bounds a request's queries, which are its last tokens.
+    Returns ``(out, lse)``: q's type [queries, heads, 128], and float32
+    [queries, heads]."""
+    _tensor(q, 3, None, "q")
+    queries, heads, dim = q.shape
+    kind = _element_type(q, "q")
+    for name, t, dims in (("k", k, 3), ("v", v, 3), ("k_rope", k_rope, 2)):
+        _tensor(t, dims, q, name)
+        if t.dtype != q.dtype or t.shape[0] != k.shape[0] or (dims == 3 and t.shape[1] != heads):
+            raise ValueError(f"{name} must have q's type, k's rows and q's heads")
+    if dim != k.shape[2] + k_rope.shape[1]:
+        raise ValueError("q's last dimension must be k's and k_rope's together")
+    n = int(q_starts.shape[0]) - 1
+    if n < 0:
+        raise ValueError("q_starts must have an entry more than there are requests")
+    _vec_i32(q_starts, n + 1, "q_starts", q)
+    _vec_i32(k_starts, n + 1, "k_starts", q)
+    out, lse = _attend_out(out, lse, q, (queries, heads, int(v.shape[2])))
+    st = _lib().dsatopk_attend_expanded(
+        _ptr(q), _stride(q, 0), _stride(q, 1), _ptr(k), _stride(k, 0), _stride(k, 1), _ptr(v),
+        _stride(v, 0), _stride(v, 1), _ptr(k_rope), _stride(k_rope, 0), kind, heads, k.shape[2],
+        k_rope.shape[1], v.shape[2], float(scale), int(bool(causal)), _ptr(q_starts),
+        _ptr(k_starts), n, queries, k.shape[0], int(max_queries), _ptr(out), _ptr(lse),
+        _stream(stream))
+    if st != 0:
+        raise DsatopkError(st, "dsatopk_attend_expanded")
     return out, lse

@@ -292,3 +292,151 @@ def test_empty_calls():
     assert out.shape == (0, 16, 512) and lse.shape == (0, 16)
     out, lse = dt.attend_selected(q, cache[:0], i32([[0, 1, -1], [5, 5, 5]]), 512, SCALE)
     assert (out == 0).all() and (lse == -math.inf).all()
+
+
+# -------------------------------------------------------------------------
+# expanded form
+
+
+def check_expanded(q_lens, k_lens, heads, kind, causal=True, joined=True, extra=0):
+    import row_top_selection_amd as dt
+
+    g = torch.Generator(DEV).manual_seed(sum(q_lens) + heads)
+    q_starts = np.concatenate([[0], np.cumsum(q_lens)])
+    k_starts = np.concatenate([[0], np.cumsum(k_lens)])
+    tq, tk = int(q_starts[-1]) + extra, int(k_starts[-1])
+    t = TYPES[kind]
+    q = torch.randn(tq, heads, 192, generator=g, device=DEV).to(t)
+    if joined:
+        kv = torch.randn(tk, heads, 256, generator=g, device=DEV).to(t)
+        k, v = kv[..., :128], kv[..., 128:]
+    else:
+        k = torch.randn(tk, heads, 128, generator=g, device=DEV).to(t)
+        v = torch.randn(tk, heads, 128, generator=g, device=DEV).to(t)
+    rope = torch.randn(tk, 64, generator=g, device=DEV).to(t)
+    out = torch.full((tq, heads, 128), 7.0, dtype=t, device=DEV)
+    lse = torch.full((tq, heads), 7.0, device=DEV)
+    dt.attend_expanded(q, k, v, rope, i32(q_starts), i32(k_starts), max(q_lens), SCALE,
+                       causal=causal, out=out, lse=lse)
+    torch.cuda.synchronize()
+    want = serve_plain.expand(q, k, v, rope, q_starts.tolist(), k_starts.tolist(), SCALE, causal)
+    n = int(q_starts[-1])
+    size = 0.0
+    if tk:
+        size = float((q.float().abs().flatten(0, 1).max(0).values * torch.cat(
+            [k.float().abs().flatten(0, 1).max(0).values, rope.float().abs().max(0).values])).sum() * SCALE)
+    close(out[:n], lse[:n], tuple(w[:n] for w in want), size, 192)
+    assert (out[n:] == 7).all() and (lse[n:] == 7).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("q_lens,k_lens,heads", [
+    ([1], [1], 1),
+    ([1, 1, 1], [1, 64, 65], 3),
+    ([128, 129, 31], [128, 129, 31], 2),
+    ([5, 0, 70], [200, 9, 70], 1),
+    ([33, 1], [513, 700], 5),
+    ([300], [300], 1),
+])
+def test_expanded(kind, q_lens, k_lens, heads):
+    check_expanded(q_lens, k_lens, heads, kind)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_expanded_queries_without_keys(causal):
+    """Requests with fewer keys than queries (the first queries see none),
+    with no keys at all, and rows behind the last request."""
+    check_expanded([10, 40, 3, 140], [4, 0, 3, 70], 2, "bf16", causal=causal, joined=False, extra=5)
+
+
+def test_expanded_without_any_key():
+    check_expanded([3], [0], 2, "bf16")
+
+
+def test_expanded_without_causality():
+    check_expanded([40, 130], [100, 65], 2, "fp16", causal=False)
+
+
+def test_expanded_hidden_keys_may_hold_anything():
+    """Keys (not values) that causality hides, and everything of other
+    requests and behind the last one."""
+    import row_top_selection_amd as dt
+
+    g = torch.Generator(DEV).manual_seed(8)
+    q, k, v, rope = (torch.randn(*s, generator=g, device=DEV).to(torch.bfloat16)
+                     for s in ((90, 2, 192), (300, 2, 128), (300, 2, 128), (300, 64)))
+    starts = i32([0, 90]), i32([60, 150])
+    a = dt.attend_expanded(q, k, v, rope, *starts, 90, SCALE)
+    for t in (k, v, rope):
+        t[:60] = float("nan")
+        t[150:] = float("inf")
+    b = dt.attend_expanded(q, k, v, rope, *starts, 90, SCALE)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]) and torch.isfinite(b[0]).all()
+    # query 0 of 90 sees key 0 alone: keys 1 .. 89 hidden from it hold infinities
+    k[61:150] = float("inf")
+    c = dt.attend_expanded(q, k, v, rope, *starts, 90, SCALE)
+    assert torch.equal(c[0][0], a[0][0]) and torch.equal(c[1][0], a[1][0])
+
+
+def test_expanded_logits_of_every_size():
+    import row_top_selection_amd as dt
+
+    g = torch.Generator(DEV).manual_seed(9)
+    n = 400
+    k = torch.randn(n, 1, 128, generator=g, device=DEV)
+    k[:, 0, 0] = torch.arange(n, device=DEV) * 0.5
+    k, rope = k.to(torch.bfloat16), torch.zeros(n, 64, dtype=torch.bfloat16, device=DEV)
+    v = torch.randn(n, 1, 128, generator=g, device=DEV).to(torch.bfloat16)
+    q = torch.zeros(4, 1, 192, device=DEV)
+    q[0, 0, 0], q[1, 0, 0], q[3, 0, 1] = 1.0, -1.0, 200.0
+    q = q.to(torch.bfloat16)
+    out, lse = dt.attend_expanded(q, k, v, rope, i32([0, 4]), i32([0, n]), 4, 1.0, causal=False)
+    torch.cuda.synchronize()
+    want = serve_plain.expand(q, k, v, rope, [0, 4], [0, n], 1.0, False)
+    for b in range(4):
+        size = float((q[b, 0, :128].float().abs() @ k[:, 0].float().abs().T).max())
+        close(out[b:b + 1], lse[b:b + 1], tuple(w[b:b + 1] for w in want), size, 192)
+
+
+def test_expanded_is_absorbed():
+    """The two forms agree where values are the latent vectors themselves:
+    one head of 128 + 64 dimensions, keys and values the same vectors."""
+    import row_top_selection_amd as dt
+
+    g = torch.Generator(DEV).manual_seed(10)
+    x = torch.randn(500, 1, 128, generator=g, device=DEV).to(torch.bfloat16)
+    rope = torch.randn(500, 64, generator=g, device=DEV).to(torch.bfloat16)
+    q = torch.randn(1, 1, 192, generator=g, device=DEV).to(torch.bfloat16)
+    a = dt.attend_expanded(q, x, x, rope, i32([0, 1]), i32([0, 500]), 1, SCALE)
+    wide_q = torch.zeros(1, 1, 320, dtype=torch.bfloat16, device=DEV)
+    wide_q[..., :128], wide_q[..., 256:] = q[..., :128], q[..., 128:]
+    cache = torch.zeros(1, 512, 320, dtype=torch.bfloat16, device=DEV)
+    cache[0, :500, :128], cache[0, :500, 256:] = x[:, 0], rope
+    b = dt.attend_paged(wide_q, cache, i32([500]), i32([[0]]), 256, SCALE)
+    # both round weights (2^-8 of the values' weighted sizes) and outputs
+    size = serve_plain.expand(q, x, x, rope, [0, 1], [0, 500], SCALE)[2][0, 0]
+    diff = (a[0][0, 0].cpu().double() - b[0][0, 0, :128].cpu().double()).abs()
+    assert (diff <= 4 * 2.0 ** -8 * size).all()
+    assert abs(float(a[1][0, 0] - b[1][0, 0])) < 1e-5 * abs(float(a[1][0, 0]))
+
+
+def test_expanded_graph_replays_follow_the_lengths():
+    import row_top_selection_amd as dt
+
+    g = torch.Generator(DEV).manual_seed(11)
+    rng = np.random.default_rng(11)
+    q, k, v, rope = (torch.randn(*s, generator=g, device=DEV).to(torch.bfloat16)
+                     for s in ((200, 4, 192), (900, 4, 128), (900, 4, 128), (900, 64)))
+    qs, ks = i32([0, 100, 200]), i32([0, 500, 900])
+    out, lse = dt.attend_expanded(q, k, v, rope, qs, ks, 200, SCALE)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dt.attend_expanded(q, k, v, rope, qs, ks, 200, SCALE, out=out, lse=lse)
+    for _ in range(4):
+        qs.copy_(i32([0, rng.integers(0, 201), 200]))
+        ks.copy_(i32([0, rng.integers(0, 901), 900]))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        eager = dt.attend_expanded(q, k, v, rope, qs, ks, 200, SCALE)
+        assert torch.equal(out, eager[0]) and torch.equal(lse, eager[1])
