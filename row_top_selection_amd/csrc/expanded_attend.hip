@@ -57,8 +57,7 @@ struct ExpandParams {
 };
 
 // Copies keys j0 .. j0 + 63 (of the request's `keys`; rows past them repeat
-// the last) of all three tensors: a wave takes 16. Chunk c of key t goes to
-// c ^ swizzle(t), of the rotary part to c ^ (swizzle(t) & 7).
+// the last) of all three tensors, swizzled: a wave takes 16.
 __device__ __forceinline__ void copy_tile(const ExpandParams& p, char* tile, const char* k,
                                           const char* v, const char* rope, int32_t j0,
                                           int32_t keys, int wave, int lane) {
@@ -66,7 +65,7 @@ __device__ __forceinline__ void copy_tile(const ExpandParams& p, char* tile, con
   for (int i = 0; i < 4; ++i) {
     const int t = wave * 16 + i * 4 + (lane >> 4);
     const int64_t j = min(j0 + t, keys - 1);
-    const int at = ((lane & 15) ^ swizzle(t)) * 16;
+    const int at = ((lane & 15) ^ swizzle32(t)) * 16;
     copy_to_lds(k + j * p.k_row + at, tile + (wave * 16 + i * 4) * kKeyBytes);
     copy_to_lds(v + j * p.v_row + at, tile + kValueAt + (wave * 16 + i * 4) * kValueBytes);
   }
@@ -74,7 +73,7 @@ __device__ __forceinline__ void copy_tile(const ExpandParams& p, char* tile, con
   for (int i = 0; i < 2; ++i) {
     const int t = wave * 16 + i * 8 + (lane >> 3);
     const int64_t j = min(j0 + t, keys - 1);
-    copy_to_lds(rope + j * p.rope_row + ((lane & 7) ^ (swizzle(t) & 7)) * 16,
+    copy_to_lds(rope + j * p.rope_row + ((lane & 7) ^ swizzle8(t)) * 16,
                 tile + kRopeAt + (wave * 16 + i * 8) * kRopeBytes);
   }
 }
@@ -97,7 +96,7 @@ __device__ __forceinline__ void tile_step(const ExpandParams& p, State& st,
   const int col = lane & 31, half = lane >> 5;
   f32x16 s[2] = {};
   {
-    const int swz = swizzle(col);
+    const int swz = swizzle32(col);
     const char* row = cur + col * kKeyBytes;
     const char* tail = cur + kRopeAt + col * kRopeBytes;
 #pragma unroll
@@ -110,7 +109,7 @@ __device__ __forceinline__ void tile_step(const ExpandParams& p, State& st,
     for (int i = 0; i < kRope / 16; ++i)
 #pragma unroll
       for (int x = 0; x < 2; ++x)
-        s[x] = T::mma32(*reinterpret_cast<const u32x4*>(tail + (((2 * i + half) ^ (swz & 7)) << 4) + x * 32 * kRopeBytes),
+        s[x] = T::mma32(*reinterpret_cast<const u32x4*>(tail + (((2 * i + half) ^ swizzle8(col)) << 4) + x * 32 * kRopeBytes),
                         q[kNope / 16 + i], s[x]);
   }
   if (!whole) {
@@ -145,7 +144,7 @@ __device__ __forceinline__ void tile_step(const ExpandParams& p, State& st,
   // lane i of 16 points at row i / 4, 8 bytes i % 4 of a 4 x 32 byte block
   const int in = lane & 15, side = (lane >> 4) & 1;
   const int tok = 4 * half + (in >> 2);
-  const int swz = swizzle(tok);
+  const int swz = swizzle32(tok);
   int at[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j)
@@ -160,7 +159,7 @@ __device__ __forceinline__ void tile_step(const ExpandParams& p, State& st,
 #pragma unroll
       for (int b = 0; b < kBlocks; ++b) {
         const u32x2 lo = read_columns(rows + at[b]);
-        const u32x2 hi = read_columns(rows + at[b ^ 2] + 8 * kValueBytes);
+        const u32x2 hi = read_columns(rows + (at[b] ^ 32) + 8 * kValueBytes);  // swizzle32(t + 8) = swizzle32(t) ^ 2
         st.o[b] = T::mma32(u32x4{lo[0], lo[1], hi[0], hi[1]}, w, st.o[b]);
       }
     }

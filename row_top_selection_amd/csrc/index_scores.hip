@@ -85,8 +85,13 @@ __device__ __forceinline__ f32x16 product(u32x4 a, u32x4 b, f32x16 c) {
     return Bf16::mma32(a, b, c);
 }
 
-// Row r's heads into LDS. A head's chunk c sits at c ^ swizzle(head)
-// (modulo the row's chunks); heads that the row does not have are zeros.
+template <int kChunks>
+__device__ __forceinline__ constexpr int swizzle_of(int head) {
+  return kChunks == 8 ? swizzle8(head) : swizzle16(head);
+}
+
+// Row r's heads into LDS, swizzled; heads that the row does not have are
+// zeros.
 template <int kBytes>
 __device__ __forceinline__ void copy_heads(const ScoreParams& p, int32_t r, int wave, int lane,
                                            char* lds) {
@@ -97,7 +102,7 @@ __device__ __forceinline__ void copy_heads(const ScoreParams& p, int32_t r, int 
   for (int h = wave * kCopyRows; h < ((p.heads + 31) & ~31); h += kCopyRows * (kBlock / 64)) {
     const int hh = h + sub;
     const char* src = hh < p.heads ? q + hh * p.q_head : zero_row();
-    copy_to_lds(src + ((c ^ swizzle(hh)) & (kChunks - 1)) * 16, lds + h * kBytes);
+    copy_to_lds(src + (c ^ swizzle_of<kChunks>(hh)) * 16, lds + h * kBytes);
   }
 }
 
@@ -128,7 +133,7 @@ struct ByteHeads {
       widen(piece[g], w);
 #pragma unroll
       for (int x = 0; x < 2; ++x)
-        *reinterpret_cast<u32x4*>(lds + h * kBytes + (((c + x) ^ swizzle(h)) & (kChunks - 1)) * 16) =
+        *reinterpret_cast<u32x4*>(lds + h * kBytes + ((c + x) ^ swizzle_of<kChunks>(h)) * 16) =
             u32x4{w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]};
     }
   }
@@ -155,7 +160,7 @@ __device__ __forceinline__ void row_sums(const ScoreParams& p, const char* __res
 #pragma unroll
     for (int s = 0; s < S::kSteps; ++s) {
       const u32x4 a = *reinterpret_cast<const u32x4*>(
-          row + (((S::chunk(s, half) ^ swizzle(head)) & (S::kChunks - 1)) << 4));
+          row + ((S::chunk(s, half) ^ swizzle_of<S::kChunks>(head)) << 4));
 #pragma unroll
       for (int n = 0; n < 2; ++n)
         acc[n] = product<kKind>(a, u32x4{key[n][4 * s], key[n][4 * s + 1], key[n][4 * s + 2], key[n][4 * s + 3]}, acc[n]);

@@ -21,14 +21,14 @@
 // tile by columns; the LDS column reads give it from the same tile that the
 // rows were read from.
 //
-// A workgroup of four waves takes one row, up to 128 heads and a range of
-// tokens (split over workgroups when there are few rows; a second kernel
-// joins the parts), 64 tokens a tile, copied to LDS ahead of their use
-// without passing through registers. The waves are WH groups of heads by WT
-// groups of a tile's tokens; token groups keep sums of their own and join
-// them at the end. The vectors of 64 tokens fill 72 KB of LDS: two tiles,
-// one workgroup and one wave per SIMD with up to 512 registers, of which the
-// sums take 256 for 32 heads a wave.
+// A workgroup takes one row, up to 128 heads and a range of tokens (split
+// over workgroups when there are few rows; a second kernel joins the parts),
+// 64 tokens a tile, copied to LDS ahead of their use without passing through
+// registers. Its waves are WH groups of 16 heads by WT groups of a tile's
+// tokens; token groups keep sums of their own and join them at the end. The
+// vectors of 64 tokens fill 72 KB of LDS: two tiles, so one workgroup a CU,
+// of 8 waves where there are heads enough. A wave's sums take 128 registers
+// and its queries 72.
 //
 // Weights are rounded to the inputs' 16-bit type for the second product
 // (off by at most 2^-8 or 2^-11 of each, of either sign); scores, maxima, sums and
@@ -39,11 +39,9 @@
 namespace dsatopk_serve {
 namespace {
 
-constexpr int kBlock = 256;
 constexpr int kTile = 64;  // tokens
 constexpr int kRope = 64;
 constexpr int kRopeBytes = kRope * 2;
-constexpr int kCopyTokens = kTile / 4;  // a wave's share of a tile's copies
 constexpr float kGrow = 8.0f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -69,123 +67,101 @@ struct AttendParams {
   float* state;
 };
 
-template <int kHeads, int kWH, int kWT, int kLatent_>
+// Waves of a workgroup: WH groups of 16 heads by WT groups of tokens.
+template <int kWH_, int kWT_, int kLatent_>
 struct Plan {
-  static constexpr int kHB = kHeads;  // heads a wave: 16 or 32
+  static constexpr int kWH = kWH_, kWT = kWT_, kWaves = kWH * kWT;
+  static constexpr int kBlock = kWaves * 64;
   static constexpr int kLatent = kLatent_;
-  static constexpr int kRow = kLatent * 2;           // bytes of a latent vector
+  static constexpr int kRow = kLatent * 2;      // bytes of a latent vector
   static constexpr int kBuffer = kTile * (kRow + kRopeBytes);
-  static constexpr int kTokens = kTile / kWT;        // a wave's of a tile
-  static constexpr int kAcc = kHB * kHB / 64;        // registers of one
-  static constexpr int kSteps = kLatent * kHB / 512; // contraction steps over the latent part
-  static constexpr int kRopeSteps = kRope * kHB / 512;
-  static constexpr int kBlocks = kLatent / kHB;      // output blocks
-  static constexpr int kGroups = 64 / kHB;           // lane groups: 2 or 4
+  static constexpr int kTokens = kTile / kWT;   // a wave's of a tile
+  static constexpr int kGo = kTokens == 16 ? 1 : 2;  // 16 tokens each, taken at once
+  static constexpr int kCopy = kTile / kWaves;  // tokens that a wave copies
+  static constexpr int kSteps = kLatent / 32;   // contraction steps over the latent part
+  static constexpr int kRopeSteps = kRope / 32;
+  static constexpr int kBlocks = kLatent / 16;  // output blocks
+  static constexpr bool kOwn = kWH == 1;        // a wave copies what it reads
 };
-
-template <int kAcc>
-struct Acc;
-template <>
-struct Acc<16> {
-  using type = f32x16;
-};
-template <>
-struct Acc<4> {
-  using type = f32x4;
-};
-
-template <class T>
-__device__ __forceinline__ f32x16 mma(u32x4 a, u32x4 b, f32x16 c) {
-  return T::mma32(a, b, c);
-}
-template <class T>
-__device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
-  return T::mma16(a, b, c);
-}
 
 // Largest (sum) over the lanes that hold the same head.
-template <int kHB>
 __device__ __forceinline__ float head_max(float x) {
-  if constexpr (kHB == 16) x = fmaxf(x, __shfl_xor(x, 16));
+  x = fmaxf(x, __shfl_xor(x, 16));
   return fmaxf(x, __shfl_xor(x, 32));
 }
-template <int kHB>
 __device__ __forceinline__ float head_sum(float x) {
-  if constexpr (kHB == 16) x += __shfl_xor(x, 16);
+  x += __shfl_xor(x, 16);
   return x + __shfl_xor(x, 32);
 }
 
-// Copies 16 tokens' vectors into a tile's rows 16 * wave ..; `at` is the
-// address of token lane % 16. Chunk c of token t goes to c ^ swizzle(t).
+// Copies the wave's P::kCopy tokens of a tile; `at` is the address of token
+// lane % P::kCopy of them.
 template <class P>
 __device__ __forceinline__ void copy_tokens(char* tile, uint64_t at, int wave, int lane) {
   constexpr int kChunks = P::kRow / 16;
   constexpr int kPer = 64 / kChunks;  // tokens a copy
+  lane = here(lane);
   const uint32_t lo = (uint32_t)at, hi = (uint32_t)(at >> 32);
+  const int first = wave * P::kCopy;
 #pragma unroll
-  for (int t = 0; t < kCopyTokens; t += kPer) {
+  for (int t = 0; t < P::kCopy; t += kPer) {
     uint64_t base = ((uint64_t)__builtin_amdgcn_readlane(hi, t) << 32) |
                     (uint32_t)__builtin_amdgcn_readlane(lo, t);
-    int chunk = lane ^ swizzle(t);
+    int chunk = lane ^ swizzle16(first + t);
     if constexpr (kPer == 2) {
       const uint64_t second = ((uint64_t)__builtin_amdgcn_readlane(hi, t + 1) << 32) |
                               (uint32_t)__builtin_amdgcn_readlane(lo, t + 1);
       if (lane >= 32) base = second;
-      chunk = (lane & 31) ^ (lane >= 32 ? swizzle(t + 1) : swizzle(t));
+      chunk = (lane & 31) ^ swizzle16(first + t + (lane >> 5));
     }
-    copy_to_lds(reinterpret_cast<const char*>(base) + chunk * 16,
-                tile + (wave * kCopyTokens + t) * P::kRow);
+    copy_to_lds(reinterpret_cast<const char*>(base) + chunk * 16, tile + (first + t) * P::kRow);
   }
 #pragma unroll
-  for (int t = 0; t < kCopyTokens; t += 8) {
+  for (int t = 0; t < P::kCopy; t += 8) {
     const int mine = t + (lane >> 3);
     const uint64_t base = ((uint64_t)(uint32_t)__shfl((int)hi, mine) << 32) |
                           (uint32_t)__shfl((int)lo, mine);
-    const int chunk = (lane & 7) ^ (swizzle(mine) & 7);
-    copy_to_lds(reinterpret_cast<const char*>(base) + P::kRow + chunk * 16,
-                tile + kTile * P::kRow + (wave * kCopyTokens + t) * kRopeBytes);
+    copy_to_lds(reinterpret_cast<const char*>(base) + P::kRow + ((lane & 7) ^ swizzle8(first + mine)) * 16,
+                tile + kTile * P::kRow + (first + t) * kRopeBytes);
   }
 }
 
 // A wave's running state.
 template <class P>
 struct State {
-  typename Acc<P::kAcc>::type o[P::kBlocks];
+  f32x4 o[P::kBlocks];
   float top, sum;  // the reference maximum (log2), this lane's part of the sum
 };
 
-// Scores, weights and sums of kGo consecutive products' tokens (kGo * kHB of
-// them) from tile row `from` on, and first the next tile's copies if `more`:
-// the two buffers are told apart so that no read of one waits for the
-// other's copies. `valid`: a bit for each token. Returns false, with `st`
-// untouched and the scores' maximum in `top`, if that is too far above the
-// reference in use.
-template <class T, class P, int kGo>
-__device__ __forceinline__ bool attend_tokens(State<P>& st, const u32x4 (&q)[P::kSteps + P::kRopeSteps],
+// Scores, weights and sums of the wave's next P::kGo * 16 tokens, from tile row
+// `from` on, and first the next tile's copies if `more`: the two buffers are
+// told apart so that no read of one waits for the other's copies. `valid`: a
+// bit for each token.
+template <class T, class P>
+__device__ __forceinline__ void attend_tokens(State<P>& st, const u32x4 (&q)[P::kSteps + P::kRopeSteps],
                                               const char* __restrict__ cur, char* __restrict__ next,
                                               bool more, uint64_t next_at, int wave, int from,
-                                              uint64_t valid, int lane, float scale2, float& top) {
-  constexpr int kHB = P::kHB;
+                                              uint64_t valid, int lane, float scale2) {
+  constexpr int kGo = P::kGo;
   if (more) copy_tokens<P>(next, next_at, wave, lane);
-  using acc_t = typename Acc<P::kAcc>::type;
-  const int col = lane % kHB, group = lane / kHB;
-  acc_t s[kGo];
+  lane = here(lane);
+  const int col = lane & 15, group = lane >> 4;
+  f32x4 s[kGo];
   {
-    const int swz = swizzle(col);  // rows `from` on: `from` is a multiple of 16
-    constexpr int kPer = 16 / P::kGroups;  // steps whose chunks share their upper bits
+    const int swz = swizzle16(col);  // rows `from` on: `from` is a multiple of 16
     const char* row = cur + (from + col) * P::kRow;
     const char* rope = cur + kTile * P::kRow + (from + col) * kRopeBytes;
 #pragma unroll
-    for (int x = 0; x < kGo; ++x) s[x] = acc_t{};
+    for (int x = 0; x < kGo; ++x) s[x] = f32x4{};
     // Reads go kAhead steps before the products that take them, and no
-    // further: registers are what a wave of 32 heads has least of.
-    constexpr int kAhead = 4, kAll = P::kSteps + P::kRopeSteps;
+    // further: registers are what a wave has least of.
+    constexpr int kAhead = 3, kAll = P::kSteps + P::kRopeSteps;
     auto read = [&](int i, int x) {
       if (i < P::kSteps)
         return *reinterpret_cast<const u32x4*>(
-            row + (((P::kGroups * (i % kPer) + group) ^ swz) << 4) + (i / kPer) * 256 + x * kHB * P::kRow);
+            row + (((4 * (i & 3) + group) ^ swz) << 4) + (i >> 2) * 256 + x * 16 * P::kRow);
       return *reinterpret_cast<const u32x4*>(
-          rope + (((P::kGroups * (i - P::kSteps) + group) ^ (swz & 7)) << 4) + x * kHB * kRopeBytes);
+          rope + (((4 * (i - P::kSteps) + group) ^ swizzle8(col)) << 4) + x * 16 * kRopeBytes);
     };
     u32x4 a[kAhead][kGo];
 #pragma unroll
@@ -197,101 +173,92 @@ __device__ __forceinline__ bool attend_tokens(State<P>& st, const u32x4 (&q)[P::
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int x = 0; x < kGo; ++x) {
-        s[x] = mma<T>(a[i % kAhead][x], q[i], s[x]);
+        s[x] = T::mma16(a[i % kAhead][x], q[i], s[x]);
         if (i + kAhead < kAll) a[i % kAhead][x] = read(i + kAhead, x);
       }
     }
   }
-  // register i of a product holds its token 8 * (i / 4) + 4 * group + i % 4
-  constexpr uint32_t kAll = kGo * kHB == 32 ? ~0u : (1u << (kGo * kHB)) - 1;
-  if ((uint32_t)valid != kAll) {
+  // register i of product x holds its token 4 * group + i
+  constexpr uint32_t kEvery = kGo == 2 ? ~0u : 0xffffu;
+  if ((uint32_t)valid != kEvery) {
     const uint32_t mine = (uint32_t)valid >> (4 * group);
 #pragma unroll
     for (int x = 0; x < kGo; ++x)
 #pragma unroll
-      for (int i = 0; i < P::kAcc; ++i)
-        if (!((mine >> (x * kHB + 8 * (i / 4) + i % 4)) & 1)) s[x][i] = -INFINITY;
+      for (int i = 0; i < 4; ++i)
+        if (!((mine >> (x * 16 + i)) & 1)) s[x][i] = -INFINITY;
   }
-  top = s[0][0];
+  float top = s[0][0];
 #pragma unroll
   for (int x = 0; x < kGo; ++x)
 #pragma unroll
-    for (int i = 0; i < P::kAcc; ++i) top = fmaxf(top, s[x][i]);
-  top = head_max<kHB>(top) * scale2;
-  if (__any(top > st.top + kGrow)) return false;
+    for (int i = 0; i < 4; ++i) top = fmaxf(top, s[x][i]);
+  top = head_max(top) * scale2;
+  if (__any(top > st.top + kGrow)) {
+    const float to = fmaxf(st.top, top);
+    const float by = st.top == -INFINITY ? 0.0f : exp2_fast(st.top - to);
+    st.top = to;
+    st.sum *= by;
+#pragma unroll
+    for (int b = 0; b < P::kBlocks; ++b) st.o[b] *= by;
+  }
   const float ref = st.top == -INFINITY ? 0.0f : st.top;
 #pragma unroll
   for (int x = 0; x < kGo; ++x)
 #pragma unroll
-    for (int i = 0; i < P::kAcc; ++i) {
+    for (int i = 0; i < 4; ++i) {
       s[x][i] = exp2_fast(fmaf(s[x][i], scale2, -ref));
       st.sum += s[x][i];
     }
 
   // sums: lane i of 16 points at row i / 4, 8 bytes i % 4 of a 4 x 32 byte block
   const int in = lane & 15;
-  if constexpr (kHB == 32) {
-    const int half = lane >> 5, side = (lane >> 4) & 1;
-    const int tok = 4 * half + (in >> 2);
-    const int swz = swizzle(tok);
-    int at[4];
+  const int tok = 4 * group + (in >> 2);
+  const int swz = swizzle16(tok);
+  int at[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      at[j] = (from + tok) * P::kRow + (((4 * j + 2 * side + ((in & 3) >> 1)) ^ swz) << 4) + 8 * (in & 1);
+  for (int j = 0; j < 8; ++j)
+    at[j] = (from + tok) * P::kRow + (((2 * j + ((in & 3) >> 1)) ^ swz) << 4) + 8 * (in & 1);
+  if constexpr (kGo == 1) {
+    const u32x2 w = {T::pack(s[0][0], s[0][1]), T::pack(s[0][2], s[0][3])};
+    constexpr int kAhead = 8;
+    u32x2 a[kAhead];
+    auto read = [&](int b) { return read_columns(cur + at[b & 7] + (b >> 3) * 256); };
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const u32x4 w = {T::pack(s[0][8 * k], s[0][8 * k + 1]), T::pack(s[0][8 * k + 2], s[0][8 * k + 3]),
-                       T::pack(s[0][8 * k + 4], s[0][8 * k + 5]), T::pack(s[0][8 * k + 6], s[0][8 * k + 7])};
-      const char* rows = cur + 16 * k * P::kRow;
-      auto read = [&](int b) {
-        const u32x2 lo = read_columns(rows + at[b & 3] + (b >> 2) * 256);
-        const u32x2 hi = read_columns(rows + at[(b & 3) ^ 2] + (b >> 2) * 256 + 8 * P::kRow);
-        return u32x4{lo[0], lo[1], hi[0], hi[1]};
-      };
-      constexpr int kAhead = 4;
-      u32x4 a[kAhead];
+    for (int b = 0; b < kAhead; ++b) a[b] = read(b);
 #pragma unroll
-      for (int b = 0; b < kAhead; ++b) a[b] = read(b);
-#pragma unroll
-      for (int b = 0; b < P::kBlocks; ++b) {
-        __builtin_amdgcn_sched_barrier(0);
-        st.o[b] = mma<T>(a[b % kAhead], w, st.o[b]);
-        if (b + kAhead < P::kBlocks) a[b % kAhead] = read(b + kAhead);
-      }
+    for (int b = 0; b < P::kBlocks; ++b) {
+      __builtin_amdgcn_sched_barrier(0);
+      st.o[b] = T::mma16_half(a[b % kAhead], w, st.o[b]);
+      if (b + kAhead < P::kBlocks) a[b % kAhead] = read(b + kAhead);
     }
   } else {
-    const int tok = 4 * group + (in >> 2);
-    const int swz = swizzle(tok);
-    int at[8];
+    const u32x4 w = {T::pack(s[0][0], s[0][1]), T::pack(s[0][2], s[0][3]),
+                     T::pack(s[1][0], s[1][1]), T::pack(s[1][2], s[1][3])};
+    constexpr int kAhead = 5;
+    u32x4 a[kAhead];
+    auto read = [&](int b) {
+      const u32x2 lo = read_columns(cur + at[b & 7] + (b >> 3) * 256);
+      const u32x2 hi = read_columns(cur + at[b & 7] + (b >> 3) * 256 + 16 * P::kRow);
+      return u32x4{lo[0], lo[1], hi[0], hi[1]};
+    };
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      at[j] = (from + tok) * P::kRow + (((2 * j + ((in & 3) >> 1)) ^ swz) << 4) + 8 * (in & 1);
-    if constexpr (kGo == 1) {
-      const u32x2 w = {T::pack(s[0][0], s[0][1]), T::pack(s[0][2], s[0][3])};
+    for (int b = 0; b < kAhead; ++b) a[b] = read(b);
 #pragma unroll
-      for (int b = 0; b < P::kBlocks; ++b)
-        st.o[b] = T::mma16_half(read_columns(cur + at[b & 7] + (b >> 3) * 256), w, st.o[b]);
-    } else {
-      const u32x4 w = {T::pack(s[0][0], s[0][1]), T::pack(s[0][2], s[0][3]),
-                       T::pack(s[1][0], s[1][1]), T::pack(s[1][2], s[1][3])};
-#pragma unroll
-      for (int b = 0; b < P::kBlocks; ++b) {
-        const u32x2 lo = read_columns(cur + at[b & 7] + (b >> 3) * 256);
-        const u32x2 hi = read_columns(cur + at[b & 7] + (b >> 3) * 256 + 16 * P::kRow);
-        st.o[b] = mma<T>(u32x4{lo[0], lo[1], hi[0], hi[1]}, w, st.o[b]);
-      }
+    for (int b = 0; b < P::kBlocks; ++b) {
+      __builtin_amdgcn_sched_barrier(0);
+      st.o[b] = T::mma16(a[b % kAhead], w, st.o[b]);
+      if (b + kAhead < P::kBlocks) a[b % kAhead] = read(b + kAhead);
     }
   }
-  return true;
 }
 
-template <class T, int kHeads, int kWH, int kWT, int kLatent, bool kPaged>
-__global__ __launch_bounds__(kBlock, 1) void attend_kernel(AttendParams p) {
-  using P = Plan<kHeads, kWH, kWT, kLatent>;
-  constexpr int kHB = P::kHB;
+template <class T, class P, bool kPaged>
+__global__ __launch_bounds__(P::kBlock) void attend_kernel(AttendParams p) {
+  constexpr int kWH = P::kWH, kWT = P::kWT;
   __shared__ __attribute__((aligned(1024))) char tiles[2 * P::kBuffer];
-  __shared__ uint32_t masks[2][4];
-  __shared__ float joined[2][4][kHB];
+  __shared__ uint32_t masks[2][P::kWaves];
+  __shared__ float joined[2][P::kWaves][16];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -316,16 +283,16 @@ __global__ __launch_bounds__(kBlock, 1) void attend_kernel(AttendParams p) {
   const int32_t first = split * per;
   const int32_t last = min(first + per, tiles_all);
 
-  // The entry (slot or page) of token lane % 16 of this wave's share of a tile, -1: none.
+  // The entry (slot or page) of token lane % P::kCopy of this wave's share of a tile, -1: none.
   auto entry_of = [&](int32_t tile) {
-    const int32_t j = tile * kTile + wave * kCopyTokens + (lane & 15);
+    const int32_t j = tile * kTile + wave * P::kCopy + lane % P::kCopy;
     if (tile >= last || j >= len) return -1;
     return list[kPaged ? j >> p.page_bits : j];
   };
   // Its address, or that of zeros.
   auto address_of = [&](int32_t tile, int32_t entry, bool& there) {
     int64_t page = entry;
-    int32_t in = tile * kTile + wave * kCopyTokens + (lane & 15);
+    int32_t in = tile * kTile + wave * P::kCopy + lane % P::kCopy;
     if constexpr (!kPaged) {
       page = entry >> p.page_bits;
       in = entry;
@@ -335,23 +302,22 @@ __global__ __launch_bounds__(kBlock, 1) void attend_kernel(AttendParams p) {
     const char* at = there ? p.cache + page * p.page + in * p.token : zero_row();
     return (uint64_t)(uintptr_t)at;
   };
+  auto bits_of = [&](bool there) { return (uint32_t)(__ballot(there) & ((1ull << P::kCopy) - 1)); };
 
   State<P> st;
   st.top = -INFINITY;
   st.sum = 0.0f;
 #pragma unroll
-  for (int b = 0; b < P::kBlocks; ++b) {
-    st.o[b] = typename Acc<P::kAcc>::type{};
-  }
+  for (int b = 0; b < P::kBlocks; ++b) st.o[b] = f32x4{};
 
-  const int col = lane % kHB, group = lane / kHB;
-  const int head = (block * kWH + wh) * kHB + col;
+  const int col = lane & 15, group = lane >> 4;
+  const int head = (block * kWH + wh) * 16 + col;
   if (first < last) {
     int32_t entry = entry_of(first);
     bool there;
     uint64_t at = address_of(first, entry, there);
-    uint32_t mask = (uint32_t)__ballot(there) & 0xffff;
-    if (kWT < 4 && lane == 0) masks[0][wave] = mask;
+    uint32_t mask = bits_of(there);
+    if (!P::kOwn && lane == 0) masks[0][wave] = mask;
     copy_tokens<P>(tiles, at, wave, lane);
     entry = entry_of(first + 1);
 
@@ -359,74 +325,44 @@ __global__ __launch_bounds__(kBlock, 1) void attend_kernel(AttendParams p) {
     const char* qh = head < p.heads ? p.q + row * p.q_row + head * p.q_head : zero_row();
 #pragma unroll
     for (int i = 0; i < P::kSteps + P::kRopeSteps; ++i)
-      q[i] = *reinterpret_cast<const u32x4*>(qh + (P::kGroups * i + group) * 16);
+      q[i] = *reinterpret_cast<const u32x4*>(qh + (4 * i + group) * 16);
 
-    // A pass of the inner loop takes the wave's next kGo * kHB tokens. It has
-    // only products touch the sums, which thereby stay where those keep
-    // them; when a maximum outgrows the reference the loop is left, the sums
-    // are rescaled, and the tokens are taken again.
-    constexpr int kGo = P::kTokens == 16 ? 1 : 32 / kHB;
-    int32_t t = first;
-    int from = P::kTokens;  // past the wave's tokens of the tile before
-    int buf = 1;
-    uint64_t valid = 0;
-    bool more = false;
-    --t;
-    for (;;) {
-      float high = 0.0f;
-      bool done = false;
-      for (;;) {
-        if (from == P::kTokens) {
-          if (++t == last) {
-            done = true;
-            break;
-          }
-          from = 0;
-          buf ^= 1;
-          if constexpr (kWT == 4) {
-            wait_copies();  // a wave copies and reads the same tokens
-            valid = mask;
-          } else {
-            copies_barrier();
-            const uint32_t lo = masks[buf][0] | masks[buf][1] << 16;
-            const uint32_t hi = masks[buf][2] | masks[buf][3] << 16;
-            const uint32_t a = __builtin_amdgcn_readfirstlane(kWT == 2 && wt ? hi : lo);
-            valid = a;
-            if constexpr (kWT == 1) valid |= (uint64_t)__builtin_amdgcn_readfirstlane(hi) << 32;
-          }
-          more = t + 1 < last;
-          if (more) {
-            at = address_of(t + 1, entry, there);
-            mask = (uint32_t)__ballot(there) & 0xffff;
-            if (kWT < 4 && lane == 0) masks[buf ^ 1][wave] = mask;
-            entry = entry_of(t + 2);
-          }
-        }
-        if (!attend_tokens<T, P, kGo>(st, q, tiles + buf * P::kBuffer, tiles + (buf ^ 1) * P::kBuffer,
-                                      more, at, wave, wt * P::kTokens + from, valid >> from, lane,
-                                      p.scale2, high))
-          break;
-        more = false;
-        from += kGo * kHB;
-      }
-      if (done) break;
-      more = false;
-      const float to = fmaxf(st.top, high);
-      const float by = st.top == -INFINITY ? 0.0f : exp2_fast(st.top - to);
-      st.top = to;
-      st.sum *= by;
+    for (int32_t t = first; t < last; ++t) {
+      const int buf = (t - first) & 1;
+      uint64_t valid;
+      if constexpr (P::kOwn) {
+        wait_copies();
+        valid = mask;
+      } else {
+        copies_barrier();
+        uint64_t all = 0;
+        constexpr int kParts = P::kTokens / P::kCopy;  // waves whose copies this one reads
 #pragma unroll
-      for (int b = 0; b < P::kBlocks; ++b) {
-        st.o[b] *= by;
+        for (int w = 0; w < kParts; ++w)
+          all |= (uint64_t)masks[buf][wt * kParts + w] << (w * P::kCopy);
+        valid = (uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(all >> 32)) << 32 |
+                (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)all);
       }
+      const bool more = t + 1 < last;
+      if (more) {
+        at = address_of(t + 1, entry, there);
+        mask = bits_of(there);
+        if (!P::kOwn && lane == 0) masks[buf ^ 1][wave] = mask;
+        entry = entry_of(t + 2);
+      }
+#pragma unroll 1
+      for (int from = 0; from < P::kTokens; from += P::kGo * 16)
+        attend_tokens<T, P>(st, q, tiles + buf * P::kBuffer, tiles + (buf ^ 1) * P::kBuffer,
+                            more && from == 0, at, wave, wt * P::kTokens + from, valid >> from, lane,
+                            p.scale2);
     }
   }
-  float sum = head_sum<kHB>(st.sum);
+
+  float sum = head_sum(st.sum);
   float top = st.top;
   if constexpr (kWT > 1) {
     // join the token groups: each wave's sums to the common maximum, then into group 0
-    constexpr int kRegs = P::kBlocks * P::kAcc;
-    if (lane < kHB) {
+    if (lane < 16) {
       joined[0][wave][lane] = top;
       joined[1][wave][lane] = sum;
     }
@@ -442,40 +378,39 @@ __global__ __launch_bounds__(kBlock, 1) void attend_kernel(AttendParams p) {
     const float by = top == -INFINITY ? 0.0f : exp2_fast(top - all);
 #pragma unroll
     for (int b = 0; b < P::kBlocks; ++b) st.o[b] *= by;
-    float* give = reinterpret_cast<float*>(tiles);
-    if (wt > 0) {
-      float* to = give + (size_t)(wave - kWH) * kRegs * 64 + lane;
+    // the upper half of the groups gives to the lower, until one is left
+    constexpr int kShare = P::kBlocks * 256;  // floats of a wave
+    static_assert(kWH * (kWT / 2) * kShare * 4 <= 2 * P::kBuffer, "the tiles' space holds what is given");
+    float* give = reinterpret_cast<float*>(tiles) + lane * 4;
 #pragma unroll
-      for (int b = 0; b < P::kBlocks; ++b)
+    for (int step = kWT / 2; step; step /= 2) {
+      __syncthreads();
+      if (wt >= step && wt < 2 * step) {
+        float* to = give + ((wt - step) * kWH + wh) * kShare;
 #pragma unroll
-        for (int i = 0; i < P::kAcc; ++i) to[(b * P::kAcc + i) * 64] = st.o[b][i];
+        for (int b = 0; b < P::kBlocks; ++b) *reinterpret_cast<f32x4*>(to + b * 256) = st.o[b];
+      }
+      __syncthreads();
+      if (wt < step) {
+        const float* from = give + (wt * kWH + wh) * kShare;
+#pragma unroll
+        for (int b = 0; b < P::kBlocks; ++b) st.o[b] += *reinterpret_cast<const f32x4*>(from + b * 256);
+      }
     }
-    __syncthreads();
     if (wt > 0) return;
-#pragma unroll
-    for (int w = 1; w < kWT; ++w) {
-      const float* from = give + (size_t)(w * kWH + wh - kWH) * kRegs * 64 + lane;
-#pragma unroll
-      for (int b = 0; b < P::kBlocks; ++b)
-#pragma unroll
-        for (int i = 0; i < P::kAcc; ++i) st.o[b][i] += from[(b * P::kAcc + i) * 64];
-    }
     top = all;
     sum = total;
   }
   if (head >= p.heads) return;
 
-  // register i of block b: element b * kHB + 8 * (i / 4) + 4 * group + i % 4 of the head's vector
+  // register i of block b: element b * 16 + 4 * group + i of the head's vector
   if (p.splits == 1) {
     const float by = sum == 0.0f ? 0.0f : 1.0f / sum;
-    char* to = p.out + ((row * p.heads + head) * kLatent + 4 * group) * 2;
+    char* to = p.out + ((row * p.heads + head) * P::kLatent + 4 * group) * 2;
 #pragma unroll
     for (int b = 0; b < P::kBlocks; ++b)
-#pragma unroll
-      for (int i = 0; i < P::kAcc; i += 4)
-        *reinterpret_cast<u32x2*>(to + (b * kHB + 2 * i) * 2) =
-            u32x2{T::pack(st.o[b][i] * by, st.o[b][i + 1] * by),
-                  T::pack(st.o[b][i + 2] * by, st.o[b][i + 3] * by)};
+      *reinterpret_cast<u32x2*>(to + b * 32) = u32x2{T::pack(st.o[b][0] * by, st.o[b][1] * by),
+                                                     T::pack(st.o[b][2] * by, st.o[b][3] * by)};
     if (p.lse && group == 0) p.lse[row * p.heads + head] = (top + log2f(sum)) * kLn2;
   } else {
     const int64_t at = (row * p.splits + split) * p.heads + head;
@@ -484,74 +419,121 @@ __global__ __launch_bounds__(kBlock, 1) void attend_kernel(AttendParams p) {
       p.state[at * 2 + 1] = sum;
     }
     if (top == -INFINITY && sum == 0.0f) return;  // nothing seen: the join skips it
-    float* to = p.part + at * kLatent + 4 * group;
+    float* to = p.part + at * P::kLatent + 4 * group;
 #pragma unroll
-    for (int b = 0; b < P::kBlocks; ++b)
-#pragma unroll
-      for (int i = 0; i < P::kAcc; i += 4)
-        *reinterpret_cast<f32x4*>(to + b * kHB + 2 * i) =
-            f32x4{st.o[b][i], st.o[b][i + 1], st.o[b][i + 2], st.o[b][i + 3]};
+    for (int b = 0; b < P::kBlocks; ++b) *reinterpret_cast<f32x4*>(to + b * 16) = st.o[b];
   }
 }
 
-// Joins the splits of one row's head: a thread has 4 elements.
+// Joins the splits of one row's head. First a thread for each split: the
+// common maximum and the factors; then kLatent / 4 threads for each of
+// kSides sets of splits, 4 elements each.
+constexpr int kMaxSplits = 256;
+constexpr int kJoinBlock = 256;
+
 template <class T, int kLatent>
-__global__ __launch_bounds__(kLatent / 4) void join_kernel(AttendParams p) {
+__global__ __launch_bounds__(kJoinBlock) void join_kernel(AttendParams p) {
+  constexpr int kSides = kJoinBlock / (kLatent / 4);
+  __shared__ float tops[kJoinBlock / 64], sums[kJoinBlock / 64];
+  __shared__ float factor[kMaxSplits];
+  __shared__ __attribute__((aligned(16))) float half[kJoinBlock * 4];
+  const int tid = threadIdx.x, wave = tid >> 6;
   const int64_t row = blockIdx.x / p.heads;
   const int head = blockIdx.x % p.heads;
   const int64_t base = row * p.splits * p.heads + head;
-  float top = -INFINITY;
-  for (int s = 0; s < p.splits; ++s) top = fmaxf(top, p.state[(base + (int64_t)s * p.heads) * 2]);
-  const float ref = top == -INFINITY ? 0.0f : top;
-  f32x4 o = {};
-  float sum = 0.0f;
-  for (int s = 0; s < p.splits; ++s) {
-    const int64_t at = base + (int64_t)s * p.heads;
-    const float x = p.state[at * 2], n = p.state[at * 2 + 1];
-    if (x == -INFINITY && n == 0.0f) continue;
-    const float by = exp2_fast(x - ref);
-    sum += n * by;
-    o += *reinterpret_cast<const f32x4*>(p.part + at * kLatent + threadIdx.x * 4) * by;
+
+  float x = -INFINITY, n = 0.0f;
+  if (tid < p.splits) {
+    const float* s = p.state + (base + (int64_t)tid * p.heads) * 2;
+    x = s[0];
+    n = s[1];
   }
-  const float by = sum == 0.0f ? 0.0f : 1.0f / sum;
-  const int64_t at = row * p.heads + head;
-  *reinterpret_cast<u32x2*>(p.out + (at * kLatent + threadIdx.x * 4) * 2) =
-      u32x2{T::pack(o[0] * by, o[1] * by), T::pack(o[2] * by, o[3] * by)};
-  if (p.lse && threadIdx.x == 0) p.lse[at] = (top + log2f(sum)) * kLn2;
+  float top = x;
+#pragma unroll
+  for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
+  if ((tid & 63) == 0) tops[wave] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kJoinBlock / 64; ++w) top = fmaxf(top, tops[w]);
+  const bool empty = x == -INFINITY && n == 0.0f;  // such a split has written no vector
+  const float by = empty ? 0.0f : exp2_fast(x - (top == -INFINITY ? 0.0f : top));
+  factor[tid] = empty ? -1.0f : by;
+  float sum = n * by;
+#pragma unroll
+  for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
+  if ((tid & 63) == 0) sums[wave] = sum;
+  __syncthreads();
+  sum = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kJoinBlock / 64; ++w) sum += sums[w];
+
+  const int side = tid / (kLatent / 4), at = tid % (kLatent / 4);
+  f32x4 o = {};
+#pragma unroll 4
+  for (int s = side; s < p.splits; s += kSides) {
+    const float f = factor[s];
+    if (f < 0.0f) continue;
+    o += *reinterpret_cast<const f32x4*>(p.part + (base + (int64_t)s * p.heads) * kLatent + at * 4) * f;
+  }
+  *reinterpret_cast<f32x4*>(half + tid * 4) = o;
+  __syncthreads();
+  if (side) return;
+#pragma unroll
+  for (int s = 1; s < kSides; ++s)
+    o += *reinterpret_cast<const f32x4*>(half + (s * (kLatent / 4) + at) * 4);
+  const float scale = sum == 0.0f ? 0.0f : 1.0f / sum;
+  *reinterpret_cast<u32x2*>(p.out + ((row * p.heads + head) * kLatent + at * 4) * 2) =
+      u32x2{T::pack(o[0] * scale, o[1] * scale), T::pack(o[2] * scale, o[3] * scale)};
+  if (p.lse && tid == 0) p.lse[row * p.heads + head] = (top + log2f(sum)) * kLn2;
 }
 
-// Heads a workgroup: 16, 32 or 64.
-int head_block(int32_t heads) { return heads <= 16 ? 16 : heads <= 32 ? 32 : 64; }
+// Heads a workgroup: 16, 32, 64 or 128.
+int head_block(int32_t heads) { return heads <= 16 ? 16 : heads <= 32 ? 32 : heads <= 64 ? 64 : 128; }
 
-// Workgroups that the chip runs at once (one per CU).
-constexpr int64_t kSlots = 256;
-
-// Parts of the token axis: enough workgroups for every CU, each with a
-// tile at least.
+// Parts of the token axis. Costs in tiles of one CU's time, which runs one
+// workgroup: a part costs its tiles and about kPart more (first loads, last
+// sums, the join). Rows as long as they may be go in rounds of 256
+// workgroups; rows of mixed lengths end with the longest row's parts, after
+// all rows' work has been shared out. The lengths are on the device, so the
+// rule weighs both, even rows twice.
 int32_t splits_for(int32_t rows, int32_t heads, int64_t tokens) {
-  const int64_t hb = head_block(heads);
-  const int64_t groups = (int64_t)rows * ((heads + hb - 1) / hb);
+  constexpr double kCus = 256, kPart = 3;
+  constexpr int kTry[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 24, 32, 48, 64, 96, 128, 192, 256};
+  const int hb = head_block(heads);
+  const double groups = (double)rows * ((heads + hb - 1) / hb);
   const int64_t tiles = (tokens + kTile - 1) / kTile;
-  int64_t s = groups > 0 ? kSlots / groups : 1;
-  if (s > tiles) s = tiles;
-  return (int32_t)(s < 1 ? 1 : s);
+  int32_t best = 1;
+  double least = 0;
+  for (const int s : kTry) {
+    if (s > 1 && s > tiles) break;
+    const double part = (double)((tiles + s - 1) / s) + kPart;
+    const double rounds = (double)(int64_t)((groups * s + kCus - 1) / kCus);
+    const double cost = 2 * rounds * part + part + groups * ((double)tiles + s * kPart) / kCus;
+    if (s == 1 || cost < least) {
+      best = s;
+      least = cost;
+    }
+  }
+  return best;
+}
+
+template <class T, class P, bool kPaged>
+int launch_plan(const AttendParams& p, void* stream) {
+  const dim3 grid((unsigned)((int64_t)p.rows * p.blocks * p.splits));
+  return launch(attend_kernel<T, P, kPaged>, grid, dim3(P::kBlock), p, stream);
 }
 
 template <class T, int kLatent, bool kPaged>
 int launch_attend(AttendParams p, void* stream) {
   const int hb = head_block(p.heads);
   p.blocks = (p.heads + hb - 1) / hb;
-  const dim3 grid((unsigned)((int64_t)p.rows * p.blocks * p.splits));
-  int st;
-  if (hb == 16)
-    st = launch(attend_kernel<T, 16, 1, 4, kLatent, kPaged>, grid, dim3(kBlock), p, stream);
-  else if (hb == 32)
-    st = launch(attend_kernel<T, 16, 2, 2, kLatent, kPaged>, grid, dim3(kBlock), p, stream);
-  else
-    st = launch(attend_kernel<T, 16, 4, 1, kLatent, kPaged>, grid, dim3(kBlock), p, stream);
+  const int st = hb == 16   ? launch_plan<T, Plan<1, 4, kLatent>, kPaged>(p, stream)
+                 : hb == 32 ? launch_plan<T, Plan<2, 4, kLatent>, kPaged>(p, stream)
+                 : hb == 64 ? launch_plan<T, Plan<4, 2, kLatent>, kPaged>(p, stream)
+                            : launch_plan<T, Plan<8, 1, kLatent>, kPaged>(p, stream);
   if (st != DSATOPK_OK || p.splits == 1) return st;
   return launch(join_kernel<T, kLatent>, dim3((unsigned)((int64_t)p.rows * p.heads)),
-                dim3(kLatent / 4), p, stream);
+                dim3(kJoinBlock), p, stream);
 }
 
 size_t part_floats(int32_t rows, int32_t heads, int32_t latent, int32_t splits) {

@@ -103,13 +103,25 @@ __device__ __forceinline__ u32x2 read_columns(const char* lds) {
   return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)lds));
 }
 
-// Where row t of an LDS tile keeps its 16-byte chunk c (rows of 16 chunks or
-// a multiple): chunk c ^ swizzle(t). Eight rows after each other have eight
-// different values modulo 8, so lanes that read one chunk of consecutive
-// rows use different banks; rows 4a .. 4a + 3 differ in bits 1 and 2, so
-// a column read's 4 rows x 2 chunks do as well.
-__device__ __forceinline__ constexpr int swizzle(int t) {
-  return ((t & 3) << 1) | ((t >> 2) & 1) | (t & 8);
+// Where row t of an LDS tile keeps its 16-byte chunk c: chunk c ^ swizzle of
+// t, so that no instruction's lanes share one of the 64 banks (256 bytes).
+// Each has 16 different values over 16 rows, for row reads (16 lanes: 16
+// rows, one chunk), and more than that for column reads:
+//   swizzle16: rows 8a .. 8a + 7 differ in bits 1 .. 3, for 32 lanes that
+//   read 8 rows x 2 chunks (products of 16 columns);
+//   swizzle32: rows 4a .. 4a + 3 differ in bits 2 and 3, for 32 lanes that
+//   read 4 rows x 4 chunks (products of 32 columns);
+//   swizzle8, for rows of 8 chunks: two rows fill the banks, and the 8 even
+//   and the 8 odd of 16 rows each have 8 different values.
+__device__ __forceinline__ constexpr int swizzle16(int t) { return ((t & 7) << 1) | ((t >> 3) & 1); }
+__device__ __forceinline__ constexpr int swizzle32(int t) { return ((t & 3) << 2) | ((t >> 2) & 3); }
+__device__ __forceinline__ constexpr int swizzle8(int t) { return (t >> 1) & 7; }
+
+// x, as a value that what follows is computed from anew: addresses made of
+// it take instructions in the loop instead of registers across it.
+__device__ __forceinline__ int here(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
 }
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
