@@ -16,8 +16,8 @@
 // the rounded weights are, register for register, the B operand of O' =
 // latent' P' (the order of tokens along that contraction is free, and is
 // taken as S' leaves it). O' has a head in each lane too: rescaling it is a
-// multiplication by the lane's own factor, done only where a row's maximum
-// grows by more than 2^8 over the one in use. The A operand of O' needs the
+// multiplication by the lane's own factor, done only where weights outgrow
+// the reference maximum in use by 2^8. The A operand of O' needs the
 // tile by columns; the LDS column reads give it from the same tile that the
 // rows were read from.
 //
@@ -42,7 +42,7 @@ namespace {
 constexpr int kTile = 64;  // tokens
 constexpr int kRope = 64;
 constexpr int kRopeBytes = kRope * 2;
-constexpr float kGrow = 8.0f;
+constexpr float kMost = 256.0f;  // of a lane's weights by a reference that is kept
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -94,34 +94,68 @@ __device__ __forceinline__ float head_sum(float x) {
   return x + __shfl_xor(x, 32);
 }
 
+// The chunk that a lane group takes in step i of the contraction over the
+// latent part (its order is free, as long as queries and keys share it).
+// 16-byte reads go through 16 lanes at a time, 8 of them from the next lane
+// group: rows 0-3 and 12-15 of one, rows 4-11 of the other. With chunks 2
+// apart in neighbouring groups swizzle16 keeps these on different banks too;
+// chunks 1 apart cost a second cycle for each.
+__device__ __forceinline__ constexpr int chunk_of(int i, int group) {
+  return 8 * (i >> 1) + 2 * group + (i & 1);
+}
+
+// A lane's places in a tile, in bytes, from which the others follow by
+// exclusive or: of the swizzled chunks that differ in bits of their number
+// only, within the row's first 256 bytes.
+template <class P>
+struct Places {
+  int copy;  // chunk of a copied vector, for the wave's token 0
+  int row;   // chunk of token lane % 16, for step 0 of the contraction
+  int rope;  // the same of its rotary part
+  int column;  // of the column reads of output block 0
+
+  __device__ __forceinline__ Places(int wave, int lane) {
+    const int col = lane & 15, group = lane >> 4;
+    const int first = wave * P::kCopy;
+    copy = P::kRow == 1024 ? (lane ^ swizzle16(first)) * 16
+                           : ((lane & 31) ^ swizzle16(first + (lane >> 5))) * 16;
+    row = col * P::kRow + ((chunk_of(0, group) ^ swizzle16(col)) << 4);
+    rope = kTile * P::kRow + col * kRopeBytes + ((group ^ swizzle8(col)) << 4);
+    // lane i of 16 points at row i / 4, 8 bytes i % 4 of a 4 x 32 byte block
+    const int tok = 4 * group + (col >> 2);
+    column = tok * P::kRow + ((((col & 3) >> 1) ^ swizzle16(tok)) << 4) + 8 * (col & 1);
+  }
+};
+
 // Copies the wave's P::kCopy tokens of a tile; `at` is the address of token
 // lane % P::kCopy of them.
 template <class P>
-__device__ __forceinline__ void copy_tokens(char* tile, uint64_t at, int wave, int lane) {
-  constexpr int kChunks = P::kRow / 16;
-  constexpr int kPer = 64 / kChunks;  // tokens a copy
-  lane = here(lane);
+__device__ __forceinline__ void copy_tokens(char* tile, uint64_t at, int place, int wave, int lane) {
+  constexpr int kPer = 1024 / P::kRow;  // tokens a copy
   const uint32_t lo = (uint32_t)at, hi = (uint32_t)(at >> 32);
   const int first = wave * P::kCopy;
 #pragma unroll
   for (int t = 0; t < P::kCopy; t += kPer) {
-    uint64_t base = ((uint64_t)__builtin_amdgcn_readlane(hi, t) << 32) |
-                    (uint32_t)__builtin_amdgcn_readlane(lo, t);
-    int chunk = lane ^ swizzle16(first + t);
+    // tokens t of 8 (16) on: swizzle16(first + t) is swizzle16(first) ^ swizzle16(t)
+    const uint32_t chunk = place ^ (swizzle16(t) * 16);
+    const uint64_t base = ((uint64_t)__builtin_amdgcn_readlane(hi, t) << 32) |
+                          (uint32_t)__builtin_amdgcn_readlane(lo, t);
+    char* to = tile + (first + t) * P::kRow;
     if constexpr (kPer == 2) {
       const uint64_t second = ((uint64_t)__builtin_amdgcn_readlane(hi, t + 1) << 32) |
                               (uint32_t)__builtin_amdgcn_readlane(lo, t + 1);
-      if (lane >= 32) base = second;
-      chunk = (lane & 31) ^ swizzle16(first + t + (lane >> 5));
+      copy_to_lds(reinterpret_cast<const char*>(lane < 32 ? base : second) + chunk, to);
+    } else {
+      copy_to_lds(reinterpret_cast<const char*>(base) + chunk, to);
     }
-    copy_to_lds(reinterpret_cast<const char*>(base) + chunk * 16, tile + (first + t) * P::kRow);
   }
 #pragma unroll
   for (int t = 0; t < P::kCopy; t += 8) {
     const int mine = t + (lane >> 3);
     const uint64_t base = ((uint64_t)(uint32_t)__shfl((int)hi, mine) << 32) |
                           (uint32_t)__shfl((int)lo, mine);
-    copy_to_lds(reinterpret_cast<const char*>(base) + P::kRow + ((lane & 7) ^ swizzle8(first + mine)) * 16,
+    const uint32_t chunk = ((lane & 7) ^ swizzle8(first + mine)) * 16;
+    copy_to_lds(reinterpret_cast<const char*>(base) + P::kRow + chunk,
                 tile + kTile * P::kRow + (first + t) * kRopeBytes);
   }
 }
@@ -140,17 +174,17 @@ struct State {
 template <class T, class P>
 __device__ __forceinline__ void attend_tokens(State<P>& st, const u32x4 (&q)[P::kSteps + P::kRopeSteps],
                                               const char* __restrict__ cur, char* __restrict__ next,
-                                              bool more, uint64_t next_at, int wave, int from,
-                                              uint64_t valid, int lane, float scale2) {
+                                              bool more, uint64_t next_at, const Places<P>& places,
+                                              int wave, int from, uint64_t valid, int lane,
+                                              float scale2) {
   constexpr int kGo = P::kGo;
-  if (more) copy_tokens<P>(next, next_at, wave, lane);
-  lane = here(lane);
-  const int col = lane & 15, group = lane >> 4;
+  if (more) copy_tokens<P>(next, next_at, here(places.copy), wave, here(lane));
+  const int group = lane >> 4;
   f32x4 s[kGo];
   {
-    const int swz = swizzle16(col);  // rows `from` on: `from` is a multiple of 16
-    const char* row = cur + (from + col) * P::kRow;
-    const char* rope = cur + kTile * P::kRow + (from + col) * kRopeBytes;
+    const int row = here(places.row), rope = here(places.rope);
+    const char* rows = cur + from * P::kRow;  // `from` is a multiple of 16: the swizzle starts over
+    const char* ropes = cur + from * kRopeBytes;
 #pragma unroll
     for (int x = 0; x < kGo; ++x) s[x] = f32x4{};
     // Reads go kAhead steps before the products that take them, and no
@@ -159,9 +193,9 @@ __device__ __forceinline__ void attend_tokens(State<P>& st, const u32x4 (&q)[P::
     auto read = [&](int i, int x) {
       if (i < P::kSteps)
         return *reinterpret_cast<const u32x4*>(
-            row + (((4 * (i & 3) + group) ^ swz) << 4) + (i >> 2) * 256 + x * 16 * P::kRow);
+            rows + (row ^ ((chunk_of(i, 0) & 15) << 4)) + (i >> 2) * 256 + x * 16 * P::kRow);
       return *reinterpret_cast<const u32x4*>(
-          rope + (((4 * (i - P::kSteps) + group) ^ swizzle8(col)) << 4) + x * 16 * kRopeBytes);
+          ropes + (rope ^ ((i - P::kSteps) << 6)) + x * 16 * kRopeBytes);
     };
     u32x4 a[kAhead][kGo];
 #pragma unroll
@@ -188,67 +222,74 @@ __device__ __forceinline__ void attend_tokens(State<P>& st, const u32x4 (&q)[P::
       for (int i = 0; i < 4; ++i)
         if (!((mine >> (x * 16 + i)) & 1)) s[x][i] = -INFINITY;
   }
-  float top = s[0][0];
+  const int column = here(places.column);
+  const char* columns = cur + from * P::kRow;
+  auto column_of = [&](int b) {
+    u32x4 v = {};
 #pragma unroll
-  for (int x = 0; x < kGo; ++x)
+    for (int x = 0; x < kGo; ++x) {
+      const u32x2 w = read_columns(columns + (column ^ ((b & 7) << 5)) + (b >> 3) * 256 + x * 16 * P::kRow);
+      v[2 * x] = w[0];
+      v[2 * x + 1] = w[1];
+    }
+    return v;
+  };
+
+  // The weights, by the reference maximum in use. It only has to be near
+  // enough: a lane's sum over kMost (or not a number) tells that it is not,
+  // as no row's maximum is looked for otherwise.
+  float w[kGo][4], sum;
+  auto weigh = [&]() {
+    const float ref = st.top == -INFINITY ? 0.0f : st.top;
+    sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) top = fmaxf(top, s[x][i]);
-  top = head_max(top) * scale2;
-  if (__any(top > st.top + kGrow)) {
-    const float to = fmaxf(st.top, top);
+    for (int x = 0; x < kGo; ++x)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        w[x][i] = exp2_fast(fmaf(s[x][i], scale2, -ref));
+        sum += w[x][i];
+      }
+  };
+  weigh();
+  if (__any(!(sum <= kMost) || st.top == -INFINITY)) {
+    float top = s[0][0];
+#pragma unroll
+    for (int x = 0; x < kGo; ++x)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = fmaxf(top, s[x][i]);
+    const float to = fmaxf(st.top, head_max(top) * scale2);
     const float by = st.top == -INFINITY ? 0.0f : exp2_fast(st.top - to);
     st.top = to;
     st.sum *= by;
 #pragma unroll
     for (int b = 0; b < P::kBlocks; ++b) st.o[b] *= by;
+    weigh();
   }
-  const float ref = st.top == -INFINITY ? 0.0f : st.top;
-#pragma unroll
-  for (int x = 0; x < kGo; ++x)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      s[x][i] = exp2_fast(fmaf(s[x][i], scale2, -ref));
-      st.sum += s[x][i];
-    }
+  st.sum += sum;
 
-  // sums: lane i of 16 points at row i / 4, 8 bytes i % 4 of a 4 x 32 byte block
-  const int in = lane & 15;
-  const int tok = 4 * group + (in >> 2);
-  const int swz = swizzle16(tok);
-  int at[8];
+  // The sums. kAhead is what the registers leave: one more block ahead spills,
+  // and a reload waits for every copy in flight (375 -> 480 us for 1024 rows
+  // of 2048 slots and 64 heads).
+  constexpr int kAhead = kGo == 1 ? 8 : 4;
+  u32x4 a[kAhead];
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    at[j] = (from + tok) * P::kRow + (((2 * j + ((in & 3) >> 1)) ^ swz) << 4) + 8 * (in & 1);
+  for (int b = 0; b < kAhead; ++b) a[b] = column_of(b);
   if constexpr (kGo == 1) {
-    const u32x2 w = {T::pack(s[0][0], s[0][1]), T::pack(s[0][2], s[0][3])};
-    constexpr int kAhead = 8;
-    u32x2 a[kAhead];
-    auto read = [&](int b) { return read_columns(cur + at[b & 7] + (b >> 3) * 256); };
-#pragma unroll
-    for (int b = 0; b < kAhead; ++b) a[b] = read(b);
+    const u32x2 v = {T::pack(w[0][0], w[0][1]), T::pack(w[0][2], w[0][3])};
 #pragma unroll
     for (int b = 0; b < P::kBlocks; ++b) {
       __builtin_amdgcn_sched_barrier(0);
-      st.o[b] = T::mma16_half(a[b % kAhead], w, st.o[b]);
-      if (b + kAhead < P::kBlocks) a[b % kAhead] = read(b + kAhead);
+      st.o[b] = T::mma16_half(u32x2{a[b % kAhead][0], a[b % kAhead][1]}, v, st.o[b]);
+      if (b + kAhead < P::kBlocks) a[b % kAhead] = column_of(b + kAhead);
     }
   } else {
-    const u32x4 w = {T::pack(s[0][0], s[0][1]), T::pack(s[0][2], s[0][3]),
-                     T::pack(s[1][0], s[1][1]), T::pack(s[1][2], s[1][3])};
-    constexpr int kAhead = 5;
-    u32x4 a[kAhead];
-    auto read = [&](int b) {
-      const u32x2 lo = read_columns(cur + at[b & 7] + (b >> 3) * 256);
-      const u32x2 hi = read_columns(cur + at[b & 7] + (b >> 3) * 256 + 16 * P::kRow);
-      return u32x4{lo[0], lo[1], hi[0], hi[1]};
-    };
-#pragma unroll
-    for (int b = 0; b < kAhead; ++b) a[b] = read(b);
+    const u32x4 v = {T::pack(w[0][0], w[0][1]), T::pack(w[0][2], w[0][3]),
+                     T::pack(w[1][0], w[1][1]), T::pack(w[1][2], w[1][3])};
 #pragma unroll
     for (int b = 0; b < P::kBlocks; ++b) {
       __builtin_amdgcn_sched_barrier(0);
-      st.o[b] = T::mma16(a[b % kAhead], w, st.o[b]);
-      if (b + kAhead < P::kBlocks) a[b % kAhead] = read(b + kAhead);
+      st.o[b] = T::mma16(a[b % kAhead], v, st.o[b]);
+      if (b + kAhead < P::kBlocks) a[b % kAhead] = column_of(b + kAhead);
     }
   }
 }
@@ -304,6 +345,7 @@ __global__ __launch_bounds__(P::kBlock) void attend_kernel(AttendParams p) {
   };
   auto bits_of = [&](bool there) { return (uint32_t)(__ballot(there) & ((1ull << P::kCopy) - 1)); };
 
+  const Places<P> places(wave, lane);
   State<P> st;
   st.top = -INFINITY;
   st.sum = 0.0f;
@@ -318,14 +360,14 @@ __global__ __launch_bounds__(P::kBlock) void attend_kernel(AttendParams p) {
     uint64_t at = address_of(first, entry, there);
     uint32_t mask = bits_of(there);
     if (!P::kOwn && lane == 0) masks[0][wave] = mask;
-    copy_tokens<P>(tiles, at, wave, lane);
+    copy_tokens<P>(tiles, at, places.copy, wave, lane);
     entry = entry_of(first + 1);
 
     u32x4 q[P::kSteps + P::kRopeSteps];
     const char* qh = head < p.heads ? p.q + row * p.q_row + head * p.q_head : zero_row();
 #pragma unroll
     for (int i = 0; i < P::kSteps + P::kRopeSteps; ++i)
-      q[i] = *reinterpret_cast<const u32x4*>(qh + (4 * i + group) * 16);
+      q[i] = *reinterpret_cast<const u32x4*>(qh + (i < P::kSteps ? chunk_of(i, group) : 4 * i + group) * 16);
 
     for (int32_t t = first; t < last; ++t) {
       const int buf = (t - first) & 1;
@@ -353,8 +395,8 @@ __global__ __launch_bounds__(P::kBlock) void attend_kernel(AttendParams p) {
 #pragma unroll 1
       for (int from = 0; from < P::kTokens; from += P::kGo * 16)
         attend_tokens<T, P>(st, q, tiles + buf * P::kBuffer, tiles + (buf ^ 1) * P::kBuffer,
-                            more && from == 0, at, wave, wt * P::kTokens + from, valid >> from, lane,
-                            p.scale2);
+                            more && from == 0, at, places, wave, wt * P::kTokens + from, valid >> from,
+                            lane, p.scale2);
     }
   }
 
