@@ -307,222 +307,6 @@ class PageMaps(NamedTuple):
     counts: "torch.Tensor"        # int32 [2]: tokens, pages opened
 
 
-def _table(page_table, like, name="page_table"):
-    import torch
-
-    if page_table.dtype != torch.int32:
-        raise ValueError(f"{name} must be int32")
-    if page_table.dim() != 2 or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
-        raise ValueError(f"{name} must be [rows, width] with contiguous columns")
-    if not page_table.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
-    if like is not None:
-        _on(page_table, like, name)
-    return page_table
-
-
-def _row_stride(t):
-    """Elements between t's rows (at least a row: what one row's stride says does not matter)."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
-
-
-def _stride(t, dim):
-    """t's stride; 0 where one entry makes it meaningless."""
-    return t.stride(dim) if t.shape[dim] > 1 else 0
-
-
-def page_maps(seq_lens, page_table, page_size: int, free_pages, num_tokens: int, new_lens=None,
-              out=None, stream=None):
-    """The pages, slots and top-k row arguments of a serving step.
-
-    Requests of ``seq_lens`` tokens after the step, ``new_lens`` of them new
-    (None: one each), take the pages that they lack from ``free_pages``:
-    these are written into ``page_table`` in place. Returns ``PageMaps``,
-    whose ``slots``, ``table_rows`` and ``row_lens`` have ``num_tokens`` rows
-    (empty ones behind the step's tokens). ``out``: a ``PageMaps`` to write
-    into."""
-    import torch
-
-    n, t = int(seq_lens.shape[0]), int(num_tokens)
-    _vec_i32(seq_lens, n, "seq_lens")
-    _vec_i32(new_lens, n, "new_lens", seq_lens)
-    _table(page_table, seq_lens)
-    if page_table.shape[0] != n:
-        raise ValueError("page_table must have one row per request")
-    _vec_i32(free_pages, int(free_pages.shape[0]), "free_pages", seq_lens)
-    if t < 0:
-        raise ValueError("num_tokens must not be negative")
-    if out is None:
-        sizes = (n + 1, t, t, t, 2)
-        # one allocation, its parts at 16-byte boundaries
-        whole = torch.empty(sum((s + 3) // 4 * 4 for s in sizes), dtype=torch.int32,
-                            device=seq_lens.device)
-        parts, at = [], 0
-        for s in sizes:
-            parts.append(whole[at:at + s])
-            at += (s + 3) // 4 * 4
-        out = PageMaps(*parts)
-    else:
-        for name, size in zip(PageMaps._fields, (n + 1, t, t, t, 2)):
-            _vec_i32(getattr(out, name), size, name, seq_lens)
-    st = _lib().dsatopk_page_maps(
-        _ptr(seq_lens), _ptr(new_lens), n, _ptr(page_table), _row_stride(page_table),
-        page_table.shape[1], int(page_size), _ptr(free_pages), free_pages.shape[0], t,
-        *(_ptr(getattr(out, name)) for name in ("token_starts", "slots", "table_rows", "row_lens",
-                                                "counts")), _stream(stream))
-    if st != 0:
-        raise DsatopkError(st, "dsatopk_page_maps")
-    return out
-
-
-def _element_type(t, name, fp8=False):
-    """The library's number for t's element type."""
-    import torch
-
-    types = {torch.bfloat16: 0, torch.float16: 1}
-    if fp8:
-        types[torch.float8_e4m3fn] = 2
-    if t.dtype not in types:
-        raise ValueError(f"{name} must be one of {', '.join(str(d) for d in types)}")
-    return types[t.dtype]
-
-
-def _tensor(t, dims, like, name):
-    """A device tensor of ``dims`` dimensions with a contiguous last one."""
-    if t.dim() != dims or (t.shape[-1] > 1 and t.stride(-1) != 1):
-        raise ValueError(f"{name} must have {dims} dimensions, the last one contiguous")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
-    if like is not None:
-        _on(t, like, name)
-    return t
-
-
-def _score_args(q, weights, keys, key_scales, key_dims):
-    import torch
-
-    _tensor(q, 3, None, "q")
-    rows, heads, dim = q.shape
-    _tensor(weights, 2, q, "weights")
-    if weights.dtype != torch.float32 or tuple(weights.shape) != (rows, heads):
-        raise ValueError(f"weights must be float32 of shape ({rows}, {heads})")
-    _tensor(keys, key_dims, q, "keys")
-    kind = _element_type(q, "q", fp8=True)
-    if keys.dtype != q.dtype or keys.shape[-1] != dim:
-        raise ValueError("keys must have q's type and head dimension")
-    if key_scales is not None:
-        _tensor(key_scales, key_dims - 1, q, "key_scales")
-        if key_scales.dtype != torch.float32 or key_scales.shape != keys.shape[:-1]:
-            raise ValueError("key_scales must be float32, one per key")
-    return kind, int(rows), int(heads), int(dim)
-
-
-def _score_out(out, rows, columns, like):
-    import torch
-
-    if out is None:
-        # a top-k's score buffer: row stride a multiple of 4
-        return torch.empty((rows, max(4, (columns + 3) // 4 * 4)), dtype=torch.float32,
-                           device=like.device)
-    _tensor(out, 2, like, "out")
-    if out.dtype != torch.float32 or out.shape[0] != rows:
-        raise ValueError(f"out must be float32 with {rows} rows")
-    return out
-
-
-def scores_paged(q, weights, keys, seq_lens, page_table, key_scales=None, table_rows=None,
-                 out=None, stream=None):
-    """Indexer scores over a paged key cache, as ``paged`` reads them.
-
-    ``q`` [rows, heads, dim] and ``keys`` [pages, page_size, dim] in
-    bfloat16, float16 or float8_e4m3fn, ``weights`` float32 [rows, heads],
-    ``key_scales`` float32 [pages, page_size] or None. Column j < seq_len of
-    row b of ``out`` gets key_scale[j] * sum_h weights[b, h] * max(0, q[b, h]
-    . key[j]); other columns are not written. Returns ``out`` (allocated with
-    a column per table position when None)."""
-    kind, rows, heads, dim = _score_args(q, weights, keys, key_scales, 3)
-    _vec_i32(seq_lens, rows, "seq_lens", q)
-    _vec_i32(table_rows, rows, "table_rows", q)
-    _table(page_table, q)
-    if table_rows is None and page_table.shape[0] != rows:
-        raise ValueError("page_table must have one row per query row without table_rows")
-    page_size = int(keys.shape[1])
-    out = _score_out(out, rows, page_table.shape[1] * page_size, q)
-    st = _lib().dsatopk_scores_paged(
-        _ptr(q), _stride(q, 0), _stride(q, 1), _ptr(weights), _stride(weights, 0), _ptr(keys),
-        keys.shape[0], _stride(keys, 0), _stride(keys, 1), _ptr(key_scales),
-        0 if key_scales is None else _stride(key_scales, 0), kind, heads, dim, _ptr(seq_lens),
-        _ptr(page_table), _row_stride(page_table), page_table.shape[1], page_size,
-        _ptr(table_rows), rows, _ptr(out), _row_stride(out), out.shape[1], _stream(stream))
-    if st != 0:
-        raise DsatopkError(st, "dsatopk_scores_paged")
-    return out
-
-
-def scores_ragged(q, weights, keys, seq_lens, row_starts, key_scales=None, out=None,
-                  stream=None):
-    """Indexer scores over flattened keys [tokens, dim], as ``ragged`` reads
-    them: row b's window is columns row_starts[b] .. row_starts[b] +
-    seq_lens[b] - 1 of ``out``; other columns are not written. Arguments as
-    for ``scores_paged``, ``key_scales`` float32 [tokens]."""
-    kind, rows, heads, dim = _score_args(q, weights, keys, key_scales, 2)
-    _vec_i32(seq_lens, rows, "seq_lens", q)
-    _vec_i32(row_starts, rows, "row_starts", q)
-    if row_starts is None:
-        raise ValueError("row_starts is required")
-    out = _score_out(out, rows, keys.shape[0], q)
-    st = _lib().dsatopk_scores_ragged(
-        _ptr(q), _stride(q, 0), _stride(q, 1), _ptr(weights), _stride(weights, 0), _ptr(keys),
-        keys.shape[0], _stride(keys, 0), _ptr(key_scales), kind, heads, dim, _ptr(seq_lens),
-        _ptr(row_starts), rows, _ptr(out), _row_stride(out), out.shape[1], _stream(stream))
-    if st != 0:
-        raise DsatopkError(st, "dsatopk_scores_ragged")
-    return out
-
-
-def _attend_out(out, lse, q, shape):
-    """Attention's results: out (q's type) of ``shape``, lse (float32) of its first two."""
-    import torch
-
-    if out is None:
-        out = torch.empty(shape, dtype=q.dtype, device=q.device)
-    elif out.dtype != q.dtype or tuple(out.shape) != shape or not out.is_contiguous():
-        raise ValueError(f"out must be a contiguous {q.dtype} tensor of shape {shape}")
-    else:
-        _on(out, q, "out")
-    if lse is None:
-        lse = torch.empty(shape[:2], dtype=torch.float32, device=q.device)
-    elif lse.dtype != torch.float32 or tuple(lse.shape) != shape[:2] or not lse.is_contiguous():
-        raise ValueError(f"lse must be a contiguous float32 tensor of shape {shape[:2]}")
-    else:
-        _on(lse, q, "lse")
-    return out, lse
-
-
-def _attend_args(q, cache, latent_dim, out, lse, workspace, max_tokens):
-    import torch
-
-    _tensor(q, 3, None, "q")
-    _tensor(cache, 3, q, "cache")
-    rows, heads, dim = q.shape
-    kind = _element_type(q, "q")
-    if cache.dtype != q.dtype or cache.shape[-1] != dim:
-        raise ValueError("cache must have q's type and last dimension")
-    out, lse = _attend_out(out, lse, q, (rows, heads, int(latent_dim)))
-    if workspace is None:
-        need = attend_bytes(rows, heads, latent_dim, max_tokens)
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous uint8 tensor")
-    else:
-        _on(workspace, q, "workspace")
-    head = (_ptr(q), _stride(q, 0), _stride(q, 1), _ptr(cache), cache.shape[0], _stride(cache, 0),
-            _stride(cache, 1), cache.shape[1], kind, heads, int(latent_dim), dim - int(latent_dim))
-    tail = (_ptr(out), _ptr(lse), _ptr(workspace), 0 if workspace is None else workspace.numel())
-    return out, lse, rows, head, tail
-
-
 def attend_bytes(num_rows: int, num_heads: int, latent_dim: int, max_tokens: int) -> int:
     """Workspace bytes of ``attend_selected`` (max_tokens: k) and
     ``attend_paged`` (max_tokens: max_seq_len)."""
@@ -530,87 +314,20 @@ def attend_bytes(num_rows: int, num_heads: int, latent_dim: int, max_tokens: int
                                            int(max_tokens)))
 
 
-def attend_selected(q, cache, slots, latent_dim: int, scale: float, out=None, lse=None,
-                    workspace=None, stream=None):
-    """Absorbed latent attention over selected cache slots.
-
-    ``q`` [rows, heads, latent_dim + 64] and ``cache`` [pages, page_size,
-    latent_dim + 64] in bfloat16 or float16; ``slots`` int32 [rows, k] as
-    ``paged`` returns them (-1: none). Returns ``(out, lse)``: q's type
-    [rows, heads, latent_dim], and float32 [rows, heads]. ``workspace``: uint8
-    of ``attend_bytes(rows, heads, latent_dim, k)`` (allocated when None)."""
-    import torch
-
-    _tensor(slots, 2, q, "slots")
-    if slots.dtype != torch.int32 or slots.shape[0] != q.shape[0]:
-        raise ValueError("slots must be int32 with one row per query row")
-    k = int(slots.shape[1])
-    out, lse, rows, head, tail = _attend_args(q, cache, latent_dim, out, lse, workspace, k)
-    st = _lib().dsatopk_attend_selected(*head, float(scale), _ptr(slots), _row_stride(slots), k,
-                                        rows, *tail, _stream(stream))
-    if st != 0:
-        raise DsatopkError(st, "dsatopk_attend_selected")
-    return out, lse
+# The serving operators' calls (csrc/serve_binding.cpp), loaded at first use.
+_SERVE = ("page_maps", "scores_paged", "scores_ragged", "attend_selected", "attend_paged",
+          "attend_expanded")
 
 
-def attend_paged(q, cache, seq_lens, page_table, latent_dim: int, scale: float, table_rows=None,
-                 max_seq_len=None, out=None, lse=None, workspace=None, stream=None):
-    """Absorbed latent attention over the first ``seq_lens`` positions of each
-    row's page table. Arguments as for ``attend_selected`` and ``paged``;
-    ``max_seq_len`` bounds ``seq_lens`` (the table's width when None) and
-    sets how rows are split."""
-    _tensor(q, 3, None, "q")
-    n = int(q.shape[0])
-    _vec_i32(seq_lens, n, "seq_lens", q)
-    _vec_i32(table_rows, n, "table_rows", q)
-    _table(page_table, q)
-    if table_rows is None and page_table.shape[0] != n:
-        raise ValueError("page_table must have one row per query row without table_rows")
-    _tensor(cache, 3, q, "cache")
-    if max_seq_len is None:
-        max_seq_len = page_table.shape[1] * cache.shape[1]
-    out, lse, rows, head, tail = _attend_args(q, cache, latent_dim, out, lse, workspace,
-                                              int(max_seq_len))
-    st = _lib().dsatopk_attend_paged(*head, float(scale), _ptr(seq_lens), _ptr(page_table),
-                                     _row_stride(page_table), page_table.shape[1],
-                                     _ptr(table_rows), int(max_seq_len), rows, *tail,
-                                     _stream(stream))
-    if st != 0:
-        raise DsatopkError(st, "dsatopk_attend_paged")
-    return out, lse
-
-
-def attend_expanded(q, k, v, k_rope, q_starts, k_starts, max_queries: int, scale: float,
-                    causal: bool = True, out=None, lse=None, stream=None):
-    """Expanded latent attention over a ragged batch of prompts.
-
-    ``q`` [queries, heads, 192], ``k`` and ``v`` [keys, heads, 128] and
-    ``k_rope`` [keys, 64] in bfloat16 or float16 (k and v may be parts of one
-    tensor); ``q_starts`` and ``k_starts`` int32 [requests + 1];
-    ``max_queries`` bounds a request's queries, which are its last tokens.
-    Returns ``(out, lse)``: q's type [queries, heads, 128], and float32
-    [queries, heads]."""
-    _tensor(q, 3, None, "q")
-    queries, heads, dim = q.shape
-    kind = _element_type(q, "q")
-    for name, t, dims in (("k", k, 3), ("v", v, 3), ("k_rope", k_rope, 2)):
-        _tensor(t, dims, q, name)
-        if t.dtype != q.dtype or t.shape[0] != k.shape[0] or (dims == 3 and t.shape[1] != heads):
-            raise ValueError(f"{name} must have q's type, k's rows and q's heads")
-    if dim != k.shape[2] + k_rope.shape[1]:
-        raise ValueError("q's last dimension must be k's and k_rope's together")
-    n = int(q_starts.shape[0]) - 1
-    if n < 0:
-        raise ValueError("q_starts must have an entry more than there are requests")
-    _vec_i32(q_starts, n + 1, "q_starts", q)
-    _vec_i32(k_starts, n + 1, "k_starts", q)
-    out, lse = _attend_out(out, lse, q, (queries, heads, int(v.shape[2])))
-    st = _lib().dsatopk_attend_expanded(
-        _ptr(q), _stride(q, 0), _stride(q, 1), _ptr(k), _stride(k, 0), _stride(k, 1), _ptr(v),
-        _stride(v, 0), _stride(v, 1), _ptr(k_rope), _stride(k_rope, 0), kind, heads, k.shape[2],
-        k_rope.shape[1], v.shape[2], float(scale), int(bool(causal)), _ptr(q_starts),
-        _ptr(k_starts), n, queries, k.shape[0], int(max_queries), _ptr(out), _ptr(lse),
-        _stream(stream))
-    if st != 0:
-        raise DsatopkError(st, "dsatopk_attend_expanded")
-    return out, lse
+def __getattr__(name):
+    if name not in _SERVE:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    _lib()  # torch's HIP runtime, then the library that the calls are linked to
+    try:
+        from . import _serve
+    except ImportError as e:
+        raise ImportError(f"{e}: run row_top_selection_amd.build.build()") from e
+    _serve.setup(DsatopkError, PageMaps)
+    for n in _SERVE:
+        globals()[n] = getattr(_serve, n)
+    return globals()[name]

@@ -1,8 +1,10 @@
-"""Ahead-of-time build of libdsatopk.so for gfx950 with hipcc (in-tree)."""
+"""Ahead-of-time build of libdsatopk.so for gfx950 with hipcc, and of the
+serving operators' Python calls with g++ (both in-tree)."""
 from __future__ import annotations
 
 import os
 import subprocess
+import sysconfig
 import tempfile
 from concurrent.futures import ThreadPoolExecutor
 from pathlib import Path
@@ -15,6 +17,8 @@ SOURCES = [PKG / "csrc" / name for name in (
 HEADERS = [PKG / "csrc" / "select_device.h", PKG / "csrc" / "serve_common.h",
            ROOT / "include" / "dsatopk.h"]
 LIB = PKG / "libdsatopk.so"
+EXT_SOURCE = PKG / "csrc" / "serve_binding.cpp"
+EXT = PKG / ("_serve" + sysconfig.get_config_var("EXT_SUFFIX"))
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 # -packed-fp32-ops: keep the compiler from forming packed fp32 instructions.
@@ -30,14 +34,33 @@ def _run(cmd, verbose):
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
-        raise RuntimeError(f"hipcc failed ({res.returncode}):\n{res.stderr}")
+        raise RuntimeError(f"{cmd[0]} failed ({res.returncode}):\n{res.stderr}")
+
+
+def _build_ext(verbose):
+    """The extension module, against the torch that is installed."""
+    from torch.utils import cpp_extension
+
+    tmp = EXT.with_suffix(".so.tmp%d" % os.getpid())
+    rocm = Path(HIPCC).resolve().parents[1]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__",
+           "-DUSE_ROCM", "-I", str(ROOT / "include")]
+    for path in (*cpp_extension.include_paths(), str(rocm / "include"),
+                 sysconfig.get_paths()["include"]):
+        cmd += ["-isystem", path]
+    cmd += [str(EXT_SOURCE), "-o", str(tmp), "-L", str(PKG), "-ldsatopk", "-Wl,-rpath,$ORIGIN"]
+    for path in cpp_extension.library_paths():
+        cmd += ["-L", path]
+    cmd += ["-ltorch_python", "-ltorch_hip", "-ltorch_cpu", "-lc10_hip", "-lc10", "-lamdhip64"]
+    _run(cmd, verbose)
+    os.replace(tmp, EXT)
 
 
 def build(force: bool = True, verbose: bool = False) -> Path:
     """Compile every HIP source into ``libdsatopk.so`` next to this file
-    (the sources side by side, then one link)."""
-    newest = max(p.stat().st_mtime for p in SOURCES + HEADERS)
-    if not force and LIB.exists() and LIB.stat().st_mtime >= newest:
+    (the sources side by side, then one link), and the extension module."""
+    newest = max(p.stat().st_mtime for p in [*SOURCES, *HEADERS, EXT_SOURCE])
+    if not force and all(p.exists() and p.stat().st_mtime >= newest for p in (LIB, EXT)):
         return LIB
     tmp = LIB.with_suffix(".so.tmp%d" % os.getpid())
     with tempfile.TemporaryDirectory() as d:
@@ -48,6 +71,7 @@ def build(force: bool = True, verbose: bool = False) -> Path:
         _run([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *map(str, objects), "-o",
               str(tmp)], verbose)
     os.replace(tmp, LIB)
+    _build_ext(verbose)
     return LIB
 
 

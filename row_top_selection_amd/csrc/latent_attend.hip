@@ -653,12 +653,11 @@ int dsatopk_attend_selected(const void* q, int64_t q_row_stride, int64_t q_head_
                             int32_t num_rows, void* out, float* lse, void* workspace,
                             size_t workspace_bytes, void* stream) {
   AttendParams p{};
-  if (k < 0 || slot_stride < k) return DSATOPK_ERR_INVALID_ARG;
+  if (k < 0 || slot_stride < k || (num_rows > 0 && k && !slots)) return DSATOPK_ERR_INVALID_ARG;
   const int st = check_attend(p, q, q_row_stride, q_head_stride, cache, num_pages, page_stride,
                               token_stride, page_size, type, num_heads, latent_dim, rope_dim,
                               scale, num_rows, k, out, lse, workspace, workspace_bytes);
   if (st != DSATOPK_OK || num_rows == 0) return st;
-  if (k && !slots) return DSATOPK_ERR_INVALID_ARG;
   p.slots = slots;
   p.slot_stride = slot_stride;
   p.selected = k;
@@ -675,13 +674,13 @@ int dsatopk_attend_paged(const void* q, int64_t q_row_stride, int64_t q_head_str
                          void* out, float* lse, void* workspace, size_t workspace_bytes,
                          void* stream) {
   AttendParams p{};
-  if (page_table_width < 1 || page_table_stride < page_table_width)
+  if (page_table_width < 1 || page_table_stride < page_table_width ||
+      (num_rows > 0 && (!seq_lens || !page_table)))
     return DSATOPK_ERR_INVALID_ARG;
   const int st = check_attend(p, q, q_row_stride, q_head_stride, cache, num_pages, page_stride,
                               token_stride, page_size, type, num_heads, latent_dim, rope_dim,
                               scale, num_rows, max_seq_len, out, lse, workspace, workspace_bytes);
   if (st != DSATOPK_OK || num_rows == 0) return st;
-  if (!seq_lens || !page_table) return DSATOPK_ERR_INVALID_ARG;
   p.seq_lens = seq_lens;
   p.table = page_table;
   p.table_stride = page_table_stride;
