@@ -60,7 +60,6 @@ struct Shape {
   static constexpr int kBytes = kDim * 2;         // of a head in LDS
   static constexpr int kChunks = kBytes / 16;
   static constexpr int kSteps = kDim / 16;        // products over the dimension
-  static constexpr int kWords = kDim / 4;         // a lane's of one key: half of it
   // The chunk that lane half `half` takes in product s. Keys of bytes come 16
   // (two chunks) at a load.
   static __device__ __forceinline__ constexpr int chunk(int s, int half) {
@@ -92,15 +91,16 @@ __device__ __forceinline__ constexpr int swizzle_of(int head) {
 
 // Row r's heads into LDS, swizzled; heads that the row does not have are
 // zeros.
-template <int kBytes>
+template <int kBytes, int kHeads>
 __device__ __forceinline__ void copy_heads(const ScoreParams& p, int32_t r, int wave, int lane,
                                            char* lds) {
   constexpr int kChunks = kBytes / 16;
   constexpr int kCopyRows = 1024 / kBytes;  // heads a wave copies at once
   const char* q = p.q + r * p.q_row;
   const int sub = lane / kChunks, c = lane % kChunks;
-  for (int h = wave * kCopyRows; h < ((p.heads + 31) & ~31); h += kCopyRows * (kBlock / 64)) {
-    const int hh = h + sub;
+#pragma unroll
+  for (int i = 0; i < kHeads / kCopyRows / (kBlock / 64); ++i) {
+    const int h = (i * (kBlock / 64) + wave) * kCopyRows, hh = h + sub;
     const char* src = hh < p.heads ? q + hh * p.q_head : zero_row();
     copy_to_lds(src + (c ^ swizzle_of<kChunks>(hh)) * 16, lds + h * kBytes);
   }
@@ -128,7 +128,7 @@ struct ByteHeads {
 #pragma unroll
     for (int g = 0; g < kGoes; ++g) {
       const int h = g * kStep + tid / kPieces, c = (tid % kPieces) * 2;
-      if (h >= ((p.heads + 31) & ~31)) break;
+      if (kStep * kGoes > kHeads && h >= kHeads) break;
       uint32_t w[8];
       widen(piece[g], w);
 #pragma unroll
@@ -142,37 +142,41 @@ struct ByteHeads {
 // One row's sums over its heads (of this lane's half of each 32) for the
 // wave's 2 x 32 tokens, while the next row's heads are copied: the two
 // buffers are told apart so that no read of one waits for the other's copy.
-template <int kKind, int kDim>
+// 32 heads at a time: with 64 the weighting of the first could go on beside
+// the products of the second, but three waves a SIMD do better at that than
+// two with 64 more registers (886 against 922 us for 4 x 1024 rows of 64
+// heads over 16384 keys each).
+template <int kKind, int kDim, int kHeads>
 __device__ __forceinline__ void row_sums(const ScoreParams& p, const char* __restrict__ heads,
                                          const float* __restrict__ weights,
                                          char* __restrict__ next, int32_t next_row, int wave,
-                                         int lane, const uint32_t (&key)[2][Shape<kKind, kDim>::kWords],
+                                         int lane, const u32x4 (&key)[2][Shape<kKind, kDim>::kSteps],
                                          float (&sum)[2]) {
   using S = Shape<kKind, kDim>;
   if (kKind != DSATOPK_FP8 && next_row >= 0)
-    copy_heads<S::kBytes>(p, next_row, wave, lane, next);
+    copy_heads<S::kBytes, kHeads>(p, next_row, wave, lane, next);
+  lane = here(lane);
   const int half = lane >> 5, col = lane & 31;
-  const int slabs = (p.heads + 31) >> 5;
-  for (int slab = 0; slab < slabs; ++slab) {
+  // chunk(s, half) ^ swizzle is chunk(s, 0) ^ (chunk(0, half) ^ swizzle)
+  const int first = col * S::kBytes + ((S::chunk(0, half) ^ swizzle_of<S::kChunks>(col)) << 4);
+#pragma unroll 1
+  for (int slab = 0; slab < kHeads / 32; ++slab) {
     f32x16 acc[2] = {};
-    const int head = slab * 32 + col;
-    const char* row = heads + head * S::kBytes;
 #pragma unroll
     for (int s = 0; s < S::kSteps; ++s) {
-      const u32x4 a = *reinterpret_cast<const u32x4*>(
-          row + ((S::chunk(s, half) ^ swizzle_of<S::kChunks>(head)) << 4));
+      const u32x4 a = *reinterpret_cast<const u32x4*>(heads + slab * 32 * S::kBytes +
+                                                      (first ^ (S::chunk(s, 0) << 4)));
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
-        acc[n] = product<kKind>(a, u32x4{key[n][4 * s], key[n][4 * s + 1], key[n][4 * s + 2], key[n][4 * s + 3]}, acc[n]);
+      for (int n = 0; n < 2; ++n) acc[n] = product<kKind>(a, key[n][s], acc[n]);
     }
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const f32x4 w = *reinterpret_cast<const f32x4*>(&weights[slab * 32 + 8 * g + 4 * half]);
+    for (int x = 0; x < 4; ++x) {
+      const f32x4 w = *reinterpret_cast<const f32x4*>(&weights[slab * 32 + 8 * x + 4 * half]);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int n = 0; n < 2; ++n)
-          sum[n] = fmaf(w[i], __builtin_elementwise_maximum(acc[n][4 * g + i], 0.0f), sum[n]);
+          sum[n] = fmaf(w[i], __builtin_elementwise_maximum(acc[n][4 * x + i], 0.0f), sum[n]);
     }
   }
 }
@@ -184,37 +188,35 @@ __global__ __launch_bounds__(kBlock, 2) void scores_kernel(ScoreParams p) {
   __shared__ __attribute__((aligned(1024))) char heads_lds[2][kHeads * kBytes];
   __shared__ __attribute__((aligned(16))) float w_lds[2][kHeads];
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int half = lane >> 5, col = lane & 31;
   const int32_t j0 = (int32_t)blockIdx.x * kTile;
-  const int32_t r0 = (int32_t)blockIdx.y * p.group;
-  const int32_t r1 = min(r0 + p.group, p.rows);
-  const int slabs = (p.heads + 31) >> 5;
+  const int64_t r64 = ((int64_t)blockIdx.z * gridDim.y + blockIdx.y) * p.group;
+  if (r64 >= p.rows) return;
+  const int32_t r0 = (int32_t)r64;
+  const int32_t r1 = (int32_t)min(r64 + p.group, (int64_t)p.rows);
   const int32_t jw = j0 + wave * kWaveTokens;
 
-  // A row's window in columns, as [lo, hi).
-  auto window = [&](int32_t r, int32_t& lo, int32_t& hi) {
-    lo = kPaged ? 0 : p.row_starts[r];
-    const int64_t end = (int64_t)lo + max(p.seq_lens[r], 0);
-    hi = (int32_t)min(end, (int64_t)p.columns);
-    if (lo < 0) lo = 0;
-  };
-  // The next row from r whose window meets this workgroup's tokens.
-  auto next_row = [&](int32_t r) {
-    for (; r < r1; ++r) {
-      int32_t lo, hi;
-      window(r, lo, hi);
-      if (lo < j0 + kTile && hi > j0 && hi > lo) break;
-    }
-    return r;
-  };
-  // A row's weights into buffer `buf`, zeros for heads that it does not have.
-  auto copy_weights = [&](int32_t r, int buf) {
-    if (tid < slabs * 32)
-      w_lds[buf][tid] = tid < p.heads ? p.weights[r * p.w_row + tid] : 0.0f;
-  };
+  // Lane i has row r0 + i's window in columns, as [lo, hi); the rows whose
+  // windows meet this workgroup's tokens are a bit each.
+  int32_t lo = 0, hi = 0, from = 0;
+  if (r0 + lane < r1) {
+    const int32_t r = r0 + lane;
+    if constexpr (kPaged)
+      from = p.table_rows ? p.table_rows[r] : r;
+    else
+      lo = p.row_starts[r];
+    hi = (int32_t)min((int64_t)lo + max(p.seq_lens[r], 0), (int64_t)p.columns);
+    lo = max(lo, 0);
+  }
+  uint64_t todo = __ballot(lo < j0 + kTile && hi > j0 && hi > lo);
+  if (todo == 0) return;
 
-  uint32_t key[2][S::kWords];
+  // This thread's weight of a row, 0 for heads that it does not have.
+  auto weight_of = [&](int32_t r) { return tid < p.heads ? p.weights[r * p.w_row + tid] : 0.0f; };
+
+  u32x4 key[2][S::kSteps];
   float scale[2] = {1.0f, 1.0f};
   auto load_keys = [&](int64_t table_row) {
 #pragma unroll
@@ -237,59 +239,58 @@ __global__ __launch_bounds__(kBlock, 2) void scores_kernel(ScoreParams p) {
 #pragma unroll
         for (int s = 0; s < kDim / 32; ++s) {
           uint32_t w[8];
-          widen(*reinterpret_cast<const u32x4*>(src + (2 * s + half) * 16), w);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) key[n][8 * s + i] = w[i];
+          widen(load16(src + (2 * s + half) * 16), w);
+          key[n][2 * s] = u32x4{w[0], w[1], w[2], w[3]};
+          key[n][2 * s + 1] = u32x4{w[4], w[5], w[6], w[7]};
         }
       } else {
 #pragma unroll
-        for (int s = 0; s < S::kSteps; ++s) {
-          const u32x4 v = *reinterpret_cast<const u32x4*>(src + S::chunk(s, half) * 16);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) key[n][4 * s + i] = v[i];
-        }
+        for (int s = 0; s < S::kSteps; ++s) key[n][s] = load16(src + S::chunk(s, half) * 16);
       }
     }
   };
 
-  int32_t r = next_row(r0);
-  if (r >= r1) return;
+  int at = __builtin_ctzll(todo);
+  todo &= todo - 1;
   int buf = 0;
-  int64_t have = -1;
+  int32_t have = -1;
   ByteHeads<kDim, kHeads> bytes;
   if constexpr (kKind == DSATOPK_FP8) {
-    bytes.load(p, r, tid);
+    bytes.load(p, r0 + at, tid);
     bytes.store(p, heads_lds[0], tid);
   } else {
-    copy_heads<kBytes>(p, r, wave, lane, heads_lds[0]);
+    copy_heads<kBytes, kHeads>(p, r0 + at, wave, lane, heads_lds[0]);
   }
-  copy_weights(r, 0);
-  while (r < r1) {
+  if (tid < kHeads) w_lds[0][tid] = weight_of(r0 + at);
+  if constexpr (!kPaged) load_keys(0);
+  for (;;) {
     if constexpr (kPaged) {
-      const int64_t want = p.table_rows ? p.table_rows[r] : r;
+      const int32_t want = __builtin_amdgcn_readlane(from, at);
       if (want != have) load_keys(have = want);
-    } else if (have < 0) {
-      load_keys(have = 0);
     }
-    const int32_t rn = next_row(r + 1);
-    copies_barrier();  // row r's heads are there, the other buffer is free
-    if (rn < r1) {
-      copy_weights(rn, buf ^ 1);
-      if constexpr (kKind == DSATOPK_FP8) bytes.load(p, rn, tid);
+    const int next = todo ? __builtin_ctzll(todo) : -1;
+    todo &= todo - 1;
+    copies_barrier();  // the row's heads are there, the other buffer is free
+    float weight = 0.0f;
+    if (next >= 0) {
+      weight = weight_of(r0 + next);
+      if constexpr (kKind == DSATOPK_FP8) bytes.load(p, r0 + next, tid);
     }
     float sum[2] = {0.0f, 0.0f};
-    row_sums<kKind, kDim>(p, heads_lds[buf], w_lds[buf], heads_lds[buf ^ 1], rn < r1 ? rn : -1,
-                          wave, lane, key, sum);
-    if constexpr (kKind == DSATOPK_FP8)
-      if (rn < r1) bytes.store(p, heads_lds[buf ^ 1], tid);
+    row_sums<kKind, kDim, kHeads>(p, heads_lds[buf], w_lds[buf], heads_lds[buf ^ 1],
+                                  next >= 0 ? r0 + next : -1, wave, lane, key, sum);
+    if (next >= 0) {
+      if constexpr (kKind == DSATOPK_FP8) bytes.store(p, heads_lds[buf ^ 1], tid);
+      if (tid < kHeads) w_lds[buf ^ 1][tid] = weight;
+    }
     // both halves' heads; then lane l keeps token l of the wave's 64
     const float t0 = (sum[0] + other_half(sum[0])) * scale[0];
     const float t1 = (sum[1] + other_half(sum[1])) * scale[1];
-    int32_t lo, hi;
-    window(r, lo, hi);
     const int32_t j = jw + lane;
-    if (j >= lo && j < hi) p.out[r * p.out_stride + j] = half ? t1 : t0;
-    r = rn;
+    if (j >= __builtin_amdgcn_readlane(lo, at) && j < __builtin_amdgcn_readlane(hi, at))
+      p.out[(r0 + at) * p.out_stride + j] = half ? t1 : t0;
+    if (next < 0) break;
+    at = next;
     buf ^= 1;
   }
 }
@@ -300,28 +301,25 @@ int launch_heads(const ScoreParams& p, bool paged, dim3 grid, void* stream) {
                : launch(scores_kernel<kKind, kDim, kHeads, false>, grid, dim3(kBlock), p, stream);
 }
 
-// Room for 64 heads leaves LDS for twice the workgroups of room for 128.
 template <int kKind, int kDim>
 int launch_scores(const ScoreParams& p, bool paged, dim3 grid, void* stream) {
-  return p.heads <= 64 ? launch_heads<kKind, kDim, 64>(p, paged, grid, stream)
-                       : launch_heads<kKind, kDim, kMaxHeads>(p, paged, grid, stream);
+  return p.heads <= 32   ? launch_heads<kKind, kDim, 32>(p, paged, grid, stream)
+         : p.heads <= 64 ? launch_heads<kKind, kDim, 64>(p, paged, grid, stream)
+                         : launch_heads<kKind, kDim, kMaxHeads>(p, paged, grid, stream);
 }
 
 int run_scores(ScoreParams p, int32_t type, int32_t dim, bool paged, void* stream) {
   const int64_t tiles = ((int64_t)p.columns + kTile - 1) / kTile;
   if (tiles == 0) return DSATOPK_OK;
   // Rows a workgroup: enough workgroups to fill the card come first, then
-  // keys read for as many rows as possible.
-  constexpr int64_t kEnough = 2048;
+  // keys read for as many rows as possible, up to a lane for each.
+  constexpr int64_t kEnough = 2048, kMostY = 65535;
   int64_t group = p.rows * tiles / kEnough;
   group = group < 1 ? 1 : group > 64 ? 64 : group;
-  int64_t groups = (p.rows + group - 1) / group;
-  if (groups > 65535) {
-    group = (p.rows + 65534) / 65535;
-    groups = (p.rows + group - 1) / group;
-  }
+  const int64_t groups = (p.rows + group - 1) / group;
   p.group = (int32_t)group;
-  const dim3 grid((unsigned)tiles, (unsigned)groups);
+  const dim3 grid((unsigned)tiles, (unsigned)(groups < kMostY ? groups : kMostY),
+                  (unsigned)((groups + kMostY - 1) / kMostY));
   switch (type * 2 + (dim == 128)) {
     case 0: return launch_scores<0, 64>(p, paged, grid, stream);
     case 1: return launch_scores<0, 128>(p, paged, grid, stream);

@@ -367,7 +367,7 @@ __global__ __launch_bounds__(P::kBlock) void attend_kernel(AttendParams p) {
     const char* qh = head < p.heads ? p.q + row * p.q_row + head * p.q_head : zero_row();
 #pragma unroll
     for (int i = 0; i < P::kSteps + P::kRopeSteps; ++i)
-      q[i] = *reinterpret_cast<const u32x4*>(qh + (i < P::kSteps ? chunk_of(i, group) : 4 * i + group) * 16);
+      q[i] = load16(qh + (i < P::kSteps ? chunk_of(i, group) : 4 * i + group) * 16);
 
     for (int32_t t = first; t < last; ++t) {
       const int buf = (t - first) & 1;

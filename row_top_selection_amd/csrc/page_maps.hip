@@ -10,9 +10,9 @@
 // token with q % p == 0 is the only one that opens its page, so it writes
 // the table entry; nobody reads an entry that the call writes.
 //
-// One launch: every workgroup takes kTokens tokens and computes the running
-// sums over the requests itself, kRequests at a time in LDS, up to those of
-// its tokens. A second launch that waited for shared sums would cost more
+// One launch: every workgroup takes kTokens tokens, kPer consecutive ones a
+// thread, and computes the running sums over the requests itself, kRequests
+// at a time in LDS, up to those of its tokens. A second launch that waited for shared sums would cost more
 // than the lengths' re-reading from L2 (8 bytes a request and workgroup).
 
 #include "serve_common.h"
@@ -37,7 +37,19 @@ struct MapParams {
   int32_t* table_rows;
   int32_t* row_lens;
   int32_t* counts;
+  bool wide;  // 16-byte stores fit slots, table_rows and row_lens
 };
+
+// Four consecutive tokens' values, those from `n` on left out.
+__device__ __forceinline__ void store4(int32_t* to, const int32_t (&v)[kPer], int n, bool wide) {
+  if (wide && n == kPer) {
+    *reinterpret_cast<int4*>(to) = int4{v[0], v[1], v[2], v[3]};
+  } else {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (j < n) to[j] = v[j];
+  }
+}
 
 // Inclusive sums over a wave's lanes.
 __device__ __forceinline__ int32_t wave_sum(int32_t v) {
@@ -53,6 +65,7 @@ __device__ __forceinline__ int32_t wave_sum(int32_t v) {
 __global__ __launch_bounds__(kBlock) void page_maps_kernel(MapParams p) {
   __shared__ int32_t start[kRequests + 1];  // first token of each request of the pass
   __shared__ int32_t first[kRequests];      // first free page of each
+  __shared__ int32_t before[kRequests];     // tokens that each held
   __shared__ int32_t sums[2][kBlock / 64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int32_t t0 = (int32_t)blockIdx.x * kTokens;
@@ -62,17 +75,18 @@ __global__ __launch_bounds__(kBlock) void page_maps_kernel(MapParams p) {
   int32_t tokens = 0, pages = 0;       // of the passes so far
 
   for (int32_t r0 = 0; r0 < p.requests; r0 += kRequests) {
-    int32_t nw[kPer], pg[kPer], n = 0, g = 0;
+    int32_t nw[kPer], pg[kPer], had[kPer], n = 0, g = 0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const int32_t r = r0 + tid * kPer + j;
-      nw[j] = pg[j] = 0;
+      nw[j] = pg[j] = had[j] = 0;
       if (r < p.requests) {
         const int32_t len = max(p.seq_lens[r], 0);
         nw[j] = p.new_lens ? min(max(p.new_lens[r], 0), len) : min(1, len);
+        had[j] = len - nw[j];
         // pages up to the end, less those up to the last held token
         pg[j] = (int32_t)(((int64_t)len + page - 1) >> p.page_bits) -
-                (int32_t)(((int64_t)len - nw[j] + page - 1) >> p.page_bits);
+                (int32_t)(((int64_t)had[j] + page - 1) >> p.page_bits);
       }
       n += nw[j];
       g += pg[j];
@@ -98,6 +112,7 @@ __global__ __launch_bounds__(kBlock) void page_maps_kernel(MapParams p) {
     for (int j = 0; j < kPer; ++j) {
       start[tid * kPer + j] = nb;
       first[tid * kPer + j] = gb;
+      before[tid * kPer + j] = had[j];
       const int32_t r = r0 + tid * kPer + j;
       if (leads && r < p.requests) p.token_starts[r] = nb;
       nb += nw[j];
@@ -106,38 +121,51 @@ __global__ __launch_bounds__(kBlock) void page_maps_kernel(MapParams p) {
     if (tid == 0) start[kRequests] = tokens;
     __syncthreads();
 
-    // this workgroup's tokens of these requests
-    const int32_t a = max(t0, start[0]), b = min(t1, tokens);
-    for (int32_t t = a + tid; t < b; t += kBlock) {
-      int lo = 0, hi = kRequests;  // start[lo] <= t < start[hi]
+    // This thread's tokens of these requests: a search for the first one's
+    // request, steps from there for the others.
+    const int32_t a = max(t0 + tid * kPer, start[0]);
+    const int32_t b = min(min(t0 + (tid + 1) * kPer, t1), tokens);
+    if (a < b) {
+      int lo = 0, hi = kRequests;  // start[lo] <= a < start[hi]
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (start[mid] <= t)
+        if (start[mid] <= a)
           lo = mid;
         else
           hi = mid;
       }
-      const int32_t r = r0 + lo;
-      const int32_t len = max(p.seq_lens[r], 0);
-      const int32_t fresh = p.new_lens ? min(max(p.new_lens[r], 0), len) : min(1, len);
-      const int32_t pos = len - fresh + (t - start[lo]);
-      const int32_t held = (int32_t)(((int64_t)len - fresh + page - 1) >> p.page_bits);
-      const int32_t at = pos >> p.page_bits;
-      int32_t entry = -1;
-      if (at < p.width) {
-        int32_t* e = p.table + r * p.table_stride + at;
+      int32_t slot[kPer], row[kPer], pos[kPer], entry[kPer];
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        entry[j] = -1;
+        if (a + j >= b) continue;
+        while (start[lo + 1] <= a + j) ++lo;
+        row[j] = r0 + lo;
+        pos[j] = before[lo] + (a + j - start[lo]);
+        const int32_t held = (int32_t)(((int64_t)before[lo] + page - 1) >> p.page_bits);
+        const int32_t at = pos[j] >> p.page_bits;
+        if (at >= p.width) continue;
         if (at < held) {
-          entry = *e;
+          entry[j] = p.table[row[j] * p.table_stride + at];
         } else {
           const int64_t f = (int64_t)first[lo] + (at - held);
-          if (f < p.num_free) entry = p.free_pages[f];
-          if ((pos & (page - 1)) == 0) *e = entry;
+          if (f < p.num_free) entry[j] = p.free_pages[f];
         }
       }
-      const int64_t slot = ((int64_t)entry << p.page_bits) + (pos & (page - 1));
-      p.slots[t] = entry < 0 || slot > INT32_MAX ? -1 : (int32_t)slot;
-      p.table_rows[t] = r;
-      p.row_lens[t] = pos + 1;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        if (a + j >= b) continue;
+        const int32_t in = pos[j] & (page - 1);
+        const int32_t at = pos[j] >> p.page_bits;
+        if (in == 0 && at < p.width) p.table[row[j] * p.table_stride + at] = entry[j];
+        const int64_t full = ((int64_t)entry[j] << p.page_bits) + in;
+        slot[j] = entry[j] < 0 || full > INT32_MAX ? -1 : (int32_t)full;
+        ++pos[j];
+      }
+      const bool wide = p.wide && (a & 3) == 0;
+      store4(p.slots + a, slot, b - a, wide);
+      store4(p.table_rows + a, row, b - a, wide);
+      store4(p.row_lens + a, pos, b - a, wide);
     }
     if (!leads && tokens >= t1) return;
     __syncthreads();
@@ -189,6 +217,7 @@ extern "C" int dsatopk_page_maps(const int32_t* seq_lens, const int32_t* new_len
   p.table_rows = table_rows;
   p.row_lens = row_lens;
   p.counts = counts;
+  p.wide = aligned16(slots) && aligned16(table_rows) && aligned16(row_lens);
   const int64_t groups = ((int64_t)num_tokens + kTokens - 1) / kTokens;
   return launch(page_maps_kernel, dim3((unsigned)(groups < 1 ? 1 : groups)), dim3(kBlock), p,
                 stream);

@@ -84,6 +84,12 @@ __device__ __forceinline__ void copy_to_lds(const void* global, char* lds) {
   __builtin_amdgcn_global_load_lds((global_u32*)(uintptr_t)global, (lds_u32*)lds, 16, 0, 0);
 }
 
+// 16 bytes from memory (said to be memory: a pointer that may come from
+// either of two places would otherwise be loaded as one that may be LDS).
+__device__ __forceinline__ u32x4 load16(const char* global) {
+  return *reinterpret_cast<const __attribute__((address_space(1))) u32x4*>((uintptr_t)global);
+}
+
 // Until every load and copy of this wave has arrived.
 __device__ __forceinline__ void wait_copies() {
   __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt 0, the other counters unbounded
