@@ -306,7 +306,7 @@ int dsatopk_paged_noalloc(const float* scores, int64_t score_stride, const int32
  *                 in order.
  *   page_size     power of two in [1, 2^20].
  *   free_pages    int32 [num_free].
- *   num_tokens    rows of the outputs below. A step of fewer tokens leaves
+ *   num_tokens    rows of the outputs below, at most 2^30. A step of fewer tokens leaves
  *                 empty rows behind them; tokens past num_tokens get neither
  *                 a row nor a page.
  *
@@ -474,8 +474,8 @@ int dsatopk_attend_paged(const void* q, int64_t q_row_stride, int64_t q_head_str
  *   k             type [num_keys, num_heads, nope_dim]
  *   v             type [num_keys, num_heads, value_dim]
  *   k_rope        type [num_keys, rope_dim]
- *                 (each with its row and head strides; k and v may be parts
- *                 of one tensor)
+ *                 (each with its row and head strides, those of keys and
+ *                 values at most 2^27; k and v may be parts of one tensor)
  *   type          DSATOPK_BF16 or DSATOPK_FP16.
  *   num_heads     1 .. 1024; nope_dim 128, rope_dim 64, value_dim 128.
  *   scale         finite and above 0.

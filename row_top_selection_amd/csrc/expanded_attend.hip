@@ -10,12 +10,15 @@
 // last query sees all). The rotary key is one for all heads: it is
 // read from its own tensor instead of being copied into every head's key.
 //
-// A workgroup takes kRows queries of one head and goes over the keys, kTile
-// at a time, copied to LDS one tile ahead. Both products are transposed: S' = K
-// Q' has a query in each lane and keys in its registers, which are, rounded,
-// the B operand of O' = V' P'; V's columns come from LDS column reads. See
-// latent_attend.hip, whose tile is the same but for its sharing one tensor.
-// Queries stay in registers throughout.
+// A workgroup of 4 or 8 waves takes 32 queries a wave of one head and goes
+// over the keys, 8 a wave at a time, through a ring of tiles in LDS. Both
+// products are transposed: S' = K Q' has a query in each lane and keys in its
+// registers, which are, rounded, the B operand of O' = V' P'; V's columns
+// come from LDS column reads. Queries stay in registers throughout.
+//
+// The scores of 32 keys are computed beside the softmax of the 32 before
+// them, one product between every few other instructions, so that the matrix
+// units work while exponentials are taken.
 //
 // Weights are rounded to the inputs' type for the second product; scores,
 // maxima, sums and accumulators are fp32.
@@ -25,19 +28,28 @@
 namespace dsatopk_serve {
 namespace {
 
-constexpr int kBlock = 256;
-constexpr int kWaves = kBlock / 64;
-constexpr int kRows = 32 * kWaves;
-constexpr int kTile = 64;
+constexpr int kKeys = 32;  // taken at once
 constexpr int kNope = 128, kRope = 64, kValue = 128;
 constexpr int kKeyBytes = kNope * 2, kRopeBytes = kRope * 2, kValueBytes = kValue * 2;
-constexpr int kRopeAt = kTile * kKeyBytes, kValueAt = kRopeAt + kTile * kRopeBytes;
-constexpr int kBuffer = kValueAt + kTile * kValueBytes;
 constexpr int kSteps = (kNope + kRope) / 16;
 constexpr int kBlocks = kValue / 32;
-constexpr float kGrow = 8.0f;
+constexpr float kMost = 256.0f;  // of a lane's weights by a reference that is kept
+constexpr int64_t kMostStride = int64_t(1) << 27;  // of a key, in elements: 8 of them are 2^31 bytes
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+
+// Eight waves share what four would each copy for themselves (a workgroup a
+// CU, tiles of 64 keys); four leave room for a second workgroup, and suit
+// short and few prompts.
+template <int kWaves_>
+struct Shape {
+  static constexpr int kWaves = kWaves_, kBlock = kWaves * 64, kRows = kWaves * 32;
+  static constexpr int kTile = kWaves * 8;
+  static constexpr int kRing = kWaves == 4 ? 4 : 3;  // tiles in LDS: kRing - 1 ahead
+  static constexpr int kRopeAt = kTile * kKeyBytes;
+  static constexpr int kValueAt = kRopeAt + kTile * kRopeBytes;
+  static constexpr int kBuffer = kValueAt + kTile * kValueBytes;
+};
 
 struct ExpandParams {
   const char* q;
@@ -56,25 +68,66 @@ struct ExpandParams {
   float* lse;
 };
 
-// Copies keys j0 .. j0 + 63 (of the request's `keys`; rows past them repeat
-// the last) of all three tensors, swizzled: a wave takes 16.
+// A lane's places in a tile and in its copies, in bytes; the others follow
+// by exclusive or of the chunk numbers' bits.
+template <class S>
+struct Places {
+  uint32_t k, v, rope;  // offset of the lane's row of 4 (8) in a copy
+  int chunk, tail;      // its chunk there, of k and v and of the rotary part
+  int row, rope_row;    // of key lane % 32, step 0 of the contraction
+  int column;           // of the column reads of output block 0
+
+  __device__ __forceinline__ Places(const ExpandParams& p, int lane) {
+    const int col = lane & 31, half = lane >> 5;
+    k = (lane >> 4) * (uint32_t)p.k_row;
+    v = (lane >> 4) * (uint32_t)p.v_row;
+    rope = (lane >> 3) * (uint32_t)p.rope_row;
+    chunk = ((lane & 15) ^ swizzle32(lane >> 4)) * 16;
+    tail = ((lane & 7) ^ swizzle8(lane >> 3)) * 16;
+    row = col * kKeyBytes + ((half ^ swizzle32(col)) << 4);
+    rope_row = S::kRopeAt + col * kRopeBytes + ((half ^ swizzle8(col)) << 4);
+    // lane i of 16 points at row i / 4, 8 bytes i % 4 of a 4 x 32 byte block
+    const int in = lane & 15, side = (lane >> 4) & 1, tok = 4 * half + (in >> 2);
+    column = S::kValueAt + tok * kValueBytes + (((2 * side + ((in & 3) >> 1)) ^ swizzle32(tok)) << 4) +
+             8 * (in & 1);
+  }
+};
+
+constexpr int kCopies = 5;  // a wave's of a tile
+
+// Copies keys j0 .. j0 + kTile - 1 (of the request's `keys`; rows past them repeat
+// the last) of all three tensors, swizzled: a wave takes 8.
+template <class S>
 __device__ __forceinline__ void copy_tile(const ExpandParams& p, char* tile, const char* k,
                                           const char* v, const char* rope, int32_t j0,
-                                          int32_t keys, int wave, int lane) {
+                                          int32_t keys, const Places<S>& at, int wave, int lane) {
+  const int t0 = wave * 8;
+  char* rope_to = tile + S::kRopeAt + t0 * kRopeBytes;
+  if (j0 + S::kTile <= keys) {
+    // whole: a uniform address and the lane's offset
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int t = wave * 16 + i * 4 + (lane >> 4);
-    const int64_t j = min(j0 + t, keys - 1);
-    const int at = ((lane & 15) ^ swizzle32(t)) * 16;
-    copy_to_lds(k + j * p.k_row + at, tile + (wave * 16 + i * 4) * kKeyBytes);
-    copy_to_lds(v + j * p.v_row + at, tile + kValueAt + (wave * 16 + i * 4) * kValueBytes);
-  }
+    for (int i = 0; i < 2; ++i) {
+      const int64_t j = j0 + t0 + i * 4;
+      const uint32_t c = at.chunk ^ (swizzle32(t0 + i * 4) * 16);
+      copy_to_lds(k + j * p.k_row + (at.k + c), tile + (t0 + i * 4) * kKeyBytes);
+      copy_to_lds(v + j * p.v_row + (at.v + c), tile + S::kValueAt + (t0 + i * 4) * kValueBytes);
+    }
+    copy_to_lds(rope + (int64_t)(j0 + t0) * p.rope_row +
+                    (at.rope + (uint32_t)(at.tail ^ (swizzle8(t0) * 16))),
+                rope_to);
+  } else {
+    lane = here(lane);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int t = wave * 16 + i * 8 + (lane >> 3);
+    for (int i = 0; i < 2; ++i) {
+      const int t = t0 + i * 4 + (lane >> 4);
+      const int64_t j = min(j0 + t, keys - 1);
+      const int c = ((lane & 15) ^ swizzle32(t)) * 16;
+      copy_to_lds(k + j * p.k_row + c, tile + (t0 + i * 4) * kKeyBytes);
+      copy_to_lds(v + j * p.v_row + c, tile + S::kValueAt + (t0 + i * 4) * kValueBytes);
+    }
+    const int t = t0 + (lane >> 3);
     const int64_t j = min(j0 + t, keys - 1);
-    copy_to_lds(rope + j * p.rope_row + ((lane & 7) ^ swizzle8(t)) * 16,
-                tile + kRopeAt + (wave * 16 + i * 8) * kRopeBytes);
+    copy_to_lds(rope + j * p.rope_row + ((lane & 7) ^ swizzle8(t)) * 16, rope_to);
   }
 }
 
@@ -83,91 +136,129 @@ struct State {
   float top, sum;
 };
 
-// One tile of 64 keys for the wave's 32 queries, and first the next tile's
-// copies. `seen`: how many of the tile's keys this lane's query sees (may be
-// negative or above 64); `whole`: all of them, for every lane of the wave.
-template <class T>
-__device__ __forceinline__ void tile_step(const ExpandParams& p, State& st,
-                                          const u32x4 (&q)[kSteps], const char* __restrict__ cur,
-                                          char* __restrict__ next, const char* k, const char* v,
-                                          const char* rope, int32_t next_j, int32_t keys,
-                                          int32_t seen, bool whole, int wave, int lane) {
-  if (next_j < keys) copy_tile(p, next, k, v, rope, next_j, keys, wave, lane);
-  const int col = lane & 31, half = lane >> 5;
-  f32x16 s[2] = {};
-  {
-    const int swz = swizzle32(col);
-    const char* row = cur + col * kKeyBytes;
-    const char* tail = cur + kRopeAt + col * kRopeBytes;
+// Weight i of scores s by the reference maximum `ref` (log2).
+__device__ __forceinline__ float weight_of(const f32x16& s, int i, float scale2, float ref) {
+  return exp2_fast(fmaf(s[i], scale2, -ref));
+}
+
+// The scores of the 32 keys `part` of a tile for the wave's 32 queries, and beside them
+// the weights of `s` (if there is one), a few after each product. Reads go
+// kAhead steps before their products. The order is kept as written: left
+// alone, the compiler puts each read right before its product, waits for it
+// there, and takes the weights after all products.
+template <class T, class S>
+__device__ __forceinline__ f32x16 scores_of(const char* tile, int part, const u32x4 (&q)[kSteps],
+                                            const Places<S>& places, const f32x16* s, float scale2,
+                                            float ref, f32x16* w, float* sum) {
+  constexpr int kAhead = 4;
+  const int row = here(places.row), rope_row = here(places.rope_row);
+  auto read = [&](int i) {
+    return *reinterpret_cast<const u32x4*>(
+        i < kNope / 16 ? tile + part * kKeys * kKeyBytes + (row ^ (i << 5))
+                       : tile + part * kKeys * kRopeBytes + (rope_row ^ ((i - kNope / 16) << 5)));
+  };
+  u32x4 a[kAhead];
 #pragma unroll
-    for (int i = 0; i < kNope / 16; ++i)
+  for (int i = 0; i < kAhead; ++i) a[i] = read(i);
+  f32x16 next = {};
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
-        s[x] = T::mma32(*reinterpret_cast<const u32x4*>(row + (((2 * i + half) ^ swz) << 4) + x * 32 * kKeyBytes),
-                        q[i], s[x]);
+  for (int i = 0; i < kSteps; ++i) {
+    __builtin_amdgcn_sched_barrier(0);
+    next = T::mma32(a[i % kAhead], q[i], next);
+    if (i + kAhead < kSteps) a[i % kAhead] = read(i + kAhead);
+    if (s) {
 #pragma unroll
-    for (int i = 0; i < kRope / 16; ++i)
-#pragma unroll
-      for (int x = 0; x < 2; ++x)
-        s[x] = T::mma32(*reinterpret_cast<const u32x4*>(tail + (((2 * i + half) ^ swizzle8(col)) << 4) + x * 32 * kRopeBytes),
-                        q[kNope / 16 + i], s[x]);
+      for (int e = 16 * i / kSteps; e < 16 * (i + 1) / kSteps; ++e) {
+        (*w)[e] = weight_of(*s, e, scale2, ref);
+        *sum += (*w)[e];
+      }
+    }
   }
+  __builtin_amdgcn_sched_barrier(0);
+  return next;
+}
+
+// 32 keys: the weights of their scores `s` and their part of the sums, and
+// the scores of the 32 after them (`after`) in their place. First, if `copy`,
+// the copies of the tile at key copy_j. The tiles are told apart so that no
+// read of one waits for the copies of another. `seen`: how many of the 32 keys
+// this lane's query sees (may be negative or above 32); `whole`: all of them, for
+// every lane of the wave.
+template <class T, class S>
+__device__ __forceinline__ void keys_step(const ExpandParams& p, State& st, f32x16& s,
+                                          const u32x4 (&q)[kSteps], const char* __restrict__ cur,
+                                          int part, const char* __restrict__ after, int after_part,
+                                          char* __restrict__ copy_to, const char* k,
+                                          const char* v, const char* rope, bool copy, int32_t copy_j,
+                                          int32_t keys, int32_t seen, bool whole,
+                                          const Places<S>& places, int wave, int lane) {
+  if (copy) copy_tile<S>(p, copy_to, k, v, rope, copy_j, keys, places, wave, lane);
+  const int half = lane >> 5;
   if (!whole) {
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (x * 32 + 8 * (i / 4) + 4 * half + i % 4 >= seen) s[x][i] = -INFINITY;
+    for (int i = 0; i < 16; ++i)
+      if (8 * (i / 4) + 4 * half + i % 4 >= seen) s[i] = -INFINITY;
   }
-  float top = s[0][0];
+  // The weights are taken by the reference maximum in use, which only has to
+  // be near enough: a lane's sum over kMost (or not a number) tells that it
+  // is not, and the scores' maximum is looked for.
+  f32x16 w;
+  float sum = 0.0f;
+  const f32x16 next = scores_of<T, S>(after, after_part, q, places, &s, p.scale2,
+                                      st.top == -INFINITY ? 0.0f : st.top, &w, &sum);
+  if (__any(!(sum <= kMost) || st.top == -INFINITY)) {
+    float top = s[0];
 #pragma unroll
-  for (int x = 0; x < 2; ++x)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) top = fmaxf(top, s[x][i]);
-  top = fmaxf(top, other_half(top)) * p.scale2;
-  if (__any(top > st.top + kGrow)) {
-    const float to = fmaxf(st.top, top);
+    for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
+    const float to = fmaxf(st.top, fmaxf(top, other_half(top)) * p.scale2);
     const float by = st.top == -INFINITY ? 0.0f : exp2_fast(st.top - to);
     st.top = to;
     st.sum *= by;
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b) st.o[b] *= by;
-  }
-  const float ref = st.top == -INFINITY ? 0.0f : st.top;
-#pragma unroll
-  for (int x = 0; x < 2; ++x)
+    sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      s[x][i] = exp2_fast(fmaf(s[x][i], p.scale2, -ref));
-      st.sum += s[x][i];
+      w[i] = weight_of(s, i, p.scale2, to == -INFINITY ? 0.0f : to);
+      sum += w[i];
     }
-  // lane i of 16 points at row i / 4, 8 bytes i % 4 of a 4 x 32 byte block
-  const int in = lane & 15, side = (lane >> 4) & 1;
-  const int tok = 4 * half + (in >> 2);
-  const int swz = swizzle32(tok);
-  int at[4];
+  }
+  st.sum += sum;
+  s = next;
+
+  const int column = here(places.column);
+  // Step n: block n % kBlocks of 16 keys' share, n / kBlocks of 2. Reads go
+  // kAhead steps before their products.
+  constexpr int kAll = 2 * kBlocks, kAhead = 5;
+  auto read = [&](int n) {
+    const int b = n % kBlocks;
+    const char* rows = cur + part * kKeys * kValueBytes + (n / kBlocks) * 16 * kValueBytes;
+    const u32x2 lo = read_columns(rows + (column ^ (b << 6)));
+    // swizzle32(t + 8) = swizzle32(t) ^ 2
+    const u32x2 hi = read_columns(rows + (column ^ (b << 6) ^ 32) + 8 * kValueBytes);
+    return u32x4{lo[0], lo[1], hi[0], hi[1]};
+  };
+  u32x4 a[kAhead];
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    at[j] = tok * kValueBytes + (((4 * j + 2 * side + ((in & 3) >> 1)) ^ swz) << 4) + 8 * (in & 1);
+  for (int n = 0; n < kAhead; ++n) a[n] = read(n);
 #pragma unroll
-  for (int x = 0; x < 2; ++x)
+  for (int g = 0; g < 2; ++g) {
+    const u32x4 y = {T::pack(w[8 * g], w[8 * g + 1]), T::pack(w[8 * g + 2], w[8 * g + 3]),
+                     T::pack(w[8 * g + 4], w[8 * g + 5]), T::pack(w[8 * g + 6], w[8 * g + 7])};
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      const u32x4 w = {T::pack(s[x][8 * g], s[x][8 * g + 1]), T::pack(s[x][8 * g + 2], s[x][8 * g + 3]),
-                       T::pack(s[x][8 * g + 4], s[x][8 * g + 5]), T::pack(s[x][8 * g + 6], s[x][8 * g + 7])};
-      const char* rows = cur + kValueAt + (x * 32 + g * 16) * kValueBytes;
-#pragma unroll
-      for (int b = 0; b < kBlocks; ++b) {
-        const u32x2 lo = read_columns(rows + at[b]);
-        const u32x2 hi = read_columns(rows + (at[b] ^ 32) + 8 * kValueBytes);  // swizzle32(t + 8) = swizzle32(t) ^ 2
-        st.o[b] = T::mma32(u32x4{lo[0], lo[1], hi[0], hi[1]}, w, st.o[b]);
-      }
+    for (int b = 0; b < kBlocks; ++b) {
+      const int n = g * kBlocks + b;
+      __builtin_amdgcn_sched_barrier(0);
+      st.o[b] = T::mma32(a[n % kAhead], y, st.o[b]);
+      if (n + kAhead < kAll) a[n % kAhead] = read(n + kAhead);
     }
+  }
 }
 
-template <class T>
-__global__ __launch_bounds__(kBlock, 2) void expand_kernel(ExpandParams p) {
-  __shared__ __attribute__((aligned(1024))) char tiles[2 * kBuffer];
+template <class T, class S>
+__global__ __launch_bounds__(S::kBlock, 2) void expand_kernel(ExpandParams p) {
+  constexpr int kRows = S::kRows, kTile = S::kTile, kRing = S::kRing, kBuffer = S::kBuffer;
+  __shared__ __attribute__((aligned(1024))) char tiles[kRing * kBuffer];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 31, half = lane >> 5;
@@ -201,7 +292,7 @@ __global__ __launch_bounds__(kBlock, 2) void expand_kernel(ExpandParams p) {
   u32x4 q[kSteps];
   const char* qh = p.q + at * p.q_row + head * p.q_head;
 #pragma unroll
-  for (int i = 0; i < kSteps; ++i) q[i] = *reinterpret_cast<const u32x4*>(qh + (2 * i + half) * 16);
+  for (int i = 0; i < kSteps; ++i) q[i] = load16(qh + (2 * i + half) * 16);
 
   State st;
   st.top = -INFINITY;
@@ -212,13 +303,39 @@ __global__ __launch_bounds__(kBlock, 2) void expand_kernel(ExpandParams p) {
   const char* k = p.k + k0 * p.k_row + head * p.k_head;
   const char* v = p.v + k0 * p.v_row + head * p.v_head;
   const char* rope = p.rope + k0 * p.rope_row;
-  if (most > 0) copy_tile(p, tiles, k, v, rope, 0, keys, wave, lane);
-  int buf = 0;
-  for (int32_t j = 0; j < most; j += kTile) {
+  const Places<S> places(p, lane);
+  if (most > 0) {
+    constexpr int kAheadTiles = kRing - 1, kParts = kTile / kKeys;
+#pragma unroll
+    for (int n = 0; n < kAheadTiles; ++n)
+      if (n * kTile < most)
+        copy_tile<S>(p, tiles + n * kBuffer, k, v, rope, n * kTile, keys, places, wave, lane);
     copies_barrier();
-    tile_step<T>(p, st, q, tiles + buf * kBuffer, tiles + (buf ^ 1) * kBuffer, k, v, rope,
-                 j + kTile < most ? j + kTile : keys, keys, mine - j, least >= j + kTile, wave, lane);
-    buf ^= 1;
+    f32x16 s = scores_of<T, S>(tiles, 0, q, places, nullptr, 0.0f, 0.0f, nullptr, nullptr);
+    int n = 0;
+    for (int32_t j0 = 0; j0 < most; j0 += kTile, ++n) {
+#pragma unroll
+      for (int part = 0; part < kParts; ++part) {
+        const bool last = part + 1 == kParts;
+        if (last) {
+          // Tile n + 1 has arrived (later ones may be under way, unless they
+          // are the last), and all waves are done with tile n - 1, whose
+          // place is the next copy's.
+          if (kAheadTiles > 2 && j0 + kAheadTiles * kTile < most + kTile)
+            wait_copies_but<(kAheadTiles - 2) * kCopies>();
+          else
+            wait_copies();
+          __syncthreads();
+        }
+        const int32_t j = j0 + part * kKeys, copy_j = j0 + kAheadTiles * kTile;
+        if (part > 0 && j >= most) break;
+        keys_step<T, S>(p, st, s, q, tiles + n % kRing * kBuffer, part,
+                        tiles + (n + last) % kRing * kBuffer, last ? 0 : part + 1,
+                        tiles + (n + kAheadTiles) % kRing * kBuffer, k, v, rope,
+                        last && copy_j < most, copy_j, keys, mine - j, least >= j + kKeys, places,
+                        wave, lane);
+      }
+    }
   }
   if (row >= rows) return;
   const float sum = st.sum + other_half(st.sum);
@@ -232,6 +349,12 @@ __global__ __launch_bounds__(kBlock, 2) void expand_kernel(ExpandParams p) {
           u32x2{T::pack(st.o[b][i] * by, st.o[b][i + 1] * by),
                 T::pack(st.o[b][i + 2] * by, st.o[b][i + 3] * by)};
   if (p.lse && half == 0) p.lse[at * p.heads + head] = (st.top + log2f(sum)) * kLn2;
+}
+
+template <class T, class S>
+int launch_expand(ExpandParams p, int32_t longest, int64_t pairs, void* stream) {
+  p.tiles = (longest + S::kRows - 1) / S::kRows;
+  return launch(expand_kernel<T, S>, dim3((unsigned)(pairs * p.tiles)), dim3(S::kBlock), p, stream);
 }
 
 }  // namespace
@@ -251,7 +374,8 @@ extern "C" int dsatopk_attend_expanded(
       num_heads > 1024 || nope_dim != kNope || rope_dim != kRope || value_dim != kValue ||
       (type != DSATOPK_BF16 && type != DSATOPK_FP16) || !(scale > 0.0f) || !(scale < INFINITY) ||
       q_row_stride < 0 || q_head_stride < 0 || k_row_stride < 0 || k_head_stride < 0 ||
-      v_row_stride < 0 || v_head_stride < 0 || rope_row_stride < 0)
+      v_row_stride < 0 || v_head_stride < 0 || rope_row_stride < 0 ||
+      k_row_stride > kMostStride || v_row_stride > kMostStride || rope_row_stride > kMostStride)
     return DSATOPK_ERR_INVALID_ARG;
   if (num_requests == 0 || num_queries == 0 || max_queries == 0) return DSATOPK_OK;
   if (!q || !out || !q_starts || !k_starts || (num_keys && (!k || !v || !k_rope)))
@@ -284,10 +408,14 @@ extern "C" int dsatopk_attend_expanded(
   p.out = static_cast<char*>(out);
   p.lse = lse;
   const int32_t longest = max_queries < num_queries ? max_queries : num_queries;
-  p.tiles = (longest + kRows - 1) / kRows;
-  const int64_t groups = ((int64_t)num_requests * num_heads + 7) / 8 * 8 * p.tiles;
-  if (groups > INT32_MAX) return DSATOPK_ERR_INVALID_ARG;
-  const dim3 grid((unsigned)groups);
-  return type == DSATOPK_BF16 ? launch(expand_kernel<Bf16>, grid, dim3(kBlock), p, stream)
-                              : launch(expand_kernel<Fp16>, grid, dim3(kBlock), p, stream);
+  const int64_t pairs = ((int64_t)num_requests * num_heads + 7) / 8 * 8;
+  if (pairs * ((longest + 127) / 128) > INT32_MAX) return DSATOPK_ERR_INVALID_ARG;
+  // Eight waves where they fill the card's 256 CUs, if all prompts are of the
+  // longest's length.
+  const bool wide = pairs * (longest / 256) >= 256;
+  const bool bf16 = type == DSATOPK_BF16;
+  return wide ? bf16 ? launch_expand<Bf16, Shape<8>>(p, longest, pairs, stream)
+                     : launch_expand<Fp16, Shape<8>>(p, longest, pairs, stream)
+         : bf16 ? launch_expand<Bf16, Shape<4>>(p, longest, pairs, stream)
+                : launch_expand<Fp16, Shape<4>>(p, longest, pairs, stream);
 }

@@ -195,7 +195,7 @@ extern "C" int dsatopk_page_maps(const int32_t* seq_lens, const int32_t* new_len
                                  int32_t num_tokens, int32_t* token_starts, int32_t* slots,
                                  int32_t* table_rows, int32_t* row_lens, int32_t* counts,
                                  void* stream) {
-  if (num_requests < 0 || num_free < 0 || num_tokens < 0 || page_table_width < 0 ||
+  if (num_requests < 0 || num_free < 0 || num_tokens < 0 || num_tokens > (1 << 30) || page_table_width < 0 ||
       page_table_stride < page_table_width || !pow2(page_size) || page_size > (1 << 20))
     return DSATOPK_ERR_INVALID_ARG;
   if (!token_starts || !counts || (num_requests && (!seq_lens || !page_table)) ||

@@ -96,6 +96,14 @@ __device__ __forceinline__ void wait_copies() {
   asm volatile("" ::: "memory");       // LDS reads stay behind it
 }
 
+// Until all but this wave's last n loads and copies have arrived.
+template <int n>
+__device__ __forceinline__ void wait_copies_but() {
+  static_assert(n >= 0 && n < 16, "the low four bits of the count");
+  __builtin_amdgcn_s_waitcnt(0x0f70 | n);
+  asm volatile("" ::: "memory");
+}
+
 // Copies of all waves visible to all waves (each waits for its own first).
 __device__ __forceinline__ void copies_barrier() {
   wait_copies();
