@@ -66,7 +66,8 @@ enum {
     DSATOPK_ERR_HIP = 4,
     /* dsatopk_paged_noalloc: num_rows above DSATOPK_NOALLOC_MAX_ROWS. */
     DSATOPK_ERR_TOO_LARGE = 5,
-    /* workspace missing or smaller than dsatopk_attend_bytes(...). */
+    /* workspace missing or smaller than dsatopk_attend_bytes(...) or
+       dsatopk_expanded_bytes(...). */
     DSATOPK_ERR_WORKSPACE_TOO_SMALL = 6
 };
 
@@ -486,6 +487,10 @@ int dsatopk_attend_paged(const void* q, int64_t q_row_stride, int64_t q_head_str
  *   out           type [num_queries, num_heads, value_dim], contiguous. Rows
  *                 of no request are not written.
  *   lse           float [num_queries, num_heads] or NULL.
+ *   workspace     at least dsatopk_expanded_bytes(num_requests, num_heads,
+ *                 num_queries, num_keys, max_queries) bytes, 16-byte aligned
+ *                 (NULL where that is 0: batches that fill the card are not
+ *                 split). Calls that overlap must not share one.
  *
  * Values must be finite, also those of keys that causality hides from some
  * queries (their weight is 0, which infinities and NaN turn into NaN). Hidden
@@ -493,8 +498,12 @@ int dsatopk_attend_paged(const void* q, int64_t q_row_stride, int64_t q_head_str
  *
  * Errors: DSATOPK_ERR_INVALID_ARG, DSATOPK_ERR_ALIGNMENT (an input not
  * 16-byte aligned or a stride no multiple of 8 elements; out not 8-byte
- * aligned), DSATOPK_ERR_HIP. No queries: a no-op.
+ * aligned), DSATOPK_ERR_WORKSPACE_TOO_SMALL, DSATOPK_ERR_HIP. No queries: a
+ * no-op.
  */
+size_t dsatopk_expanded_bytes(int32_t num_requests, int32_t num_heads, int32_t num_queries,
+                              int32_t num_keys, int32_t max_queries);
+
 int dsatopk_attend_expanded(const void* q, int64_t q_row_stride, int64_t q_head_stride,
                             const void* k, int64_t k_row_stride, int64_t k_head_stride,
                             const void* v, int64_t v_row_stride, int64_t v_head_stride,
@@ -503,7 +512,8 @@ int dsatopk_attend_expanded(const void* q, int64_t q_row_stride, int64_t q_head_
                             int32_t value_dim, float scale, int32_t causal,
                             const int32_t* q_starts, const int32_t* k_starts,
                             int32_t num_requests, int32_t num_queries, int32_t num_keys,
-                            int32_t max_queries, void* out, float* lse, void* stream);
+                            int32_t max_queries, void* out, float* lse, void* workspace,
+                            size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -32,7 +32,7 @@ EXPORTS = ("dsatopk_status_string", "dsatopk_plan_bytes", "dsatopk_plan", "dsato
            "dsatopk_paged", "dsatopk_paged_packed", "dsatopk_ragged", "dsatopk_paged_noalloc",
            "dsatopk_page_maps", "dsatopk_scores_paged", "dsatopk_scores_ragged",
            "dsatopk_attend_bytes", "dsatopk_attend_selected", "dsatopk_attend_paged",
-           "dsatopk_attend_expanded")
+           "dsatopk_attend_expanded", "dsatopk_expanded_bytes")
 
 
 class DsatopkError(RuntimeError):
@@ -95,7 +95,9 @@ def _lib():
         lib.dsatopk_attend_paged.restype = ctypes.c_int
         lib.dsatopk_attend_expanded.argtypes = [P, i64, i64, P, i64, i64, P, i64, i64, P, i64, i32,
                                                 i32, i32, i32, i32, f32, i32, P, P, i32, i32, i32,
-                                                i32, P, P, P]
+                                                i32, P, P, P, sz, P]
+        lib.dsatopk_expanded_bytes.argtypes = [i32, i32, i32, i32, i32]
+        lib.dsatopk_expanded_bytes.restype = sz
         lib.dsatopk_attend_expanded.restype = ctypes.c_int
         _handle = lib
     return _handle
@@ -312,6 +314,13 @@ def attend_bytes(num_rows: int, num_heads: int, latent_dim: int, max_tokens: int
     ``attend_paged`` (max_tokens: max_seq_len)."""
     return int(_lib().dsatopk_attend_bytes(int(num_rows), int(num_heads), int(latent_dim),
                                            int(max_tokens)))
+
+
+def expanded_bytes(num_requests: int, num_heads: int, num_queries: int, num_keys: int,
+                   max_queries: int) -> int:
+    """Workspace bytes of ``attend_expanded``."""
+    return int(_lib().dsatopk_expanded_bytes(int(num_requests), int(num_heads), int(num_queries),
+                                             int(num_keys), int(max_queries)))
 
 
 # The serving operators' calls (csrc/serve_binding.cpp), loaded at first use.

@@ -20,6 +20,9 @@
 // them, one product between every few other instructions, so that the matrix
 // units work while exponentials are taken.
 //
+// Few rows of many keys are split over workgroups by keys; a second kernel
+// joins the parts.
+//
 // Weights are rounded to the inputs' type for the second product; scores,
 // maxima, sums and accumulators are fp32.
 
@@ -62,10 +65,12 @@ struct ExpandParams {
   int64_t rope_row;
   const int32_t* q_starts;
   const int32_t* k_starts;
-  int32_t requests, heads, tiles, num_q, num_k, causal;
+  int32_t requests, heads, tiles, num_q, num_k, causal, splits;
   float scale2;
   char* out;
   float* lse;
+  float* part;   // [splits, num_q, heads, kValue], then [splits, num_q, heads, 2]
+  float* state;
 };
 
 // A lane's places in a tile and in its copies, in bytes; the others follow
@@ -206,6 +211,21 @@ __device__ __forceinline__ void keys_step(const ExpandParams& p, State& st, f32x
   float sum = 0.0f;
   const f32x16 next = scores_of<T, S>(after, after_part, q, places, &s, p.scale2,
                                       st.top == -INFINITY ? 0.0f : st.top, &w, &sum);
+  const int column = here(places.column);
+  // Step n: block n % kBlocks of 16 keys' share, n / kBlocks of 2. Reads go
+  // kAhead steps before their products.
+  constexpr int kAll = 2 * kBlocks, kAhead = 5;
+  auto read = [&](int n) {
+    const int b = n % kBlocks;
+    const char* rows = cur + part * kKeys * kValueBytes + (n / kBlocks) * 16 * kValueBytes;
+    const u32x2 lo = read_columns(rows + (column ^ (b << 6)));
+    // swizzle32(t + 8) = swizzle32(t) ^ 2
+    const u32x2 hi = read_columns(rows + (column ^ (b << 6) ^ 32) + 8 * kValueBytes);
+    return u32x4{lo[0], lo[1], hi[0], hi[1]};
+  };
+  u32x4 a[kAhead];
+#pragma unroll
+  for (int n = 0; n < kAhead; ++n) a[n] = read(n);
   if (__any(!(sum <= kMost) || st.top == -INFINITY)) {
     float top = s[0];
 #pragma unroll
@@ -226,21 +246,6 @@ __device__ __forceinline__ void keys_step(const ExpandParams& p, State& st, f32x
   st.sum += sum;
   s = next;
 
-  const int column = here(places.column);
-  // Step n: block n % kBlocks of 16 keys' share, n / kBlocks of 2. Reads go
-  // kAhead steps before their products.
-  constexpr int kAll = 2 * kBlocks, kAhead = 5;
-  auto read = [&](int n) {
-    const int b = n % kBlocks;
-    const char* rows = cur + part * kKeys * kValueBytes + (n / kBlocks) * 16 * kValueBytes;
-    const u32x2 lo = read_columns(rows + (column ^ (b << 6)));
-    // swizzle32(t + 8) = swizzle32(t) ^ 2
-    const u32x2 hi = read_columns(rows + (column ^ (b << 6) ^ 32) + 8 * kValueBytes);
-    return u32x4{lo[0], lo[1], hi[0], hi[1]};
-  };
-  u32x4 a[kAhead];
-#pragma unroll
-  for (int n = 0; n < kAhead; ++n) a[n] = read(n);
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
     const u32x4 y = {T::pack(w[8 * g], w[8 * g + 1]), T::pack(w[8 * g + 2], w[8 * g + 3]),
@@ -268,6 +273,7 @@ __global__ __launch_bounds__(S::kBlock, 2) void expand_kernel(ExpandParams p) {
   // 8 apart so that they share an L2. Late rows see most keys: they go first.
   const uint32_t pairs = (uint32_t)(p.requests * p.heads);
   const uint32_t id = blockIdx.x;
+  const int split = blockIdx.y;
   const uint32_t pair = id / (8 * p.tiles) * 8 + id % 8;
   if (pair >= pairs) return;
   const int tile = p.tiles - 1 - (int)(id / 8 % p.tiles);
@@ -286,8 +292,12 @@ __global__ __launch_bounds__(S::kBlock, 2) void expand_kernel(ExpandParams p) {
     return p.causal ? min(max(i + 1 + keys - rows, 0), keys) : keys;
   };
   const int32_t mine = sees(row < rows ? row : rows - 1);
-  const int32_t most = sees(min(first + kRows, rows) - 1);
+  const int32_t all = sees(min(first + kRows, rows) - 1);
   const int32_t least = sees(min(first + wave * 32, rows - 1));
+  // this part's keys: [start, most)
+  const int32_t share = ((all + kTile - 1) / kTile + p.splits - 1) / p.splits * kTile;
+  const int32_t start = min(split * share, all);
+  const int32_t most = min(start + share, all);
 
   u32x4 q[kSteps];
   const char* qh = p.q + at * p.q_row + head * p.q_head;
@@ -304,16 +314,16 @@ __global__ __launch_bounds__(S::kBlock, 2) void expand_kernel(ExpandParams p) {
   const char* v = p.v + k0 * p.v_row + head * p.v_head;
   const char* rope = p.rope + k0 * p.rope_row;
   const Places<S> places(p, lane);
-  if (most > 0) {
+  if (start < most) {
     constexpr int kAheadTiles = kRing - 1, kParts = kTile / kKeys;
 #pragma unroll
     for (int n = 0; n < kAheadTiles; ++n)
-      if (n * kTile < most)
-        copy_tile<S>(p, tiles + n * kBuffer, k, v, rope, n * kTile, keys, places, wave, lane);
+      if (start + n * kTile < most)
+        copy_tile<S>(p, tiles + n * kBuffer, k, v, rope, start + n * kTile, keys, places, wave, lane);
     copies_barrier();
     f32x16 s = scores_of<T, S>(tiles, 0, q, places, nullptr, 0.0f, 0.0f, nullptr, nullptr);
     int n = 0;
-    for (int32_t j0 = 0; j0 < most; j0 += kTile, ++n) {
+    for (int32_t j0 = start; j0 < most; j0 += kTile, ++n) {
 #pragma unroll
       for (int part = 0; part < kParts; ++part) {
         const bool last = part + 1 == kParts;
@@ -339,6 +349,22 @@ __global__ __launch_bounds__(S::kBlock, 2) void expand_kernel(ExpandParams p) {
   }
   if (row >= rows) return;
   const float sum = st.sum + other_half(st.sum);
+  if (p.splits > 1) {
+    const int64_t to = ((int64_t)split * p.num_q + at) * p.heads + head;
+    if (half == 0) {
+      p.state[to * 2] = st.top;
+      p.state[to * 2 + 1] = sum;
+    }
+    if (st.top == -INFINITY && sum == 0.0f) return;  // nothing seen: the join skips it
+    float* part = p.part + to * kValue + 4 * half;
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4)
+        *reinterpret_cast<f32x4*>(part + b * 32 + 2 * i) =
+            f32x4{st.o[b][i], st.o[b][i + 1], st.o[b][i + 2], st.o[b][i + 3]};
+    return;
+  }
   const float by = sum == 0.0f ? 0.0f : 1.0f / sum;
   char* to = p.out + ((at * p.heads + head) * kValue + 4 * half) * 2;
 #pragma unroll
@@ -351,16 +377,100 @@ __global__ __launch_bounds__(S::kBlock, 2) void expand_kernel(ExpandParams p) {
   if (p.lse && half == 0) p.lse[at * p.heads + head] = (st.top + log2f(sum)) * kLn2;
 }
 
+// Joins the parts of the rows' heads: 32 threads for each, 4 elements a
+// thread. Rows of no request, or past their request's max_queries, have not
+// been computed and are left alone.
+constexpr int kJoinBlock = 256, kJoinEach = kValue / 4;
+
+template <class T>
+__global__ __launch_bounds__(kJoinBlock) void expand_join_kernel(ExpandParams p) {
+  const int64_t at = (int64_t)blockIdx.x * (kJoinBlock / kJoinEach) + threadIdx.x / kJoinEach;
+  const int64_t each = (int64_t)p.num_q * p.heads;
+  if (at >= each) return;
+  const int32_t row = (int32_t)(at / p.heads);
+  int lo = 0, hi = p.requests;  // q_starts[lo] <= row < q_starts[hi], if it is in a request
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (p.q_starts[mid] <= row)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  if (row < p.q_starts[lo] || row >= p.q_starts[lo + 1] ||
+      row - p.q_starts[lo] >= p.tiles * Shape<4>::kRows)
+    return;
+  float top = -INFINITY;
+#pragma unroll 4
+  for (int s = 0; s < p.splits; ++s) top = fmaxf(top, p.state[(s * each + at) * 2]);
+  const float ref = top == -INFINITY ? 0.0f : top;
+  f32x4 o = {};
+  float sum = 0.0f;
+  const int e = threadIdx.x % kJoinEach * 4;
+#pragma unroll 4
+  for (int s = 0; s < p.splits; ++s) {
+    const float x = p.state[(s * each + at) * 2], n = p.state[(s * each + at) * 2 + 1];
+    if (x == -INFINITY && n == 0.0f) continue;
+    const float by = exp2_fast(x - ref);
+    sum += n * by;
+    o += *reinterpret_cast<const f32x4*>(p.part + (s * each + at) * kValue + e) * by;
+  }
+  const float by = sum == 0.0f ? 0.0f : 1.0f / sum;
+  *reinterpret_cast<u32x2*>(p.out + (at * kValue + e) * 2) =
+      u32x2{T::pack(o[0] * by, o[1] * by), T::pack(o[2] * by, o[3] * by)};
+  if (p.lse && e == 0) p.lse[at] = (top + log2f(sum)) * kLn2;
+}
+
+// Workgroups of a batch, and the parts that its keys are cut into: where four
+// waves a workgroup leave half the card's places (two a CU) empty, as many
+// as fill them, of 512 keys at least by the requests' mean.
+struct Cut {
+  int64_t pairs;
+  int32_t longest, splits;
+  bool wide;
+};
+Cut cut_of(int32_t requests, int32_t heads, int32_t queries, int32_t keys, int32_t max_queries) {
+  Cut c;
+  c.pairs = ((int64_t)requests * heads + 7) / 8 * 8;
+  c.longest = max_queries < queries ? max_queries : queries;
+  // Eight waves where they fill the card's 256 CUs, if all prompts are of the
+  // longest's length.
+  c.wide = c.pairs * (c.longest / 256) >= 256;
+  const int64_t groups = (int64_t)requests * heads * ((c.longest + 127) / 128);
+  int64_t s = groups > 0 ? 512 / groups : 1;
+  const int64_t most = requests > 0 ? keys / requests / 512 : 1;
+  if (s > most) s = most;
+  c.splits = c.wide || s < 2 ? 1 : s > 64 ? 64 : (int32_t)s;
+  return c;
+}
+
 template <class T, class S>
-int launch_expand(ExpandParams p, int32_t longest, int64_t pairs, void* stream) {
-  p.tiles = (longest + S::kRows - 1) / S::kRows;
-  return launch(expand_kernel<T, S>, dim3((unsigned)(pairs * p.tiles)), dim3(S::kBlock), p, stream);
+int launch_expand(ExpandParams p, const Cut& c, void* stream) {
+  p.tiles = (c.longest + S::kRows - 1) / S::kRows;
+  p.splits = c.splits;
+  const int st = launch(expand_kernel<T, S>, dim3((unsigned)(c.pairs * p.tiles), (unsigned)c.splits),
+                        dim3(S::kBlock), p, stream);
+  if (st != DSATOPK_OK || c.splits == 1) return st;
+  const int64_t each = (int64_t)p.num_q * p.heads;
+  constexpr int kPer = kJoinBlock / kJoinEach;
+  return launch(expand_join_kernel<T>, dim3((unsigned)((each + kPer - 1) / kPer)), dim3(kJoinBlock), p,
+                stream);
+}
+
+size_t part_floats(const Cut& c, int32_t queries, int32_t heads) {
+  return c.splits == 1 ? 0 : (size_t)c.splits * queries * heads * (kValue + 2);
 }
 
 }  // namespace
 }  // namespace dsatopk_serve
 
 using namespace dsatopk_serve;
+
+extern "C" size_t dsatopk_expanded_bytes(int32_t num_requests, int32_t num_heads, int32_t num_queries,
+                                         int32_t num_keys, int32_t max_queries) {
+  if (num_requests < 1 || num_heads < 1 || num_queries < 1 || num_keys < 0 || max_queries < 1) return 0;
+  return part_floats(cut_of(num_requests, num_heads, num_queries, num_keys, max_queries), num_queries,
+                     num_heads) * sizeof(float);
+}
 
 extern "C" int dsatopk_attend_expanded(
     const void* q, int64_t q_row_stride, int64_t q_head_stride, const void* k,
@@ -369,7 +479,7 @@ extern "C" int dsatopk_attend_expanded(
     int32_t num_heads, int32_t nope_dim, int32_t rope_dim, int32_t value_dim, float scale,
     int32_t causal, const int32_t* q_starts, const int32_t* k_starts, int32_t num_requests,
     int32_t num_queries, int32_t num_keys, int32_t max_queries, void* out, float* lse,
-    void* stream) {
+    void* workspace, size_t workspace_bytes, void* stream) {
   if (num_requests < 0 || num_queries < 0 || num_keys < 0 || max_queries < 0 || num_heads < 1 ||
       num_heads > 1024 || nope_dim != kNope || rope_dim != kRope || value_dim != kValue ||
       (type != DSATOPK_BF16 && type != DSATOPK_FP16) || !(scale > 0.0f) || !(scale < INFINITY) ||
@@ -407,15 +517,18 @@ extern "C" int dsatopk_attend_expanded(
   p.scale2 = scale * kLog2e;
   p.out = static_cast<char*>(out);
   p.lse = lse;
-  const int32_t longest = max_queries < num_queries ? max_queries : num_queries;
-  const int64_t pairs = ((int64_t)num_requests * num_heads + 7) / 8 * 8;
-  if (pairs * ((longest + 127) / 128) > INT32_MAX) return DSATOPK_ERR_INVALID_ARG;
-  // Eight waves where they fill the card's 256 CUs, if all prompts are of the
-  // longest's length.
-  const bool wide = pairs * (longest / 256) >= 256;
+  const Cut c = cut_of(num_requests, num_heads, num_queries, num_keys, max_queries);
+  if (c.pairs * ((c.longest + 127) / 128) > INT32_MAX) return DSATOPK_ERR_INVALID_ARG;
+  if (c.splits > 1) {
+    if (!workspace || workspace_bytes < part_floats(c, num_queries, num_heads) * sizeof(float))
+      return DSATOPK_ERR_WORKSPACE_TOO_SMALL;
+    if (!aligned16(workspace)) return DSATOPK_ERR_ALIGNMENT;
+    p.part = static_cast<float*>(workspace);
+    p.state = p.part + (size_t)c.splits * num_queries * num_heads * kValue;
+  }
   const bool bf16 = type == DSATOPK_BF16;
-  return wide ? bf16 ? launch_expand<Bf16, Shape<8>>(p, longest, pairs, stream)
-                     : launch_expand<Fp16, Shape<8>>(p, longest, pairs, stream)
-         : bf16 ? launch_expand<Bf16, Shape<4>>(p, longest, pairs, stream)
-                : launch_expand<Fp16, Shape<4>>(p, longest, pairs, stream);
+  return c.wide ? bf16 ? launch_expand<Bf16, Shape<8>>(p, c, stream)
+                       : launch_expand<Fp16, Shape<8>>(p, c, stream)
+         : bf16 ? launch_expand<Bf16, Shape<4>>(p, c, stream)
+                : launch_expand<Fp16, Shape<4>>(p, c, stream);
 }

@@ -374,6 +374,20 @@ struct Results {
   }
 };
 
+// The given workspace, or one of `need` bytes.
+at::Tensor workspace_of(PyObject* given, size_t need, const at::Tensor& q) {
+  if (given && given != Py_None) {
+    const at::Tensor& t = tensor(given, "workspace");
+    if (t.scalar_type() != at::kByte || !t.is_contiguous())
+      refuse("workspace must be a contiguous uint8 tensor");
+    on_device(t, &q, "workspace");
+    return t;
+  }
+  return need ? empty({(int64_t)need}, at::kByte, q) : at::Tensor();
+}
+void* room_ptr(const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
+size_t room_bytes(const at::Tensor& t) { return t.defined() ? (size_t)t.numel() : 0; }
+
 // The absorbed forms' common arguments.
 struct Absorbed {
   const at::Tensor &q, &cache;
@@ -393,17 +407,8 @@ struct Absorbed {
       refuse("cache must have q's type and last dimension");
   }
   void room(PyObject* given, int64_t tokens) {
-    if (given && given != Py_None) {
-      workspace = tensor(given, "workspace");
-      if (workspace.scalar_type() != at::kByte || !workspace.is_contiguous())
-        refuse("workspace must be a contiguous uint8 tensor");
-      on_device(workspace, &q, "workspace");
-    } else if (const size_t need = dsatopk_attend_bytes(rows, heads, latent, tokens)) {
-      workspace = empty({(int64_t)need}, at::kByte, q);
-    }
+    workspace = workspace_of(given, dsatopk_attend_bytes(rows, heads, latent, tokens), q);
   }
-  void* room_ptr() const { return workspace.defined() ? workspace.data_ptr() : nullptr; }
-  size_t room_bytes() const { return workspace.defined() ? (size_t)workspace.numel() : 0; }
 };
 
 PyObject* attend_selected(PyObject* const* args, Py_ssize_t n, PyObject* kw) {
@@ -424,8 +429,8 @@ PyObject* attend_selected(PyObject* const* args, Py_ssize_t n, PyObject* kw) {
                               size32(s.cache.size(1), "cache"), s.type, s.heads, s.latent,
                               size32(s.q.size(2) - s.latent, "q"), scale, ints(slots),
                               row_stride(slots), k, s.rows, s.results.out.data_ptr(),
-                              static_cast<float*>(s.results.lse.data_ptr()), s.room_ptr(),
-                              s.room_bytes(), on.stream),
+                              static_cast<float*>(s.results.lse.data_ptr()), room_ptr(s.workspace),
+                              room_bytes(s.workspace), on.stream),
       "dsatopk_attend_selected");
   return pair(s.results.out, s.results.lse);
 }
@@ -452,15 +457,15 @@ PyObject* attend_paged(PyObject* const* args, Py_ssize_t n, PyObject* kw) {
                            size32(s.q.size(2) - s.latent, "q"), scale, ints(lens), ints(tab),
                            row_stride(tab), size32(tab.size(1), "page_table"), rows, longest, s.rows,
                            s.results.out.data_ptr(), static_cast<float*>(s.results.lse.data_ptr()),
-                           s.room_ptr(), s.room_bytes(), on.stream),
+                           room_ptr(s.workspace), room_bytes(s.workspace), on.stream),
       "dsatopk_attend_paged");
   return pair(s.results.out, s.results.lse);
 }
 
 PyObject* attend_expanded(PyObject* const* args, Py_ssize_t n, PyObject* kw) {
   static const char* const names[] = {"q", "k", "v", "k_rope", "q_starts", "k_starts", "max_queries",
-                                      "scale", "causal", "out", "lse", "stream"};
-  const Args<12> a("attend_expanded", names, 8, args, n, kw);
+                                      "scale", "causal", "out", "lse", "workspace", "stream"};
+  const Args<13> a("attend_expanded", names, 8, args, n, kw);
   const at::Tensor& q = shaped(a.at[0], 3, nullptr, "q");
   const at::Tensor& k = shaped(a.at[1], 3, &q, "k");
   const at::Tensor& v = shaped(a.at[2], 3, &q, "v");
@@ -480,16 +485,20 @@ PyObject* attend_expanded(PyObject* const* args, Py_ssize_t n, PyObject* kw) {
   const int causal = a.at[8] ? PyObject_IsTrue(a.at[8]) : 1;
   if (causal < 0) throw Failed{};
   const Results r(a.at[9], a.at[10], q, v.size(2));
-  const On on(q, a.at[11]);
+  const int32_t requests = size32(qs.size(0) - 1, "q_starts"), heads = size32(q.size(1), "q");
+  const int32_t queries = size32(q.size(0), "q"), keys = size32(k.size(0), "k");
+  const at::Tensor room = workspace_of(
+      a.at[11], dsatopk_expanded_bytes(requests, heads, queries, keys, longest), q);
+  const On on(q, a.at[12]);
   check_status(
       dsatopk_attend_expanded(q.data_ptr(), stride(q, 0), stride(q, 1), k.data_ptr(), stride(k, 0),
                               stride(k, 1), v.data_ptr(), stride(v, 0), stride(v, 1),
-                              rope.data_ptr(), stride(rope, 0), type, size32(q.size(1), "q"),
+                              rope.data_ptr(), stride(rope, 0), type, heads,
                               size32(k.size(2), "k"), size32(rope.size(1), "k_rope"),
                               size32(v.size(2), "v"), scale, causal, ints(qs), ints(ks),
-                              size32(qs.size(0) - 1, "q_starts"), size32(q.size(0), "q"),
-                              size32(k.size(0), "k"), longest, r.out.data_ptr(),
-                              static_cast<float*>(r.lse.data_ptr()), on.stream),
+                              requests, queries, keys, longest, r.out.data_ptr(),
+                              static_cast<float*>(r.lse.data_ptr()), room_ptr(room),
+                              room_bytes(room), on.stream),
       "dsatopk_attend_expanded");
   return pair(r.out, r.lse);
 }
@@ -571,7 +580,7 @@ page table.
 Arguments as for attend_selected and paged(); max_seq_len bounds seq_lens (the
 table's width when None) and sets how rows are split.)doc";
 
-const char attend_expanded_doc[] = R"doc(attend_expanded(q, k, v, k_rope, q_starts, k_starts, max_queries, scale, causal=True, out=None, lse=None, stream=None)
+const char attend_expanded_doc[] = R"doc(attend_expanded(q, k, v, k_rope, q_starts, k_starts, max_queries, scale, causal=True, out=None, lse=None, workspace=None, stream=None)
 --
 
 Expanded latent attention over a ragged batch of prompts.
@@ -580,7 +589,8 @@ q [queries, heads, 192], k and v [keys, heads, 128] and k_rope [keys, 64] in
 bfloat16 or float16 (k and v may be parts of one tensor); q_starts and
 k_starts int32 [requests + 1]; max_queries bounds a request's queries, which
 are its last tokens. Returns (out, lse): q's type [queries, heads, 128], and
-float32 [queries, heads].)doc";
+float32 [queries, heads]. workspace: uint8 of expanded_bytes(requests, heads,
+queries, keys, max_queries) (allocated when None).)doc";
 
 #define SERVE_CALL(name) \
   {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(guarded<name>)), \

@@ -342,6 +342,51 @@ def test_expanded(kind, q_lens, k_lens, heads):
     check_expanded(q_lens, k_lens, heads, kind)
 
 
+@pytest.mark.parametrize("q_lens,k_lens,heads,kind", [
+    ([2, 130, 1], [3000, 2050, 1], 1, "bf16"),   # parts of many sizes, and empty ones
+    ([40, 0, 7], [5000, 10, 600], 2, "fp16"),
+    ([1], [20000], 1, "bf16"),
+])
+def test_expanded_split_over_keys(q_lens, k_lens, heads, kind):
+    import row_top_selection_amd as dt
+
+    assert dt.expanded_bytes(len(q_lens), heads, sum(q_lens) + 3, sum(k_lens), max(q_lens)) > 0
+    check_expanded(q_lens, k_lens, heads, kind, extra=3)
+
+
+def test_expanded_wide_workgroups():
+    """Enough rows for eight waves a workgroup: odd lengths, a prompt shorter
+    than the longest by more than a workgroup's rows, keys that end inside a
+    tile and inside its halves."""
+    import row_top_selection_amd as dt
+
+    g = torch.Generator(DEV).manual_seed(12)
+    q_lens, k_lens, heads = [515, 300, 1, 600, 512], [517, 333, 65, 631, 512], 64
+    qs, ks = np.concatenate([[0], np.cumsum(q_lens)]), np.concatenate([[0], np.cumsum(k_lens)])
+    q, k, v, rope = (torch.randn(*s, generator=g, device=DEV).to(torch.bfloat16) for s in (
+        (qs[-1], heads, 192), (ks[-1], heads, 128), (ks[-1], heads, 128), (ks[-1], 64)))
+    out, lse = dt.attend_expanded(q, k, v, rope, i32(qs), i32(ks), 600, SCALE)
+    torch.cuda.synchronize()
+    # heads apart: each as a batch of its own, by the narrow kernel
+    for h in (0, 17, 63):
+        one = [t[:, h:h + 1] for t in (q, k, v)]
+        a = dt.attend_expanded(*one, rope, i32(qs), i32(ks), 600, SCALE)
+        size = float((one[0].float().abs().flatten(0, 1).max(0).values * torch.cat(
+            [one[1].float().abs().flatten(0, 1).max(0).values, rope.float().abs().max(0).values])).sum() * SCALE)
+        rows = [0, 1, 255, 256, 514, 515, 814, 815, 816, 1415, 1416, 1927]
+        want_out = torch.zeros(len(rows), 1, 128, dtype=torch.float64)
+        want_lse, want_size = torch.zeros(len(rows), 1, dtype=torch.float64), torch.zeros_like(want_out)
+        for n, i in enumerate(rows):
+            r = int(np.searchsorted(qs, i, side="right")) - 1
+            end = int(ks[r]) + i - int(qs[r]) + 1 + k_lens[r] - q_lens[r]
+            kv = slice(int(ks[r]), end)
+            o, l, s = serve_plain.expand(one[0][i:i + 1], one[1][kv], one[2][kv], rope[kv], [0, 1],
+                                         [0, end - int(ks[r])], SCALE, False)
+            want_out[n], want_lse[n], want_size[n] = o[0], l[0], s[0]
+        for got in (a, (out[:, h:h + 1], lse[:, h:h + 1])):
+            close(got[0][rows], got[1][rows], (want_out, want_lse, want_size), size, 192)
+
+
 @pytest.mark.parametrize("causal", [True, False])
 def test_expanded_queries_without_keys(causal):
     """Requests with fewer keys than queries (the first queries see none),

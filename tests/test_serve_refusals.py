@@ -109,7 +109,7 @@ def test_attend_paged_refuses(lib, kw, code):
 EXPANDED = dict(q=A16, q_row=1536, q_head=192, k=A16, k_row=2048, k_head=256, v=A16, v_row=2048,
                 v_head=256, rope=A16, rope_row=64, type=0, heads=8, nope=128, rope_dim=64, value=128,
                 scale=0.1, causal=1, qs=A16, ks=A16, requests=2, queries=100, keys=200, longest=60,
-                out=A16, lse=A16, stream=None)
+                out=A16, lse=A16, work=None, bytes=0, stream=None)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -120,6 +120,8 @@ EXPANDED = dict(q=A16, q_row=1536, q_head=192, k=A16, k_row=2048, k_head=256, v=
     (dict(qs=None), 1), (dict(ks=None), 1), (dict(k_row=-8), 1), (dict(q=A8), 2), (dict(k=A4), 2),
     (dict(v=A8), 2), (dict(rope=A8), 2), (dict(out=A4), 2), (dict(lse=0x10001), 2),
     (dict(q_head=196), 2), (dict(k_row=2052), 2), (dict(v_head=260), 2), (dict(rope_row=68), 2),
+    (dict(k_row=1 << 28), 1), (dict(keys=20000), 6), (dict(keys=20000, work=A16, bytes=64), 6),
+    (dict(keys=20000, work=A4, bytes=1 << 40), 2),
 ])
 def test_attend_expanded_refuses(lib, kw, code):
     assert call(lib.dsatopk_attend_expanded, EXPANDED, kw) == code
@@ -141,6 +143,14 @@ def test_attend_bytes(lib):
     few = dt.attend_bytes(1, 16, 512, 131072)
     assert few >= 16 * (512 + 2) * 4 and few % 4 == 0
     assert dt.attend_bytes(1, 16, 512, 64) == 0  # one tile: nothing to split
+
+
+def test_expanded_bytes(lib):
+    assert dt.expanded_bytes(4, 16, 4096, 65536, 1024) == 0  # fills the card
+    assert dt.expanded_bytes(2, 8, 100, 200, 60) == 0        # too few keys to split
+    assert dt.expanded_bytes(0, 8, 100, 200, 60) == 0
+    few = dt.expanded_bytes(2, 1, 300, 10000, 164)
+    assert few >= 2 * 300 * 130 * 4 and few % (300 * 130 * 4) == 0
 
 
 def test_status_string(lib):
