@@ -508,21 +508,25 @@ __global__ __launch_bounds__(256) void join_few_kernel(AttendParams p) {
   if (p.lse && e == 0) p.lse[at] = (top + log2f(sum)) * kLn2;
 }
 
-// Joins the splits of one row's head. First a thread for each split: the
-// common maximum and the factors; then kLatent / 4 threads for each of
-// kSides sets of splits, 4 elements each.
-constexpr int kMaxSplits = 256;
+// Joins the splits of 4 * kEach elements of one row's head. First a thread
+// for each split: the common maximum and the factors; then kEach threads for
+// each of kJoinBlock / kEach sets of splits, 4 elements each. Many splits
+// mean few rows: a workgroup takes 128 elements then (64 parts of 8 rows of 16
+// heads: 8 us, and 20 by whole heads); up to kMidSplits, a head (8 parts of
+// 66 rows of 40 heads: 10 us, and 14 by quarters).
+constexpr int kMaxSplits = 256, kMidSplits = 16;
 constexpr int kJoinBlock = 256;
 
-template <class T, int kLatent>
+template <class T, int kLatent, int kEach>
 __global__ __launch_bounds__(kJoinBlock) void join_kernel(AttendParams p) {
-  constexpr int kSides = kJoinBlock / (kLatent / 4);
+  constexpr int kSides = kJoinBlock / kEach, kSlices = kLatent / (4 * kEach);
   __shared__ float tops[kJoinBlock / 64], sums[kJoinBlock / 64];
   __shared__ float factor[kMaxSplits];
   __shared__ __attribute__((aligned(16))) float half[kJoinBlock * 4];
   const int tid = threadIdx.x, wave = tid >> 6;
-  const int64_t row = blockIdx.x / p.heads;
-  const int head = blockIdx.x % p.heads;
+  const uint32_t which = blockIdx.x / kSlices, slice = blockIdx.x % kSlices;
+  const int64_t row = which / p.heads;
+  const int head = which % p.heads;
   const int64_t base = row * p.splits * p.heads + head;
 
   float x = -INFINITY, n = 0.0f;
@@ -550,24 +554,25 @@ __global__ __launch_bounds__(kJoinBlock) void join_kernel(AttendParams p) {
 #pragma unroll
   for (int w = 0; w < kJoinBlock / 64; ++w) sum += sums[w];
 
-  const int side = tid / (kLatent / 4), at = tid % (kLatent / 4);
+  const int side = tid / kEach;
+  const int e = (slice * kEach + tid % kEach) * 4;
   f32x4 o = {};
 #pragma unroll 4
   for (int s = side; s < p.splits; s += kSides) {
     const float f = factor[s];
     if (f < 0.0f) continue;
-    o += *reinterpret_cast<const f32x4*>(p.part + (base + (int64_t)s * p.heads) * kLatent + at * 4) * f;
+    o += *reinterpret_cast<const f32x4*>(p.part + (base + (int64_t)s * p.heads) * kLatent + e) * f;
   }
   *reinterpret_cast<f32x4*>(half + tid * 4) = o;
   __syncthreads();
   if (side) return;
 #pragma unroll
   for (int s = 1; s < kSides; ++s)
-    o += *reinterpret_cast<const f32x4*>(half + (s * (kLatent / 4) + at) * 4);
+    o += *reinterpret_cast<const f32x4*>(half + (s * kEach + tid) * 4);
   const float scale = sum == 0.0f ? 0.0f : 1.0f / sum;
-  *reinterpret_cast<u32x2*>(p.out + ((row * p.heads + head) * kLatent + at * 4) * 2) =
+  *reinterpret_cast<u32x2*>(p.out + ((row * p.heads + head) * kLatent + e) * 2) =
       u32x2{T::pack(o[0] * scale, o[1] * scale), T::pack(o[2] * scale, o[3] * scale)};
-  if (p.lse && tid == 0) p.lse[row * p.heads + head] = (top + log2f(sum)) * kLn2;
+  if (p.lse && e == 0) p.lse[row * p.heads + head] = (top + log2f(sum)) * kLn2;
 }
 
 // Heads a workgroup: 16, 32, 64 or 128.
@@ -620,8 +625,11 @@ int launch_attend(AttendParams p, void* stream) {
     return launch(join_few_kernel<T, kLatent>,
                   dim3((unsigned)(((int64_t)p.rows * p.heads + kPer - 1) / kPer)), dim3(256), p, stream);
   }
-  return launch(join_kernel<T, kLatent>, dim3((unsigned)((int64_t)p.rows * p.heads)),
-                dim3(kJoinBlock), p, stream);
+  const int64_t heads = (int64_t)p.rows * p.heads;
+  return p.splits <= kMidSplits
+             ? launch(join_kernel<T, kLatent, kLatent / 4>, dim3((unsigned)heads), dim3(kJoinBlock), p, stream)
+             : launch(join_kernel<T, kLatent, 32>, dim3((unsigned)(heads * (kLatent / 128))), dim3(kJoinBlock),
+                      p, stream);
 }
 
 size_t part_floats(int32_t rows, int32_t heads, int32_t latent, int32_t splits) {
