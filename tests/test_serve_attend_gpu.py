@@ -485,3 +485,31 @@ def test_expanded_graph_replays_follow_the_lengths():
         torch.cuda.synchronize()
         eager = dt.attend_expanded(q, k, v, rope, qs, ks, 200, SCALE)
         assert torch.equal(out, eager[0]) and torch.equal(lse, eager[1])
+
+
+@pytest.mark.parametrize("heads,k,pages", [(64, 300, 9), (128, 2048, 100), (32, 257, 1000), (17, 640, 3)])
+def test_selected_many_rows(heads, k, pages):
+    """Batches of prompt rows: more rows than the card has CUs, of every
+    length, with holes and repeated slots."""
+    import row_top_selection_amd as dt
+
+    g = torch.Generator(DEV).manual_seed(heads)
+    rng = np.random.default_rng(heads)
+    rows = 513
+    q, cache = make(g, rows, heads, 512, pages, 64, "bf16")
+    slots = rng.integers(0, pages * 64, (rows, k))
+    slots[rng.random((rows, k)) < 0.1] = -1
+    slots[np.arange(k) >= rng.integers(0, k + 1, rows)[:, None]] = -1
+    slots[0], slots[1], slots[2, 0] = -1, 7, pages * 64
+    out, lse = dt.attend_selected(q, cache, i32(slots), 512, SCALE)
+    again = dt.attend_selected(q, cache, i32(slots), 512, SCALE)
+    torch.cuda.synchronize()
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+    some = [0, 1, 2, 3, 100, 255, 256, 511, 512]
+    picked = [s[(s >= 0) & (s < pages * 64)] for s in slots[some]]
+    vectors = cache.view(-1, 576)
+    want = serve_plain.attend(q[some], vectors, 512, SCALE, picked)
+    close(out[some], lse[some], want, logit_size(q, vectors, SCALE), 576)
+    # a batch of the same rows that is split
+    few = dt.attend_selected(q[some], cache, i32(slots[some]), 512, SCALE)
+    close(few[0], few[1], want, logit_size(q, vectors, SCALE), 576)
