@@ -3365,7 +3365,7 @@ const char* dsatopk_status_string(int status) {
   switch (status) {
     case DSATOPK_OK: return "ok";
     case DSATOPK_ERR_INVALID_ARG: return "invalid argument";
-    case DSATOPK_ERR_ALIGNMENT: return "a pointer or stride is not aligned as the call needs (scores: 16 bytes, stride a multiple of 4)";
+    case DSATOPK_ERR_ALIGNMENT: return "scores not 16-byte aligned or stride not a multiple of 4, or another pointer or stride not aligned as its call needs";
     case DSATOPK_ERR_PLAN_TOO_SMALL: return "plan buffer too small";
     case DSATOPK_ERR_HIP: return "HIP runtime error";
     case DSATOPK_ERR_TOO_LARGE:
