@@ -129,7 +129,7 @@ __global__ __launch_bounds__(kBlock) void page_maps_kernel(MapParams p) {
     const int32_t a = max(t0 + tid * kPer, start[0]);
     const int32_t b = min(min(t0 + (tid + 1) * kPer, t1), tokens);
     if (a < b) {
-      int lo = 0, hi = kRequests;  // start[lo] <= a < start[hi]
+      int lo = 0, hi = min(kRequests, p.requests - r0);  // start[lo] <= a < start[hi]
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (start[mid] <= a)
