@@ -23,18 +23,18 @@
 //
 // A workgroup takes one row, up to 128 heads and a range of tokens (split
 // over workgroups when there are few rows; a second kernel joins the parts),
-// 64 tokens a tile, copied to LDS ahead of their use without passing through
-// registers. Its waves are WH groups of 16 heads by WT groups of a tile's
-// tokens; token groups keep sums of their own and join them at the end. The
-// vectors of 64 tokens fill 72 KB of LDS: two tiles, so one workgroup a CU,
-// of 8 waves where there are heads enough. A wave's sums take 128 registers
-// and its queries 72.
+// a tile of 32 or 64 tokens at a time, copied to LDS one tile ahead without
+// passing through registers. Its waves are WH groups of 16 heads by WT groups
+// of a tile's tokens; token groups keep sums of their own and join them at
+// the end. A wave's sums take 128 registers and its queries 72, so eight waves
+// fill a CU: for up to 64 heads two workgroups of four, which do not wait for
+// each other (1024 rows of 64 heads: 342 us, and 370 as one workgroup of eight
+// with tiles of 64 tokens), for more heads one of eight.
 //
 // 1024 prompt rows of 2048 slots and 64 heads (out of 4 x 16384 tokens) take
-// 370 us, 0.79 PFLOP/s: what is left is the wait for LDS reads, of which the
-// registers let a wave have six (QK) or four (PV) under way. 128 decode rows of
-// 128 heads take 120 us (2.8 TB/s), 8 rows of 131072 tokens and 16 heads 238
-// us: 5.1 TB/s, as fast as memory copies.
+// 342 us, 0.85 PFLOP/s: copies and products each take about 300 by themselves
+// and overlap in part. 128 decode rows of 128 heads take 120 us (2.8 TB/s), 8 rows
+// of 131072 tokens and 16 heads 238 us: 5.1 TB/s, as fast as memory copies.
 //
 // Weights are rounded to the inputs' 16-bit type for the second product
 // (off by at most 2^-8 or 2^-11 of each, of either sign); scores, maxima, sums and
@@ -45,7 +45,6 @@
 namespace dsatopk_serve {
 namespace {
 
-constexpr int kTile = 64;  // tokens
 constexpr int kRope = 64;
 constexpr int kRopeBytes = kRope * 2;
 constexpr int kFewSplits = 4;  // joined in one go
@@ -75,9 +74,10 @@ struct AttendParams {
 };
 
 // Waves of a workgroup: WH groups of 16 heads by WT groups of tokens.
-template <int kWH_, int kWT_, int kLatent_>
+template <int kWH_, int kWT_, int kTile_, int kLatent_>
 struct Plan {
   static constexpr int kWH = kWH_, kWT = kWT_, kWaves = kWH * kWT;
+  static constexpr int kTile = kTile_;          // tokens
   static constexpr int kBlock = kWaves * 64;
   static constexpr int kLatent = kLatent_;
   static constexpr int kRow = kLatent * 2;      // bytes of a latent vector
@@ -127,7 +127,7 @@ struct Places {
     copy = P::kRow == 1024 ? (lane ^ swizzle16(first)) * 16
                            : ((lane & 31) ^ swizzle16(first + (lane >> 5))) * 16;
     row = col * P::kRow + ((chunk_of(0, group) ^ swizzle16(col)) << 4);
-    rope = kTile * P::kRow + col * kRopeBytes + ((group ^ swizzle8(col)) << 4);
+    rope = P::kTile * P::kRow + col * kRopeBytes + ((group ^ swizzle8(col)) << 4);
     // lane i of 16 points at row i / 4, 8 bytes i % 4 of a 4 x 32 byte block
     const int tok = 4 * group + (col >> 2);
     column = tok * P::kRow + ((((col & 3) >> 1) ^ swizzle16(tok)) << 4) + 8 * (col & 1);
@@ -163,7 +163,7 @@ __device__ __forceinline__ void copy_tokens(char* tile, uint64_t at, int place, 
                           (uint32_t)__shfl((int)lo, mine);
     const uint32_t chunk = ((lane & 7) ^ swizzle8(first + mine)) * 16;
     copy_to_lds(reinterpret_cast<const char*>(base) + P::kRow + chunk,
-                tile + kTile * P::kRow + (first + t) * kRopeBytes);
+                tile + P::kTile * P::kRow + (first + t) * kRopeBytes);
   }
 }
 
@@ -276,7 +276,7 @@ __device__ __forceinline__ void attend_tokens(State<P>& st, const u32x4 (&q)[P::
 
   // The sums. kAhead is what the registers leave: one more block ahead spills,
   // and a reload waits for every copy in flight (375 -> 480 us for 1024 rows
-  // of 2048 slots and 64 heads).
+  // of 2048 slots and 64 heads, when they were one workgroup a CU).
   constexpr int kAhead = kGo == 1 ? 8 : 4;
   u32x4 a[kAhead];
 #pragma unroll
@@ -302,7 +302,7 @@ __device__ __forceinline__ void attend_tokens(State<P>& st, const u32x4 (&q)[P::
 }
 
 template <class T, class P, bool kPaged>
-__global__ __launch_bounds__(P::kBlock) void attend_kernel(AttendParams p) {
+__global__ __launch_bounds__(P::kBlock, P::kOwn ? 1 : 2) void attend_kernel(AttendParams p) {
   constexpr int kWH = P::kWH, kWT = P::kWT;
   __shared__ __attribute__((aligned(1024))) char tiles[2 * P::kBuffer];
   __shared__ uint32_t masks[2][P::kWaves];
@@ -320,27 +320,27 @@ __global__ __launch_bounds__(P::kBlock) void attend_kernel(AttendParams p) {
   int32_t len = p.selected;
   const int32_t* list;
   if constexpr (kPaged) {
-    const int64_t most = min((int64_t)p.table_width << p.page_bits, (int64_t)(INT32_MAX - kTile));
+    const int64_t most = min((int64_t)p.table_width << p.page_bits, (int64_t)(INT32_MAX - P::kTile));
     len = (int32_t)min((int64_t)max(p.seq_lens[row], 0), most);
     list = p.table + (p.table_rows ? p.table_rows[row] : row) * p.table_stride;
   } else {
     list = p.slots + row * p.slot_stride;
   }
-  const int32_t tiles_all = (len + kTile - 1) / kTile;
+  const int32_t tiles_all = (len + P::kTile - 1) / P::kTile;
   const int32_t per = (tiles_all + p.splits - 1) / p.splits;
   const int32_t first = split * per;
   const int32_t last = min(first + per, tiles_all);
 
   // The entry (slot or page) of token lane % P::kCopy of this wave's share of a tile, -1: none.
   auto entry_of = [&](int32_t tile) {
-    const int32_t j = tile * kTile + wave * P::kCopy + lane % P::kCopy;
+    const int32_t j = tile * P::kTile + wave * P::kCopy + lane % P::kCopy;
     if (tile >= last || j >= len) return -1;
     return list[kPaged ? j >> p.page_bits : j];
   };
   // Its address, or that of zeros.
   auto address_of = [&](int32_t tile, int32_t entry, bool& there) {
     int64_t page = entry;
-    int32_t in = tile * kTile + wave * P::kCopy + lane % P::kCopy;
+    int32_t in = tile * P::kTile + wave * P::kCopy + lane % P::kCopy;
     if constexpr (!kPaged) {
       page = entry >> p.page_bits;
       in = entry;
@@ -584,7 +584,9 @@ __global__ __launch_bounds__(kJoinBlock) void join_kernel(AttendParams p) {
 // Heads a workgroup: 16, 32, 64 or 128.
 int head_block(int32_t heads) { return heads <= 16 ? 16 : heads <= 32 ? 32 : heads <= 64 ? 64 : 128; }
 
-// Parts of the token axis. Costs in tiles of one CU's time, which runs one
+constexpr int kUnit = 64;
+
+// Parts of the token axis. Costs in 64 tokens of one CU's time, which runs one
 // workgroup: a part costs its tiles and about kPart more (first loads, last
 // sums, the join). Rows as long as they may be go in rounds of 256
 // workgroups; rows of mixed lengths end with the longest row's parts, after
@@ -595,7 +597,7 @@ int32_t splits_for(int32_t rows, int32_t heads, int64_t tokens) {
   constexpr int kTry[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 24, 32, 48, 64, 96, 128, 192, 256};
   const int hb = head_block(heads);
   const double groups = (double)rows * ((heads + hb - 1) / hb);
-  const int64_t tiles = (tokens + kTile - 1) / kTile;
+  const int64_t tiles = (tokens + kUnit - 1) / kUnit;
   int32_t best = 1;
   double least = 0;
   for (const int s : kTry) {
@@ -621,10 +623,10 @@ template <class T, int kLatent, bool kPaged>
 int launch_attend(AttendParams p, void* stream) {
   const int hb = head_block(p.heads);
   p.blocks = (p.heads + hb - 1) / hb;
-  const int st = hb == 16   ? launch_plan<T, Plan<1, 4, kLatent>, kPaged>(p, stream)
-                 : hb == 32 ? launch_plan<T, Plan<2, 4, kLatent>, kPaged>(p, stream)
-                 : hb == 64 ? launch_plan<T, Plan<4, 2, kLatent>, kPaged>(p, stream)
-                            : launch_plan<T, Plan<8, 1, kLatent>, kPaged>(p, stream);
+  const int st = hb == 16   ? launch_plan<T, Plan<1, 4, 64, kLatent>, kPaged>(p, stream)
+                 : hb == 32 ? launch_plan<T, Plan<2, 2, 32, kLatent>, kPaged>(p, stream)
+                 : hb == 64 ? launch_plan<T, Plan<4, 1, 32, kLatent>, kPaged>(p, stream)
+                            : launch_plan<T, Plan<8, 1, 64, kLatent>, kPaged>(p, stream);
   if (st != DSATOPK_OK || p.splits == 1) return st;
   if (p.splits <= kFewSplits) {
     constexpr int kPer = 256 / (kLatent / 4);
@@ -651,7 +653,7 @@ int check_attend(AttendParams& p, const void* q, int64_t q_row, int64_t q_head, 
   if (rows < 0 || heads < 1 || heads > 1024 || (latent != 256 && latent != 512) || rope != kRope ||
       (type != DSATOPK_BF16 && type != DSATOPK_FP16) || !(scale > 0.0f) || !(scale < INFINITY) ||
       num_pages < 0 || page_stride < 0 || token_stride < 0 || !pow2(page_size) ||
-      page_size > (1 << 20) || q_row < 0 || q_head < 0 || tokens < 0 || tokens > INT32_MAX - kTile)
+      page_size > (1 << 20) || q_row < 0 || q_head < 0 || tokens < 0 || tokens > INT32_MAX - kUnit)
     return DSATOPK_ERR_INVALID_ARG;
   if (rows == 0) return DSATOPK_OK;
   if (!q || !out || (num_pages && !cache)) return DSATOPK_ERR_INVALID_ARG;
