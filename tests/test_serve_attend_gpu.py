@@ -141,6 +141,27 @@ def test_paged(kind, heads, latent, page, per, lens):
         close(out, lse, want, logit_size(q, vectors, SCALE), latent + 64)
 
 
+@pytest.mark.parametrize("heads,latent,lens", [(16, 256, [20000, 3, 9000]), (70, 512, [12000, 0]),
+                                               (33, 256, [9999])])
+def test_paged_long_rows_in_many_parts(heads, latent, lens):
+    import row_top_selection_amd as dt
+
+    g = torch.Generator(DEV).manual_seed(heads)
+    page, pages = 64, 40
+    width = -(-max(lens) // page)
+    q, cache = make(g, len(lens), heads, latent, pages, page, "bf16")
+    table = torch.randint(0, pages, (len(lens), width), generator=g, device=DEV).to(torch.int32)
+    out, lse = dt.attend_paged(q, cache, i32(lens), table, latent, SCALE)
+    torch.cuda.synchronize()
+    picked = []
+    for b, n in enumerate(lens):
+        j = np.arange(n)
+        picked.append(table[b].cpu().numpy()[j // page] * page + j % page)
+    vectors = cache.view(-1, latent + 64)
+    want = serve_plain.attend(q, vectors, latent, SCALE, picked)
+    close(out, lse, want, logit_size(q, vectors, SCALE), latent + 64)
+
+
 def test_paged_pages_that_are_not_there():
     import row_top_selection_amd as dt
 

@@ -180,6 +180,63 @@ def test_scores_ragged(kind, rows, heads, dim):
     close_scores(got, want, size, dim + heads + 2)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp16", "fp8"])
+@pytest.mark.parametrize("heads,dim", [(8, 64), (40, 128), (70, 64)])
+def test_scores_of_many_rows_paged(kind, heads, dim):
+    """Batches whose workgroups go over several rows: tables that change inside
+    a group, rows that a tile does not reach, empty rows."""
+    import row_top_selection_amd as dt
+
+    g = torch.Generator(DEV).manual_seed(heads)
+    rng = np.random.default_rng(heads)
+    n, per, page, width = 1200, 2, 16, 44
+    rows = n * per
+    q, w, keys, scales = make(g, rows, heads, dim, (400, page), kind)
+    table = rng.integers(0, 400, (n, width))
+    lens = rng.integers(-1, width * page + 1, rows)
+    lens[rng.random(rows) < 0.3] = 0
+    out = dt.scores_paged(q, w, keys, i32(lens), i32(table), key_scales=scales,
+                          table_rows=i32(np.arange(rows) // per),
+                          out=torch.full((rows, width * page), -7.0, device=DEV))
+    torch.cuda.synchronize()
+    some = np.concatenate([np.arange(12), rng.permutation(rows)[:60], [rows - 1]])
+    windows = []
+    for b in some:
+        j = np.arange(max(0, lens[b]))
+        windows.append((0, table[b // per][j // page] * page + j % page))
+    want, size = serve_plain.scores(q[some], w[some], keys.view(-1, dim).float(),
+                                    None if scales is None else scales.view(-1), windows,
+                                    torch.full((len(some), width * page), -7.0))
+    close_scores(out[torch.as_tensor(some, device=DEV)], want, size, dim + heads + 2)
+    # every row, by the kernel itself a few rows at a time
+    for first in (0, 1111, rows - 7):
+        part = slice(first, first + 7)
+        few = dt.scores_paged(q[part], w[part], keys, i32(lens[part]), i32(table), key_scales=scales,
+                              table_rows=i32(np.arange(rows)[part] // per),
+                              out=torch.full((7, width * page), -7.0, device=DEV))
+        assert torch.equal(few, out[part])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+def test_scores_of_many_rows_ragged(kind):
+    import row_top_selection_amd as dt
+
+    g = torch.Generator(DEV).manual_seed(77)
+    rng = np.random.default_rng(77)
+    rows, total = 5000, 2100
+    q, w, keys, scales = make(g, rows, 16, 128, (total,), kind)
+    starts = np.sort(rng.integers(0, total, rows))
+    lens = np.minimum(rng.integers(-2, 900, rows), total - starts)
+    out = dt.scores_ragged(q, w, keys, i32(lens), i32(starts), key_scales=scales,
+                           out=torch.full((rows, total), 1e3, device=DEV))
+    torch.cuda.synchronize()
+    some = np.concatenate([np.arange(70), rng.permutation(rows)[:60], [rows - 1]])
+    windows = [(int(starts[b]), np.arange(starts[b], starts[b] + max(0, lens[b]))) for b in some]
+    want, size = serve_plain.scores(q[some], w[some], keys.float(), scales, windows,
+                                    torch.full((len(some), total), 1e3))
+    close_scores(out[torch.as_tensor(some, device=DEV)], want, size, 128 + 16 + 2)
+
+
 def test_scores_with_strided_inputs():
     import row_top_selection_amd as dt
 
