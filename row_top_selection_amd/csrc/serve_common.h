@@ -14,7 +14,6 @@ namespace dsatopk_serve {
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 fp16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 fp16x4 __attribute__((ext_vector_type(4)));
@@ -27,16 +26,12 @@ using lds_u32 = __attribute__((address_space(3))) uint32_t;
 using lds_i16x4 = __attribute__((address_space(3))) i16x4;
 using global_u32 = const __attribute__((address_space(1))) uint32_t;
 
-constexpr int kWave = 64;
-
 // A 16-bit float type's matrix instructions. In all of them lane l holds
 // row (A) or column (B) l % 32 (l % 16), and along the contraction the
 // lane group l / 32 (l / 16) holds consecutive elements; the result has
 // column l % 32 (l % 16) and rows 8 * (i / 4) + 4 * (l / 32) + i % 4
 // (4 * (l / 16) + i) in its i-th register.
 struct Bf16 {
-  using x4 = bf16x4;
-  using x8 = bf16x8;
   static __device__ __forceinline__ f32x16 mma32(u32x4 a, u32x4 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
                                                    __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
@@ -57,8 +52,6 @@ struct Bf16 {
 };
 
 struct Fp16 {
-  using x4 = fp16x4;
-  using x8 = fp16x8;
   static __device__ __forceinline__ f32x16 mma32(u32x4 a, u32x4 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(fp16x8, a),
                                                   __builtin_bit_cast(fp16x8, b), c, 0, 0, 0);
