@@ -7,6 +7,7 @@
 #include <Python.h>
 
 #include <ATen/hip/EmptyTensor.h>
+#include <c10/hip/HIPCachingAllocator.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -171,34 +172,62 @@ int32_t element_type(const at::Tensor& t, const char* name, bool fp8) {
   }
 }
 
-at::Tensor empty(at::IntArrayRef size, at::ScalarType type, const at::Tensor& like) {
-  return at::detail::empty_cuda(size, type, like.device(), c10::nullopt);
-}
-
-// Calls go to the tensors' device, and to its current stream unless one is given.
-struct On {
-  int before = -1, device;
+// Where a call goes: its tensors' device, and that device's current stream
+// unless one is given. A given stream is the current one while this lives, so
+// that what the call allocates is of that stream: memory that earlier work of
+// the current stream may still use is not written by the other, and a
+// workspace that the call frees goes back to work behind its kernels only.
+class On {
+ public:
   void* stream;
-  On(const at::Tensor& like, PyObject* given) : device(like.get_device()) {
-    if (given && given != Py_None) {
-      if (PyLong_Check(given)) {
-        stream = reinterpret_cast<void*>(PyLong_AsUnsignedLongLong(given));
-      } else {
-        PyObject* s = PyObject_GetAttrString(given, "cuda_stream");
-        if (!s) throw Failed{};
-        stream = reinterpret_cast<void*>(PyLong_AsUnsignedLongLong(s));
-        Py_DECREF(s);
-      }
-      if (PyErr_Occurred()) throw Failed{};
-    } else {
-      stream = c10::hip::getCurrentHIPStream((c10::DeviceIndex)device).stream();
-    }
+
+  On(const at::Tensor& like, PyObject* given)
+      : device_(like.get_device()),
+        before_(c10::hip::getCurrentHIPStream((c10::DeviceIndex)device_)) {
+    stream = given && given != Py_None ? handle(given) : before_.stream();
+    other_ = stream != before_.stream();
+    if (other_)
+      c10::hip::setCurrentHIPStream(
+          c10::hip::getStreamFromExternal((hipStream_t)stream, (c10::DeviceIndex)device_));
     int now = -1;
-    if (hipGetDevice(&now) == hipSuccess && now != device && hipSetDevice(device) == hipSuccess)
-      before = now;
+    if (hipGetDevice(&now) == hipSuccess && now != device_ && hipSetDevice(device_) == hipSuccess)
+      device_before_ = now;
   }
+  On(const On&) = delete;
+  On& operator=(const On&) = delete;
   ~On() {
-    if (before >= 0) (void)hipSetDevice(before);
+    if (other_) c10::hip::setCurrentHIPStream(before_);
+    if (device_before_ >= 0) (void)hipSetDevice(device_before_);
+  }
+
+  // What only this call uses.
+  at::Tensor room(int64_t bytes, const at::Tensor& like) const {
+    return at::detail::empty_cuda({bytes}, at::kByte, like.device(), c10::nullopt);
+  }
+  // What the caller gets, who may read and drop it on the stream that was current.
+  at::Tensor empty(at::IntArrayRef size, at::ScalarType type, const at::Tensor& like) const {
+    at::Tensor t = at::detail::empty_cuda(size, type, like.device(), c10::nullopt);
+    if (other_) c10::hip::HIPCachingAllocator::recordStream(t.storage().data_ptr(), before_);
+    return t;
+  }
+
+ private:
+  int device_, device_before_ = -1;
+  c10::hip::HIPStream before_;
+  bool other_;
+
+  static void* handle(PyObject* given) {
+    unsigned long long h;
+    if (PyLong_Check(given)) {
+      h = PyLong_AsUnsignedLongLong(given);
+    } else {
+      PyObject* s = PyObject_GetAttrString(given, "cuda_stream");
+      if (!s) throw Failed{};
+      h = PyLong_AsUnsignedLongLong(s);
+      Py_DECREF(s);
+    }
+    if (PyErr_Occurred()) throw Failed{};
+    return reinterpret_cast<void*>(h);
   }
 };
 
@@ -226,6 +255,7 @@ PyObject* page_maps(PyObject* const* args, Py_ssize_t n, PyObject* kw) {
   const int32_t tokens = integer32(a.at[4], "num_tokens");
   if (tokens < 0) refuse("num_tokens must not be negative");
   const int32_t* fresh = vector_or_null(a.at[5], requests, &lens, "new_lens");
+  const On on(lens, a.at[7]);
   static const char* const fields[] = {"token_starts", "slots", "table_rows", "row_lens", "counts"};
   const int64_t sizes[] = {requests + int64_t(1), tokens, tokens, tokens, 2};
   int32_t* to[5];
@@ -243,7 +273,7 @@ PyObject* page_maps(PyObject* const* args, Py_ssize_t n, PyObject* kw) {
     PyObject* made[5] = {};
     bool fine = true;
     for (int i = 0; i < 5; ++i) {
-      const at::Tensor t = empty({sizes[i]}, at::kInt, lens);
+      const at::Tensor t = on.empty({sizes[i]}, at::kInt, lens);
       to[i] = const_cast<int32_t*>(ints(t));
       made[i] = THPVariable_Wrap(t);
       fine = fine && made[i];
@@ -253,7 +283,6 @@ PyObject* page_maps(PyObject* const* args, Py_ssize_t n, PyObject* kw) {
     if (!out) throw Failed{};
   }
   try {
-    const On on(lens, a.at[7]);
     check_status(dsatopk_page_maps(ints(lens), fresh, requests, const_cast<int32_t*>(ints(tab)),
                                    row_stride(tab), size32(tab.size(1), "page_table"), page,
                                    ints(free), size32(free.size(0), "free_pages"), tokens, to[0],
@@ -288,10 +317,10 @@ struct Scores {
         refuse("key_scales must be float32, one per key");
     }
   }
-  at::Tensor out(PyObject* o, int64_t columns) const {
+  at::Tensor out(const On& on, PyObject* o, int64_t columns) const {
     // a top-k's score buffer: a row stride that is a multiple of 4
     if (!o || o == Py_None)
-      return empty({rows, std::max<int64_t>(4, (columns + 3) / 4 * 4)}, at::kFloat, q);
+      return on.empty({rows, std::max<int64_t>(4, (columns + 3) / 4 * 4)}, at::kFloat, q);
     const at::Tensor& t = shaped(o, 2, &q, "out");
     if (t.scalar_type() != at::kFloat || t.size(0) != rows)
       refuse("out must be float32 with " + std::to_string(rows) + " rows");
@@ -310,8 +339,8 @@ PyObject* scores_paged(PyObject* const* args, Py_ssize_t n, PyObject* kw) {
   if (!rows && tab.size(0) != s.rows)
     refuse("page_table must have one row per query row without table_rows");
   const int32_t page = size32(s.keys.size(1), "keys");
-  const at::Tensor out = s.out(a.at[7], tab.size(1) * page);
   const On on(s.q, a.at[8]);
+  const at::Tensor out = s.out(on, a.at[7], tab.size(1) * page);
   check_status(
       dsatopk_scores_paged(s.q.data_ptr(), stride(s.q, 0), stride(s.q, 1),
                            static_cast<const float*>(s.weights.data_ptr()), stride(s.weights, 0),
@@ -332,8 +361,8 @@ PyObject* scores_ragged(PyObject* const* args, Py_ssize_t n, PyObject* kw) {
   const Scores s(a.at[0], a.at[1], a.at[2], a.at[5], 2);
   const at::Tensor& lens = vector(a.at[3], s.rows, &s.q, "seq_lens");
   const at::Tensor& starts = vector(a.at[4], s.rows, &s.q, "row_starts");
-  const at::Tensor out = s.out(a.at[6], s.keys.size(0));
   const On on(s.q, a.at[7]);
+  const at::Tensor out = s.out(on, a.at[6], s.keys.size(0));
   check_status(
       dsatopk_scores_ragged(s.q.data_ptr(), stride(s.q, 0), stride(s.q, 1),
                             static_cast<const float*>(s.weights.data_ptr()), stride(s.weights, 0),
@@ -349,7 +378,7 @@ PyObject* scores_ragged(PyObject* const* args, Py_ssize_t n, PyObject* kw) {
 // Attention's results: out (q's type) of rows x heads x dim, lse (float32) of rows x heads.
 struct Results {
   at::Tensor out, lse;
-  Results(PyObject* o, PyObject* l, const at::Tensor& q, int64_t dim) {
+  Results(const On& on, PyObject* o, PyObject* l, const at::Tensor& q, int64_t dim) {
     if (o && o != Py_None) {
       out = tensor(o, "out");
       if (out.scalar_type() != q.scalar_type() || out.dim() != 3 || out.size(0) != q.size(0) ||
@@ -359,7 +388,7 @@ struct Results {
       on_device(out, &q, "out");
     } else {
       if (dim < 0) refuse("latent_dim must not be negative");
-      out = empty({q.size(0), q.size(1), dim}, q.scalar_type(), q);
+      out = on.empty({q.size(0), q.size(1), dim}, q.scalar_type(), q);
     }
     if (l && l != Py_None) {
       lse = tensor(l, "lse");
@@ -369,13 +398,13 @@ struct Results {
                std::to_string(q.size(1)) + ")");
       on_device(lse, &q, "lse");
     } else {
-      lse = empty({q.size(0), q.size(1)}, at::kFloat, q);
+      lse = on.empty({q.size(0), q.size(1)}, at::kFloat, q);
     }
   }
 };
 
 // The given workspace, or one of `need` bytes.
-at::Tensor workspace_of(PyObject* given, size_t need, const at::Tensor& q) {
+at::Tensor workspace_of(const On& on, PyObject* given, size_t need, const at::Tensor& q) {
   if (given && given != Py_None) {
     const at::Tensor& t = tensor(given, "workspace");
     if (t.scalar_type() != at::kByte || !t.is_contiguous())
@@ -383,7 +412,7 @@ at::Tensor workspace_of(PyObject* given, size_t need, const at::Tensor& q) {
     on_device(t, &q, "workspace");
     return t;
   }
-  return need ? empty({(int64_t)need}, at::kByte, q) : at::Tensor();
+  return need ? on.room((int64_t)need, q) : at::Tensor();
 }
 void* room_ptr(const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
 size_t room_bytes(const at::Tensor& t) { return t.defined() ? (size_t)t.numel() : 0; }
@@ -392,22 +421,24 @@ size_t room_bytes(const at::Tensor& t) { return t.defined() ? (size_t)t.numel() 
 struct Absorbed {
   const at::Tensor &q, &cache;
   int32_t type, rows, heads, latent;
+  On on;
   Results results;
   at::Tensor workspace;
-  Absorbed(PyObject* q_, PyObject* c_, PyObject* latent_, PyObject* out, PyObject* lse)
+  Absorbed(PyObject* q_, PyObject* c_, PyObject* latent_, PyObject* out, PyObject* lse, PyObject* stream)
       : q(shaped(q_, 3, nullptr, "q")),
         cache(shaped(c_, 3, &q, "cache")),
         type(element_type(q, "q", false)),
         rows(size32(q.size(0), "q")),
         heads(size32(q.size(1), "q")),
         latent(integer32(latent_, "latent_dim")),
-        results((check(), out), lse, q, latent) {}
+        on((check(), q), stream),
+        results(on, out, lse, q, latent) {}
   void check() const {
     if (cache.scalar_type() != q.scalar_type() || cache.size(2) != q.size(2))
       refuse("cache must have q's type and last dimension");
   }
   void room(PyObject* given, int64_t tokens) {
-    workspace = workspace_of(given, dsatopk_attend_bytes(rows, heads, latent, tokens), q);
+    workspace = workspace_of(on, given, dsatopk_attend_bytes(rows, heads, latent, tokens), q);
   }
 };
 
@@ -415,14 +446,13 @@ PyObject* attend_selected(PyObject* const* args, Py_ssize_t n, PyObject* kw) {
   static const char* const names[] = {"q", "cache", "slots", "latent_dim", "scale",
                                       "out", "lse", "workspace", "stream"};
   const Args<9> a("attend_selected", names, 5, args, n, kw);
-  Absorbed s(a.at[0], a.at[1], a.at[3], a.at[5], a.at[6]);
+  Absorbed s(a.at[0], a.at[1], a.at[3], a.at[5], a.at[6], a.at[8]);
   const at::Tensor& slots = shaped(a.at[2], 2, &s.q, "slots");
   if (slots.scalar_type() != at::kInt || slots.size(0) != s.rows)
     refuse("slots must be int32 with one row per query row");
   const int32_t k = size32(slots.size(1), "slots");
   const float scale = number(a.at[4], "scale");
   s.room(a.at[7], k);
-  const On on(s.q, a.at[8]);
   check_status(
       dsatopk_attend_selected(s.q.data_ptr(), stride(s.q, 0), stride(s.q, 1), s.cache.data_ptr(),
                               s.cache.size(0), stride(s.cache, 0), stride(s.cache, 1),
@@ -430,7 +460,7 @@ PyObject* attend_selected(PyObject* const* args, Py_ssize_t n, PyObject* kw) {
                               size32(s.q.size(2) - s.latent, "q"), scale, ints(slots),
                               row_stride(slots), k, s.rows, s.results.out.data_ptr(),
                               static_cast<float*>(s.results.lse.data_ptr()), room_ptr(s.workspace),
-                              room_bytes(s.workspace), on.stream),
+                              room_bytes(s.workspace), s.on.stream),
       "dsatopk_attend_selected");
   return pair(s.results.out, s.results.lse);
 }
@@ -439,7 +469,7 @@ PyObject* attend_paged(PyObject* const* args, Py_ssize_t n, PyObject* kw) {
   static const char* const names[] = {"q", "cache", "seq_lens", "page_table", "latent_dim", "scale",
                                       "table_rows", "max_seq_len", "out", "lse", "workspace", "stream"};
   const Args<12> a("attend_paged", names, 6, args, n, kw);
-  Absorbed s(a.at[0], a.at[1], a.at[4], a.at[8], a.at[9]);
+  Absorbed s(a.at[0], a.at[1], a.at[4], a.at[8], a.at[9], a.at[11]);
   const at::Tensor& lens = vector(a.at[2], s.rows, &s.q, "seq_lens");
   const int32_t* rows = vector_or_null(a.at[6], s.rows, &s.q, "table_rows");
   const at::Tensor& tab = table(a.at[3], &s.q);
@@ -449,7 +479,6 @@ PyObject* attend_paged(PyObject* const* args, Py_ssize_t n, PyObject* kw) {
   const int64_t longest =
       a.given(7) ? integer(a.at[7], "max_seq_len") : tab.size(1) * s.cache.size(1);
   s.room(a.at[10], longest);
-  const On on(s.q, a.at[11]);
   check_status(
       dsatopk_attend_paged(s.q.data_ptr(), stride(s.q, 0), stride(s.q, 1), s.cache.data_ptr(),
                            s.cache.size(0), stride(s.cache, 0), stride(s.cache, 1),
@@ -457,7 +486,7 @@ PyObject* attend_paged(PyObject* const* args, Py_ssize_t n, PyObject* kw) {
                            size32(s.q.size(2) - s.latent, "q"), scale, ints(lens), ints(tab),
                            row_stride(tab), size32(tab.size(1), "page_table"), rows, longest, s.rows,
                            s.results.out.data_ptr(), static_cast<float*>(s.results.lse.data_ptr()),
-                           room_ptr(s.workspace), room_bytes(s.workspace), on.stream),
+                           room_ptr(s.workspace), room_bytes(s.workspace), s.on.stream),
       "dsatopk_attend_paged");
   return pair(s.results.out, s.results.lse);
 }
@@ -484,12 +513,12 @@ PyObject* attend_expanded(PyObject* const* args, Py_ssize_t n, PyObject* kw) {
   const float scale = number(a.at[7], "scale");
   const int causal = a.at[8] ? PyObject_IsTrue(a.at[8]) : 1;
   if (causal < 0) throw Failed{};
-  const Results r(a.at[9], a.at[10], q, v.size(2));
+  const On on(q, a.at[12]);
+  const Results r(on, a.at[9], a.at[10], q, v.size(2));
   const int32_t requests = size32(qs.size(0) - 1, "q_starts"), heads = size32(q.size(1), "q");
   const int32_t queries = size32(q.size(0), "q"), keys = size32(k.size(0), "k");
   const at::Tensor room = workspace_of(
-      a.at[11], dsatopk_expanded_bytes(requests, heads, queries, keys, longest), q);
-  const On on(q, a.at[12]);
+      on, a.at[11], dsatopk_expanded_bytes(requests, heads, queries, keys, longest), q);
   check_status(
       dsatopk_attend_expanded(q.data_ptr(), stride(q, 0), stride(q, 1), k.data_ptr(), stride(k, 0),
                               stride(k, 1), v.data_ptr(), stride(v, 0), stride(v, 1),
@@ -538,7 +567,11 @@ Requests of seq_lens tokens after the step, new_lens of them new (None: one
 each), take the pages that they lack from free_pages: these are written into
 page_table in place. Returns PageMaps, whose slots, table_rows and row_lens
 have num_tokens rows (empty ones behind the step's tokens). out: a PageMaps
-to write into.)doc";
+to write into.
+
+stream (here and in the other calls): a stream, or its handle, to go to
+instead of the current one, as if it were the current one: inputs have to be
+ready on it, and what the call allocates is of it.)doc";
 
 const char scores_paged_doc[] = R"doc(scores_paged(q, weights, keys, seq_lens, page_table, key_scales=None, table_rows=None, out=None, stream=None)
 --
