@@ -427,8 +427,9 @@ int dsatopk_scores_ragged(const void* q, int64_t q_row_stride, int64_t q_head_st
  *                 one.
  *
  * Scores, softmax and sums are fp32; the softmax's weights are rounded to
- * `type` before the second product. The order of the sums is fixed: the
- * same inputs give the same bits.
+ * `type` before the second product: off by at most half a step, for
+ * DSATOPK_FP16 at least 2^-35 of the row's largest weight. The order of the
+ * sums is fixed: the same inputs give the same bits.
  *
  * Errors: DSATOPK_ERR_INVALID_ARG, DSATOPK_ERR_ALIGNMENT (q, cache or
  * workspace not 16-byte aligned, out not 8-byte aligned, a stride of q or

@@ -28,8 +28,10 @@
 // falls with what the matrix units switch: the same call on zeros takes 530
 // us.
 //
-// Weights are rounded to the inputs' type for the second product; scores,
-// maxima, sums and accumulators are fp32.
+// Weights are rounded to the inputs' type for the second product (off by at
+// most 2^-8 of each in bfloat16; in half precision by 2^-11 of each or 2^-35
+// of the row's largest, see kLift); scores, maxima, sums and accumulators are
+// fp32.
 
 #include "serve_common.h"
 
@@ -41,7 +43,6 @@ constexpr int kNope = 128, kRope = 64, kValue = 128;
 constexpr int kKeyBytes = kNope * 2, kRopeBytes = kRope * 2, kValueBytes = kValue * 2;
 constexpr int kSteps = (kNope + kRope) / 16;
 constexpr int kBlocks = kValue / 32;
-constexpr float kMost = 256.0f;  // of a lane's weights by a reference that is kept
 constexpr int64_t kMostStride = int64_t(1) << 27;  // of a key, in elements: 8 of them are 2^31 bytes
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -146,7 +147,7 @@ struct State {
   float top, sum;
 };
 
-// Weight i of scores s by the reference maximum `ref` (log2).
+// Weight i of scores s by the reference `ref` (log2).
 __device__ __forceinline__ float weight_of(const f32x16& s, int i, float scale2, float ref) {
   return exp2_fast(fmaf(s[i], scale2, -ref));
 }
@@ -209,7 +210,7 @@ __device__ __forceinline__ void keys_step(const ExpandParams& p, State& st, f32x
     for (int i = 0; i < 16; ++i)
       if (8 * (i / 4) + 4 * half + i % 4 >= seen) s[i] = -INFINITY;
   }
-  // The weights are taken by the reference maximum in use, which only has to
+  // The weights are taken by the reference in use, which only has to
   // be near enough: a lane's sum over kMost (or not a number) tells that it
   // is not, and the scores' maximum is looked for.
   f32x16 w;
@@ -231,11 +232,11 @@ __device__ __forceinline__ void keys_step(const ExpandParams& p, State& st, f32x
   u32x4 a[kAhead];
 #pragma unroll
   for (int n = 0; n < kAhead; ++n) a[n] = read(n);
-  if (__any(!(sum <= kMost) || st.top == -INFINITY)) {
+  if (__any(!(sum <= T::kMost) || st.top == -INFINITY)) {
     float top = s[0];
 #pragma unroll
     for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
-    const float to = fmaxf(st.top, fmaxf(top, other_half(top)) * p.scale2);
+    const float to = fmaxf(st.top, fmaxf(top, other_half(top)) * p.scale2 - T::kLift);
     const float by = st.top == -INFINITY ? 0.0f : exp2_fast(st.top - to);
     st.top = to;
     st.sum *= by;

@@ -17,7 +17,7 @@
 // latent' P' (the order of tokens along that contraction is free, and is
 // taken as S' leaves it). O' has a head in each lane too: rescaling it is a
 // multiplication by the lane's own factor, done only where weights outgrow
-// the reference maximum in use by 2^8. The A operand of O' needs the
+// the reference in use (by 2^8; kMost of the type). The A operand of O' needs the
 // tile by columns; the LDS column reads give it from the same tile that the
 // rows were read from.
 //
@@ -36,9 +36,10 @@
 // and overlap in part. 128 decode rows of 128 heads take 120 us (2.8 TB/s), 8 rows
 // of 131072 tokens and 16 heads 238 us: 5.1 TB/s, as fast as memory copies.
 //
-// Weights are rounded to the inputs' 16-bit type for the second product
-// (off by at most 2^-8 or 2^-11 of each, of either sign); scores, maxima, sums and
-// both products' accumulators are fp32.
+// Weights are rounded to the inputs' 16-bit type for the second product (off
+// by at most 2^-8 of each in bfloat16; in half precision by 2^-11 of each or
+// 2^-35 of the row's largest, see kLift); scores, maxima, sums and both
+// products' accumulators are fp32.
 
 #include "serve_common.h"
 
@@ -48,7 +49,6 @@ namespace {
 constexpr int kRope = 64;
 constexpr int kRopeBytes = kRope * 2;
 constexpr int kFewSplits = 4;  // joined in one go
-constexpr float kMost = 256.0f;  // of a lane's weights by a reference that is kept
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -171,7 +171,7 @@ __device__ __forceinline__ void copy_tokens(char* tile, uint64_t at, int place, 
 template <class P>
 struct State {
   f32x4 o[P::kBlocks];
-  float top, sum;  // the reference maximum (log2), this lane's part of the sum
+  float top, sum;  // the reference (log2), this lane's part of the sum
 };
 
 // Scores, weights and sums of the wave's next P::kGo * 16 tokens, from tile row
@@ -242,7 +242,7 @@ __device__ __forceinline__ void attend_tokens(State<P>& st, const u32x4 (&q)[P::
     return v;
   };
 
-  // The weights, by the reference maximum in use. It only has to be near
+  // The weights, by the reference in use. It only has to be near
   // enough: a lane's sum over kMost (or not a number) tells that it is not,
   // as no row's maximum is looked for otherwise.
   float w[kGo][4], sum;
@@ -258,13 +258,13 @@ __device__ __forceinline__ void attend_tokens(State<P>& st, const u32x4 (&q)[P::
       }
   };
   weigh();
-  if (__any(!(sum <= kMost) || st.top == -INFINITY)) {
+  if (__any(!(sum <= T::kMost) || st.top == -INFINITY)) {
     float top = s[0][0];
 #pragma unroll
     for (int x = 0; x < kGo; ++x)
 #pragma unroll
       for (int i = 0; i < 4; ++i) top = fmaxf(top, s[x][i]);
-    const float to = fmaxf(st.top, head_max(top) * scale2);
+    const float to = fmaxf(st.top, head_max(top) * scale2 - T::kLift);
     const float by = st.top == -INFINITY ? 0.0f : exp2_fast(st.top - to);
     st.top = to;
     st.sum *= by;

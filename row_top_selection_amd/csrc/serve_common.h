@@ -26,12 +26,27 @@ using lds_u32 = __attribute__((address_space(3))) uint32_t;
 using lds_i16x4 = __attribute__((address_space(3))) i16x4;
 using global_u32 = const __attribute__((address_space(1))) uint32_t;
 
+// How attention scales its softmax's weights before it rounds them to a 16-bit
+// type: by a reference 2^kLift below a maximum of the row's scores, which is
+// kept until a lane's weights add up to more than kMost. bfloat16 has fp32's
+// exponents, so that every weight is off by at most 2^-8 of itself wherever
+// it lies. Half precision ends 14 (with fewer bits: 24) binary orders below 1
+// and 16 above: weights up to kMost, its largest number, stay finite, and one is
+// off by at most 2^-11 of itself or 2^-25, half of the last step, where that is
+// more: 2^-35 of the row's largest weight, which is 2^kLift at least. From 1
+// down it would lose bits of weights 10 nats below the maximum, and all of
+// those 18 below, which can be most of an output: many tokens beside one of
+// large score and small value.
+constexpr float kBf16Lift = 0.0f, kBf16Most = 256.0f;
+constexpr float kFp16Lift = 10.0f, kFp16Most = 65504.0f;
+
 // A 16-bit float type's matrix instructions. In all of them lane l holds
 // row (A) or column (B) l % 32 (l % 16), and along the contraction the
 // lane group l / 32 (l / 16) holds consecutive elements; the result has
 // column l % 32 (l % 16) and rows 8 * (i / 4) + 4 * (l / 32) + i % 4
 // (4 * (l / 16) + i) in its i-th register.
 struct Bf16 {
+  static constexpr float kLift = kBf16Lift, kMost = kBf16Most;
   static __device__ __forceinline__ f32x16 mma32(u32x4 a, u32x4 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
                                                    __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
@@ -52,6 +67,7 @@ struct Bf16 {
 };
 
 struct Fp16 {
+  static constexpr float kLift = kFp16Lift, kMost = kFp16Most;
   static __device__ __forceinline__ f32x16 mma32(u32x4 a, u32x4 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(fp16x8, a),
                                                   __builtin_bit_cast(fp16x8, b), c, 0, 0, 0);
