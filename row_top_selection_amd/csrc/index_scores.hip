@@ -151,7 +151,7 @@ struct ByteHeads {
 // the products of the second, but three waves a SIMD do better at that than
 // two with 64 more registers (886 against 922 us for 4 x 1024 rows of 64
 // heads over 16384 keys each).
-template <int kKind, int kDim, int kHeads>
+template <int kKind, int kDim, int kHeads, bool kWhole>
 __device__ __forceinline__ void row_sums(const ScoreParams& p, const char* __restrict__ heads,
                                          const float* __restrict__ weights,
                                          char* __restrict__ next, int32_t next_row, int wave,
@@ -174,6 +174,16 @@ __device__ __forceinline__ void row_sums(const ScoreParams& p, const char* __res
 #pragma unroll
       for (int n = 0; n < 2; ++n) acc[n] = product<kKind>(a, key[n][s], acc[n]);
     }
+    // Zeros stand in for heads that the row does not have: an infinite key
+    // makes no number of them. (Kernels of their own for kHeads heads, which have
+    // no such test in the loop: 879 us for the rows above, and 901 with it. A
+    // loop over whole slabs with the rest behind it costs the decode rows
+    // of 64 heads their third wave a SIMD: 63 and 68 us.)
+    if (!kWhole && slab * 32 + 32 > p.heads) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (slab * 32 + 8 * (i / 4) + 4 * half + i % 4 >= p.heads) acc[0][i] = acc[1][i] = 0.0f;
+    }
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
       const f32x4 w = *reinterpret_cast<const f32x4*>(&weights[slab * 32 + 8 * x + 4 * half]);
@@ -186,7 +196,8 @@ __device__ __forceinline__ void row_sums(const ScoreParams& p, const char* __res
   }
 }
 
-template <int kKind, int kDim, int kHeads, bool kPaged>
+// kWhole: the row has kHeads heads, not fewer.
+template <int kKind, int kDim, int kHeads, bool kWhole, bool kPaged>
 __global__ __launch_bounds__(kBlock, 2) void scores_kernel(ScoreParams p) {
   using S = Shape<kKind, kDim>;
   constexpr int kBytes = S::kBytes;
@@ -282,8 +293,8 @@ __global__ __launch_bounds__(kBlock, 2) void scores_kernel(ScoreParams p) {
       if constexpr (kKind == DSATOPK_FP8) bytes.load(p, r0 + next, tid);
     }
     float sum[2] = {0.0f, 0.0f};
-    row_sums<kKind, kDim, kHeads>(p, heads_lds[buf], w_lds[buf], heads_lds[buf ^ 1],
-                                  next >= 0 ? r0 + next : -1, wave, lane, key, sum);
+    row_sums<kKind, kDim, kHeads, kWhole>(p, heads_lds[buf], w_lds[buf], heads_lds[buf ^ 1],
+                                          next >= 0 ? r0 + next : -1, wave, lane, key, sum);
     if (next >= 0) {
       if constexpr (kKind == DSATOPK_FP8) bytes.store(p, heads_lds[buf ^ 1], tid);
       if (tid < kHeads) w_lds[buf ^ 1][tid] = weight;
@@ -302,8 +313,11 @@ __global__ __launch_bounds__(kBlock, 2) void scores_kernel(ScoreParams p) {
 
 template <int kKind, int kDim, int kHeads>
 int launch_heads(const ScoreParams& p, bool paged, dim3 grid, void* stream) {
-  return paged ? launch(scores_kernel<kKind, kDim, kHeads, true>, grid, dim3(kBlock), p, stream)
-               : launch(scores_kernel<kKind, kDim, kHeads, false>, grid, dim3(kBlock), p, stream);
+  const auto kernel = p.heads == kHeads ? paged ? scores_kernel<kKind, kDim, kHeads, true, true>
+                                                : scores_kernel<kKind, kDim, kHeads, true, false>
+                      : paged           ? scores_kernel<kKind, kDim, kHeads, false, true>
+                                        : scores_kernel<kKind, kDim, kHeads, false, false>;
+  return launch(kernel, grid, dim3(kBlock), p, stream);
 }
 
 template <int kKind, int kDim>
