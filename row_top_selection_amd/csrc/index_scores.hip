@@ -234,16 +234,17 @@ __global__ __launch_bounds__(kBlock, 2) void scores_kernel(ScoreParams p) {
 
   u32x4 key[2][S::kSteps];
   float scale[2] = {1.0f, 1.0f};
+  bool there[2] = {true, true};  // the lane's tokens have a key
   auto load_keys = [&](int64_t table_row) {
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
       const int32_t j = jw + n * 32 + col;
       const char* src = zero_row();
-      scale[n] = 0.0f;
       if constexpr (kPaged) {
         const int32_t e = j >> p.page_bits, in = j & ((1 << p.page_bits) - 1);
         const int32_t page = e < p.table_width ? p.table[table_row * p.table_stride + e] : -1;
-        if (page >= 0 && page < p.num_pages) {
+        there[n] = page >= 0 && page < p.num_pages;
+        if (there[n]) {
           src = p.keys + page * p.key_page + in * p.key_token;
           scale[n] = p.scales ? p.scales[page * p.scale_page + in] : 1.0f;
         }
@@ -300,8 +301,12 @@ __global__ __launch_bounds__(kBlock, 2) void scores_kernel(ScoreParams p) {
       if (tid < kHeads) w_lds[buf ^ 1][tid] = weight;
     }
     // both halves' heads; then lane l keeps token l of the wave's 64
-    const float t0 = (sum[0] + other_half(sum[0])) * scale[0];
-    const float t1 = (sum[1] + other_half(sum[1])) * scale[1];
+    float t0 = (sum[0] + other_half(sum[0])) * scale[0];
+    float t1 = (sum[1] + other_half(sum[1])) * scale[1];
+    if constexpr (kPaged) {  // 0 without a key, whatever the row holds
+      t0 = there[0] ? t0 : 0.0f;
+      t1 = there[1] ? t1 : 0.0f;
+    }
     const int32_t j = jw + lane;
     if (j >= __builtin_amdgcn_readlane(lo, at) && j < __builtin_amdgcn_readlane(hi, at))
       p.out[(r0 + at) * p.out_stride + j] = half ? t1 : t0;
