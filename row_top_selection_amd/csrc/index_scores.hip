@@ -354,9 +354,11 @@ int run_scores(ScoreParams p, int32_t type, int32_t dim, bool paged, void* strea
   }
 }
 
-// What both forms check. Strides come in elements.
+// What both forms check. Strides come in elements. What has no entries (no
+// pages or tokens, no columns) may be null.
 int check_scores(const void* q, int64_t q_row, int64_t q_head, const float* weights,
-                 int64_t w_row, const void* keys, int64_t key_token, const int32_t* seq_lens,
+                 int64_t w_row, const void* keys, int64_t num_keys, int64_t key_token,
+                 const int32_t* seq_lens,
                  int32_t type, int32_t heads, int32_t dim, int32_t rows, const float* out,
                  int64_t out_stride, int64_t columns) {
   if (rows < 0 || heads < 1 || heads > kMaxHeads || (dim != 64 && dim != 128) ||
@@ -364,7 +366,8 @@ int check_scores(const void* q, int64_t q_row, int64_t q_head, const float* weig
       out_stride < columns || q_row < 0 || q_head < 0 || key_token < 0 || w_row < 0)
     return DSATOPK_ERR_INVALID_ARG;
   if (rows == 0) return DSATOPK_OK;
-  if (!q || !weights || !keys || !seq_lens || !out) return DSATOPK_ERR_INVALID_ARG;
+  if (!q || !weights || (num_keys && !keys) || !seq_lens || (columns && !out))
+    return DSATOPK_ERR_INVALID_ARG;
   const int64_t size = type == DSATOPK_FP8 ? 1 : 2;
   if (!aligned16(q) || !aligned16(keys) || (q_row * size) % 16 || (q_head * size) % 16 ||
       (key_token * size) % 16 || !aligned4(out) || !aligned4(weights))
@@ -389,7 +392,7 @@ int dsatopk_scores_paged(const void* q, int64_t q_row_stride, int64_t q_head_str
                          int32_t num_rows, float* out, int64_t out_stride, int64_t columns,
                          void* stream) {
   const int st = check_scores(q, q_row_stride, q_head_stride, weights, weight_stride, keys,
-                              key_token_stride, seq_lens, type, num_heads, head_dim, num_rows,
+                              num_pages, key_token_stride, seq_lens, type, num_heads, head_dim, num_rows,
                               out, out_stride, columns);
   if (st != DSATOPK_OK || num_rows == 0) return st;
   if (!page_table || page_table_width < 1 || page_table_stride < page_table_width ||
@@ -432,7 +435,7 @@ int dsatopk_scores_ragged(const void* q, int64_t q_row_stride, int64_t q_head_st
                           const int32_t* seq_lens, const int32_t* row_starts, int32_t num_rows,
                           float* out, int64_t out_stride, int64_t columns, void* stream) {
   const int st = check_scores(q, q_row_stride, q_head_stride, weights, weight_stride, keys,
-                              key_stride, seq_lens, type, num_heads, head_dim, num_rows, out,
+                              num_keys, key_stride, seq_lens, type, num_heads, head_dim, num_rows, out,
                               out_stride, columns);
   if (st != DSATOPK_OK || num_rows == 0) return st;
   if (!row_starts || num_keys < 0) return DSATOPK_ERR_INVALID_ARG;

@@ -1,0 +1,47 @@
+"""Tensors without entries in the serving operators: torch gives them a null
+pointer, which is no error where nothing of them is read."""
+import numpy as np
+import pytest
+import torch
+
+import row_top_selection_amd as dt
+from tests.test_serve_refusals import RAGGED, call
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return dt.lib()
+
+
+def test_no_keys_are_no_error(lib):
+    # nothing is launched: there is no column to write
+    assert call(lib.dsatopk_scores_ragged, RAGGED, dict(n=0, keys=None)) == 0
+    assert call(lib.dsatopk_scores_ragged, RAGGED, dict(n=0, keys=None, out=None, columns=0, out_stride=0)) == 0
+    assert call(lib.dsatopk_scores_ragged, RAGGED, dict(keys=None)) == 1
+    assert call(lib.dsatopk_scores_ragged, RAGGED, dict(out=None)) == 1
+
+
+def i32(v):
+    return torch.as_tensor(np.asarray(v, dtype=np.int32)).cuda()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float8_e4m3fn])
+def test_scores_of_an_empty_cache(kind):
+    q, w = torch.ones(3, 64, 128, device="cuda").to(kind), torch.ones(3, 64, device="cuda")
+    scales = torch.ones(0, 16, device="cuda")
+    out = torch.full((3, 64), 5.0, device="cuda")
+    for s in (None, scales):
+        got = dt.scores_paged(q, w, torch.ones(0, 16, 128, device="cuda").to(kind), i32([0, 64, 9]), i32(np.zeros((3, 4))),
+                              key_scales=s, out=out.clone())
+        # pages that are not there score 0
+        want = torch.full((3, 64), 5.0, device="cuda")
+        want[1], want[2, :9] = 0.0, 0.0
+        assert torch.equal(got, want)
+    for s in (None, scales[:, 0].contiguous()):
+        got = dt.scores_ragged(q, w, torch.ones(0, 128, device="cuda").to(kind), i32([0, 7, 9]), i32([0, 0, 3]),
+                               key_scales=s, out=out.clone())
+        assert torch.equal(got, out)
+    assert dt.scores_ragged(q, w, torch.ones(0, 128, device="cuda").to(kind), i32([0] * 3), i32([0] * 3)).shape[0] == 3
+    none = torch.empty(3, 0, device="cuda")
+    assert dt.scores_ragged(q, w, torch.ones(8, 128, device="cuda").to(kind), i32([8] * 3), i32([0] * 3), out=none) is none
