@@ -201,7 +201,8 @@ extern "C" int dsatopk_page_maps(const int32_t* seq_lens, const int32_t* new_len
   if (num_requests < 0 || num_free < 0 || num_tokens < 0 || num_tokens > (1 << 30) || page_table_width < 0 ||
       page_table_stride < page_table_width || !pow2(page_size) || page_size > (1 << 20))
     return DSATOPK_ERR_INVALID_ARG;
-  if (!token_starts || !counts || (num_requests && (!seq_lens || !page_table)) ||
+  if (!token_starts || !counts || (num_requests && !seq_lens) ||
+      (num_requests && page_table_width && !page_table) ||
       (num_free && !free_pages) || (num_tokens && (!slots || !table_rows || !row_lens)))
     return DSATOPK_ERR_INVALID_ARG;
   MapParams p{};

@@ -45,3 +45,17 @@ def test_scores_of_an_empty_cache(kind):
     assert dt.scores_ragged(q, w, torch.ones(0, 128, device="cuda").to(kind), i32([0] * 3), i32([0] * 3)).shape[0] == 3
     none = torch.empty(3, 0, device="cuda")
     assert dt.scores_ragged(q, w, torch.ones(8, 128, device="cuda").to(kind), i32([8] * 3), i32([0] * 3), out=none) is none
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("requests", [1, 3])
+def test_page_maps_of_a_table_without_columns(requests):
+    """Every new token is past the table's width: counted, without a slot."""
+    from tests import serve_plain
+
+    lens, free = [5, 0, 9][:requests], np.arange(20)
+    table = torch.empty(requests, 0, dtype=torch.int32, device="cuda")
+    got = dt.page_maps(i32(lens), table, 4, i32(free), 16, new_lens=i32(lens))
+    want = serve_plain.page_maps(lens, lens, np.zeros((requests, 0)), 4, free, 16)
+    for name in ("token_starts", "slots", "table_rows", "row_lens", "counts"):
+        assert getattr(got, name).tolist() == list(want[name]), name
