@@ -25,6 +25,15 @@ PyObject* g_page_maps;  // PageMaps
 
 struct Failed {};  // a Python error is set
 
+// A reference of one's own.
+struct Ref {
+  PyObject* is;
+  explicit Ref(PyObject* o) : is(o) {}
+  Ref(const Ref&) = delete;
+  Ref& operator=(const Ref&) = delete;
+  ~Ref() { Py_XDECREF(is); }
+};
+
 [[noreturn]] void refuse(const std::string& what) {
   PyErr_SetString(PyExc_ValueError, what.c_str());
   throw Failed{};
@@ -259,13 +268,14 @@ PyObject* page_maps(PyObject* const* args, Py_ssize_t n, PyObject* kw) {
   static const char* const fields[] = {"token_starts", "slots", "table_rows", "row_lens", "counts"};
   const int64_t sizes[] = {requests + int64_t(1), tokens, tokens, tokens, 2};
   int32_t* to[5];
+  at::Tensor given[5];  // an attribute may be made when it is asked for, and be nobody else's
   PyObject* out = nullptr;
   if (a.given(6)) {
     for (int i = 0; i < 5; ++i) {
-      PyObject* o = PyObject_GetAttrString(a.at[6], fields[i]);
-      if (!o) throw Failed{};
-      Py_DECREF(o);  // `out` keeps it
-      to[i] = const_cast<int32_t*>(ints(vector(o, sizes[i], &lens, fields[i])));
+      const Ref o(PyObject_GetAttrString(a.at[6], fields[i]));
+      if (!o.is) throw Failed{};
+      given[i] = vector(o.is, sizes[i], &lens, fields[i]);
+      to[i] = const_cast<int32_t*>(ints(given[i]));
     }
     out = a.at[6];
     Py_INCREF(out);

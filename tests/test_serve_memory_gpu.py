@@ -1,0 +1,46 @@
+"""What page_maps holds and lets go of."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+def i32(v):
+    return torch.as_tensor(np.asarray(v, dtype=np.int32)).cuda()
+
+
+FIELDS = ("token_starts", "slots", "table_rows", "row_lens", "counts")
+
+
+def test_outputs_that_are_made_when_asked_for_are_held():
+    """Fields of `out` that nobody else holds: all are alive until the call is
+    made, so that no two of them are one block."""
+    import row_top_selection_amd as dt
+
+    sizes, at = (2, 64, 64, 64, 2), {}
+
+    class Made:
+        def __getattr__(self, name):
+            t = torch.zeros(sizes[FIELDS.index(name)], dtype=torch.int32, device="cuda")
+            at[name] = t.data_ptr()
+            return t
+
+    out = Made()
+    got = dt.page_maps(i32([40]), i32([[3]]), 64, i32([1]), 64, new_lens=i32([40]), out=out)
+    torch.cuda.synchronize()
+    assert got is out and len(set(at.values())) == 5
+
+
+def test_a_field_that_does_not_fit_is_refused():
+    import row_top_selection_amd as dt
+
+    args = (i32([40]), i32([[3]]), 64, i32([1]), 64)
+    out = dt.page_maps(*args)
+    for name in FIELDS:
+        with pytest.raises(ValueError, match=name):
+            dt.page_maps(*args, out=out._replace(**{name: i32([0] * 9)}))
+        with pytest.raises(ValueError, match=name):
+            dt.page_maps(*args, out=out._replace(**{name: None}))
+    with pytest.raises(AttributeError):
+        dt.page_maps(*args, out=out[:3])
