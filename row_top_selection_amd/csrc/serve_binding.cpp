@@ -267,42 +267,35 @@ PyObject* page_maps(PyObject* const* args, Py_ssize_t n, PyObject* kw) {
   const On on(lens, a.at[7]);
   static const char* const fields[] = {"token_starts", "slots", "table_rows", "row_lens", "counts"};
   const int64_t sizes[] = {requests + int64_t(1), tokens, tokens, tokens, 2};
-  int32_t* to[5];
-  at::Tensor given[5];  // an attribute may be made when it is asked for, and be nobody else's
-  PyObject* out = nullptr;
+  // Held until the call is made: an attribute of `out` may be made when it is
+  // asked for, and be nobody else's.
+  at::Tensor to[5];
+  for (int i = 0; i < 5; ++i) {
+    if (!a.given(6)) {
+      to[i] = on.empty({sizes[i]}, at::kInt, lens);
+      continue;
+    }
+    const Ref o(PyObject_GetAttrString(a.at[6], fields[i]));
+    if (!o.is) throw Failed{};
+    to[i] = vector(o.is, sizes[i], &lens, fields[i]);
+  }
+  auto at = [&](int i) { return const_cast<int32_t*>(ints(to[i])); };
+  check_status(dsatopk_page_maps(ints(lens), fresh, requests, const_cast<int32_t*>(ints(tab)),
+                                 row_stride(tab), size32(tab.size(1), "page_table"), page,
+                                 ints(free), size32(free.size(0), "free_pages"), tokens, at(0),
+                                 at(1), at(2), at(3), at(4), on.stream),
+               "dsatopk_page_maps");
   if (a.given(6)) {
-    for (int i = 0; i < 5; ++i) {
-      const Ref o(PyObject_GetAttrString(a.at[6], fields[i]));
-      if (!o.is) throw Failed{};
-      given[i] = vector(o.is, sizes[i], &lens, fields[i]);
-      to[i] = const_cast<int32_t*>(ints(given[i]));
-    }
-    out = a.at[6];
-    Py_INCREF(out);
-  } else {
-    PyObject* made[5] = {};
-    bool fine = true;
-    for (int i = 0; i < 5; ++i) {
-      const at::Tensor t = on.empty({sizes[i]}, at::kInt, lens);
-      to[i] = const_cast<int32_t*>(ints(t));
-      made[i] = THPVariable_Wrap(t);
-      fine = fine && made[i];
-    }
-    if (fine) out = PyObject_Vectorcall(g_page_maps, made, 5, nullptr);
-    for (PyObject* o : made) Py_XDECREF(o);
-    if (!out) throw Failed{};
+    Py_INCREF(a.at[6]);
+    return a.at[6];
   }
-  try {
-    check_status(dsatopk_page_maps(ints(lens), fresh, requests, const_cast<int32_t*>(ints(tab)),
-                                   row_stride(tab), size32(tab.size(1), "page_table"), page,
-                                   ints(free), size32(free.size(0), "free_pages"), tokens, to[0],
-                                   to[1], to[2], to[3], to[4], on.stream),
-                 "dsatopk_page_maps");
-  } catch (...) {
-    Py_DECREF(out);
-    throw;
-  }
-  return out;
+  const Ref made[5] = {Ref(THPVariable_Wrap(to[0])), Ref(THPVariable_Wrap(to[1])),
+                       Ref(THPVariable_Wrap(to[2])), Ref(THPVariable_Wrap(to[3])),
+                       Ref(THPVariable_Wrap(to[4]))};
+  PyObject* fields_of[5];
+  for (int i = 0; i < 5; ++i)
+    if (!(fields_of[i] = made[i].is)) throw Failed{};
+  return PyObject_Vectorcall(g_page_maps, fields_of, 5, nullptr);
 }
 
 struct Scores {

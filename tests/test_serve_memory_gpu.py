@@ -44,3 +44,22 @@ def test_a_field_that_does_not_fit_is_refused():
             dt.page_maps(*args, out=out._replace(**{name: None}))
     with pytest.raises(AttributeError):
         dt.page_maps(*args, out=out[:3])
+
+
+def test_outputs_of_a_failed_allocation_are_given_back():
+    import row_top_selection_amd as dt
+
+    lens, table, free = i32([4]), i32([[0]]), i32([1])
+    dt.page_maps(lens, table, 64, free, 4)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    before = torch.cuda.memory_allocated()
+    room = torch.cuda.memory_reserved() + (3 << 30)
+    torch.cuda.set_per_process_memory_fraction(room / torch.cuda.get_device_properties(0).total_memory)
+    try:
+        with pytest.raises(RuntimeError, match="out of memory"):
+            dt.page_maps(lens, table, 64, free, 1 << 29)  # outputs of 2 GB: the first fits
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    assert torch.cuda.memory_allocated() == before
+    torch.cuda.empty_cache()
