@@ -9,11 +9,12 @@
 #include <ATen/hip/EmptyTensor.h>
 #include <c10/hip/HIPCachingAllocator.h>
 #include <c10/hip/HIPStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
+#include <exception>
 #include <initializer_list>
-#include <stdexcept>
 #include <string>
 
 #include "dsatopk.h"
@@ -535,16 +536,15 @@ PyObject* attend_expanded(PyObject* const* args, Py_ssize_t n, PyObject* kw) {
   return pair(r.out, r.lse);
 }
 
-// No C++ exception leaves a call.
+// No C++ exception leaves a call: torch's become the Python errors that its own
+// calls raise.
 template <PyObject* (*fn)(PyObject* const*, Py_ssize_t, PyObject*)>
 PyObject* guarded(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
   try {
     return fn(args, n, kw);
   } catch (const Failed&) {
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
   } catch (...) {
-    PyErr_SetString(PyExc_RuntimeError, "unknown failure");
+    torch::translate_exception_to_python(std::current_exception());
   }
   return nullptr;
 }

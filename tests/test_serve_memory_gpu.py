@@ -63,3 +63,17 @@ def test_outputs_of_a_failed_allocation_are_given_back():
         torch.cuda.set_per_process_memory_fraction(1.0)
     assert torch.cuda.memory_allocated() == before
     torch.cuda.empty_cache()
+
+
+def test_out_of_memory_is_torchs_error():
+    import row_top_selection_amd as dt
+
+    lens, table, free = i32([4]), i32([[0]]), i32([1])
+    torch.cuda.empty_cache()
+    room = torch.cuda.memory_reserved() + (1 << 30)
+    torch.cuda.set_per_process_memory_fraction(room / torch.cuda.get_device_properties(0).total_memory)
+    try:
+        with pytest.raises(torch.OutOfMemoryError):
+            dt.page_maps(lens, table, 64, free, 1 << 29)
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
