@@ -7,6 +7,7 @@
 #include <Python.h>
 
 #include <ATen/hip/EmptyTensor.h>
+#include <c10/core/AutogradState.h>
 #include <c10/hip/HIPCachingAllocator.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -85,7 +86,14 @@ struct Args {
 
 const at::Tensor& tensor(PyObject* o, const char* name) {
   if (!THPVariable_Check(o)) refuse(std::string(name) + " must be a tensor");
-  return THPVariable_Unpack(o);
+  const at::Tensor& t = THPVariable_Unpack(o);
+  // results would be without their history, and without a word
+  const c10::AutogradState& state = c10::AutogradState::get_tls_state();
+  if ((state.get_grad_mode() && t.requires_grad()) ||
+      (state.get_fw_grad_mode() && t._fw_grad(/*level=*/0).defined()))
+    refuse(std::string(name) + " has gradients to keep, which this call does not compute (detach it, or "
+                               "call under torch.no_grad())");
+  return t;
 }
 
 int64_t integer(PyObject* o, const char* name) {
@@ -574,7 +582,8 @@ to write into.
 
 stream (here and in the other calls): a stream, or its handle, to go to
 instead of the current one, as if it were the current one: inputs have to be
-ready on it, and what the call allocates is of it.)doc";
+ready on it, and what the call allocates is of it. None of the calls has a
+gradient: tensors that require one are refused where gradients are recorded.)doc";
 
 const char scores_paged_doc[] = R"doc(scores_paged(q, weights, keys, seq_lens, page_table, key_scales=None, table_rows=None, out=None, stream=None)
 --
