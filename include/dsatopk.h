@@ -416,7 +416,8 @@ int dsatopk_scores_ragged(const void* q, int64_t q_row_stride, int64_t q_head_st
  *   num_heads     1 .. 1024; latent_dim 256 or 512; rope_dim 64.
  *   scale         finite and above 0.
  *   slots         int32 [num_rows, k], rows slot_stride apart.
- *   max_seq_len   an upper bound on seq_lens. It sets how the tokens are
+ *   max_seq_len   an upper bound on seq_lens, at most 2^31 - 65 (rows of a
+ *                 larger table are cut there). It sets how the tokens are
  *                 split over workgroups (and the workspace's size); longer
  *                 rows are read whole all the same.
  *   out           type [num_rows, num_heads, latent_dim], contiguous.

@@ -13,7 +13,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
-#include <cmath>
+#include <algorithm>
 #include <exception>
 #include <initializer_list>
 #include <string>
@@ -488,8 +488,10 @@ PyObject* attend_paged(PyObject* const* args, Py_ssize_t n, PyObject* kw) {
   if (!rows && tab.size(0) != s.rows)
     refuse("page_table must have one row per query row without table_rows");
   const float scale = number(a.at[5], "scale");
+  // a table may have more positions than the largest bound, 2^31 - 65
   const int64_t longest =
-      a.given(7) ? integer(a.at[7], "max_seq_len") : tab.size(1) * s.cache.size(1);
+      a.given(7) ? integer(a.at[7], "max_seq_len")
+                 : std::min<int64_t>(tab.size(1) * s.cache.size(1), INT32_MAX - 64);
   s.room(a.at[10], longest);
   check_status(
       dsatopk_attend_paged(s.q.data_ptr(), stride(s.q, 0), stride(s.q, 1), s.cache.data_ptr(),
@@ -623,7 +625,7 @@ Absorbed latent attention over the first seq_lens positions of each row's
 page table.
 
 Arguments as for attend_selected and paged(); max_seq_len bounds seq_lens (the
-table's width when None) and sets how rows are split.)doc";
+table's positions when None) and sets how rows are split.)doc";
 
 const char attend_expanded_doc[] = R"doc(attend_expanded(q, k, v, k_rope, q_starts, k_starts, max_queries, scale, causal=True, out=None, lse=None, workspace=None, stream=None)
 --

@@ -59,3 +59,15 @@ def test_page_maps_of_a_table_without_columns(requests):
     want = serve_plain.page_maps(lens, lens, np.zeros((requests, 0)), 4, free, 16)
     for name in ("token_starts", "slots", "table_rows", "row_lens", "counts"):
         assert getattr(got, name).tolist() == list(want[name]), name
+
+
+@pytest.mark.gpu
+def test_a_table_of_more_positions_than_a_row_may_have():
+    """2048 pages of 2^20 tokens: no row is that long, and the call's default
+    bound on the rows is no reason to refuse it."""
+    cache = torch.zeros(1, 1 << 20, 320, dtype=torch.bfloat16, device="cuda")
+    cache[0, :9, 3] = 2.0
+    q = torch.zeros(1, 4, 320, dtype=torch.bfloat16, device="cuda")
+    table = torch.zeros(1, 2048, dtype=torch.int32, device="cuda")
+    out, lse = dt.attend_paged(q, cache, i32([9]), table, 256, 0.1)
+    assert (out[..., 3] == 2).all() and (lse - np.log(9)).abs().max() < 1e-6
