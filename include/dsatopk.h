@@ -359,7 +359,10 @@ int dsatopk_page_maps(const int32_t* seq_lens, const int32_t* new_lens, int32_t 
  *   out           float [num_rows, >= columns], rows out_stride apart; a
  *                 top-k's score buffer (for it: 16-byte aligned, out_stride
  *                 a multiple of 4).
- *   columns       at most 2^30.
+ *   columns       at most 2^30. The work is shared out by columns (and the
+ *                 table's positions, if fewer), not by seq_lens: a call on a
+ *                 table or buffer much wider than its longest row is slower
+ *                 than on their first columns.
  *
  * A page outside [0, num_pages) reads as keys of score 0. Products are
  * exact, sums are fp32.

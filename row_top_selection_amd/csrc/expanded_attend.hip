@@ -23,8 +23,8 @@
 // Few rows of many keys are split over workgroups by keys; a second kernel
 // joins the parts.
 //
-// 4 x 1024 queries behind 15360 earlier tokens, 16 heads: 615 us, 1.08 PFLOP/s
-// (a large library product of random numbers reaches 1.36 here). The clock
+// 4 x 1024 queries behind 15360 earlier tokens, 16 heads: 620 us, 1.07 PFLOP/s
+// (a large library product of random numbers reaches 1.37 here). The clock
 // falls with what the matrix units switch: the same call on zeros takes 530
 // us.
 //
@@ -428,7 +428,11 @@ __global__ __launch_bounds__(kJoinBlock) void expand_join_kernel(ExpandParams p)
 
 // Workgroups of a batch, and the parts that its keys are cut into: where four
 // waves a workgroup leave half the card's places (two a CU) empty, as many
-// as fill them, of 512 keys at least by the requests' mean.
+// as fill them, of 512 keys at least by the requests' mean. Measured with
+// 256 / 512 / 1024 keys at least (us): 2 x 164 queries over 4906 keys each, one
+// head, 33 / 28 / 41; 8 over 8200, four heads, 29 / 27 / 36; one over 20000, 42 /
+// 40 / 39; 1500 over 13500, one head, 163 / 135 / 118; but 4 x 64 over 2064, two
+// heads, 18 / 23 / 34 and 8 x 32 over 1532, one head, 17 / 27 / 41.
 struct Cut {
   int64_t pairs;
   int32_t longest, splits;
@@ -439,7 +443,12 @@ Cut cut_of(int32_t requests, int32_t heads, int32_t queries, int32_t keys, int32
   c.pairs = ((int64_t)requests * heads + 7) / 8 * 8;
   c.longest = max_queries < queries ? max_queries : queries;
   // Eight waves where they fill the card's 256 CUs, if all prompts are of the
-  // longest's length.
+  // longest's length. Measured with eight waves and with four (us): 4 x 1024
+  // queries behind 15360 earlier tokens, 16 heads (256 workgroups of eight) 619
+  // and 668; 2 x 1024 (128) 490 and 346; uneven prompts of up to 777 (240) 42
+  // and 33, of up to 1500 (480) 115 and 114. Of the two, the rule takes the slower
+  // for 3 x 1024 (192: 517 and 566) and where a last workgroup is mostly empty:
+  // 4 x 300 behind 4096, 64 heads, 350 and 308.
   c.wide = c.pairs * (c.longest / 256) >= 256;
   const int64_t groups = (int64_t)requests * heads * ((c.longest + 127) / 128);
   int64_t s = groups > 0 ? 512 / groups : 1;

@@ -18,8 +18,9 @@
 // buffered, copied there without passing through registers). Keys are read
 // once per row group, and again only where the table row changes.
 //
-// 128 rows over 8192 paged keys each (bf16, 64 heads): 63 us, 4.4 TB/s, bound
-// by memory. 4 x 1024 rows over 16384 keys each (e4m3, 64 heads): 870 us, 1.23
+// 128 rows over 8192 paged keys each (bf16, 64 heads): 62 us, 4.4 TB/s, bound
+// by memory, with a table and a score buffer as wide as the rows (wider ones:
+// see run_scores). 4 x 1024 rows over 16384 keys each (e4m3, 64 heads): 870 us, 1.23
 // PFLOP/s, bound by the matrix units (each 32 x 32 tile's 8 products also need
 // 32 vector instructions for the weighting, which other waves' products hide).
 
@@ -336,7 +337,14 @@ int run_scores(ScoreParams p, int32_t type, int32_t dim, bool paged, void* strea
   const int64_t tiles = ((int64_t)p.columns + kTile - 1) / kTile;
   if (tiles == 0) return DSATOPK_OK;
   // Rows a workgroup: enough workgroups to fill the card come first, then
-  // keys read for as many rows as possible, up to a lane for each.
+  // keys read for as many rows as possible, up to a lane for each. With 1024 /
+  // 2048 / 4096 as enough (us): 128 rows of 8192 paged keys 69 / 64 / 64, of two
+  // and four rows a request 82 / 76 / 76 and 106 / 100 / 99 (in a group of
+  // one row each reads its request's keys for itself); 256 rows over
+  // 16384 keys 74 / 75 / 80, 1024 over 4096 69 / 70 / 75, 4096 over 16384 868 to 870.
+  // The rows' lengths are on the device: what counts here is the buffer's and the
+  // table's width, and in ones much wider than the rows few of the groups have work.
+  // The 128 rows of 8192 in a table of 131072 take 228 us instead of 64.
   constexpr int64_t kEnough = 2048, kMostY = 65535;
   int64_t group = p.rows * tiles / kEnough;
   group = group < 1 ? 1 : group > 64 ? 64 : group;

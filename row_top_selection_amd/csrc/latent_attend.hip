@@ -32,9 +32,10 @@
 // with tiles of 64 tokens), for more heads one of eight.
 //
 // 1024 prompt rows of 2048 slots and 64 heads (out of 4 x 16384 tokens) take
-// 342 us, 0.85 PFLOP/s: copies and products each take about 300 by themselves
-// and overlap in part. 128 decode rows of 128 heads take 120 us (2.8 TB/s), 8 rows
-// of 131072 tokens and 16 heads 238 us: 5.1 TB/s, as fast as memory copies.
+// 347 us, 0.84 PFLOP/s: copies and products each take about 300 by themselves
+// and overlap in part. 128 decode rows of 128 heads take 117 us (2.9 TB/s), 8 rows
+// of 131072 tokens and 16 heads 238 us: 5.1 TB/s, where sums along the rows of a
+// 4 GB matrix read 6.2.
 //
 // Weights are rounded to the inputs' 16-bit type for the second product (off
 // by at most 2^-8 of each in bfloat16; in half precision by 2^-11 of each or

@@ -14,8 +14,8 @@
 // thread, and computes the running sums over the requests itself, kRequests
 // at a time in LDS, up to those of its tokens. A second launch that waited for shared sums would cost more
 // than the lengths' re-reading from L2 (8 bytes a request and workgroup).
-// 128 requests of one new token: 4.8 us on the GPU, latency alone; half a
-// million tokens of 256 requests: 7.8 us (0.8 TB/s), where the running sums and the
+// 128 requests of one new token: 4.7 us on the GPU, latency alone; half a
+// million tokens of 256 requests: 7.5 us (0.8 TB/s), where the running sums and the
 // search in front of each thread's four tokens take most.
 
 #include "serve_common.h"

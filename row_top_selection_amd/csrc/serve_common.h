@@ -127,7 +127,8 @@ __device__ __forceinline__ u32x2 read_columns(const char* lds) {
 }
 
 // Where row t of an LDS tile keeps its 16-byte chunk c: chunk c ^ swizzle of
-// t, so that no instruction's lanes share one of the 64 banks (256 bytes).
+// t, so that the lanes of a read share none of the 64 banks (256 bytes). (The stores
+// of the scores' widened 8-bit heads do: a fifth of that kernel's LDS cycles.)
 // Each has 16 different values over 16 rows, for row reads (16 lanes: 16
 // rows, one chunk), and more than that for column reads:
 //   swizzle16: rows 8a .. 8a + 7 differ in bits 1 .. 3, for 32 lanes that
