@@ -339,8 +339,7 @@ int run_scores(ScoreParams p, int32_t type, int32_t dim, bool paged, void* strea
   // Rows a workgroup: enough workgroups to fill the card come first, then
   // keys read for as many rows as possible, up to a lane for each. With 1024 /
   // 2048 / 4096 as enough (us): 128 rows of 8192 paged keys 69 / 64 / 64, of two
-  // and four rows a request 82 / 76 / 76 and 106 / 100 / 99 (in a group of
-  // one row each reads its request's keys for itself); 256 rows over
+  // and four rows a request 82 / 76 / 76 and 106 / 100 / 99; 256 rows over
   // 16384 keys 74 / 75 / 80, 1024 over 4096 69 / 70 / 75, 4096 over 16384 868 to 870.
   // The rows' lengths are on the device: what counts here is the buffer's and the
   // table's width, and in ones much wider than the rows few of the groups have work.
