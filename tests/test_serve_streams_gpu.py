@@ -191,3 +191,18 @@ def test_two_threads_with_streams_of_their_own():
     for t in threads:
         t.join()
     assert not wrong
+
+
+@pytest.mark.parametrize("what", CALLS)
+def test_the_default_stream_given_while_another_is_current(what):
+    call, _ = what(torch.Generator(DEV).manual_seed(6))
+    want = [t.clone() for t in as_tuple(call())]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        for stream in (0, torch.cuda.default_stream()):
+            got = as_tuple(call(stream=stream))
+            assert torch.cuda.current_stream() == side
+            assert all(owner(t) == 0 for t in got)
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
