@@ -84,7 +84,7 @@ enum {
 enum {
     DSATOPK_BF16 = 0, /* bfloat16 */
     DSATOPK_FP16 = 1, /* IEEE half */
-    DSATOPK_FP8 = 2   /* e4m3 without infinities (OCP), scores only */
+    DSATOPK_FP8 = 2   /* e4m3 without infinities (OCP), the indexer only */
 };
 
 /* Human-readable name of a status code (static string, never NULL). */
@@ -282,8 +282,8 @@ int dsatopk_paged_noalloc(const float* scores, int64_t score_stride, const int32
                           int32_t k, int32_t* out, void* stream);
 
 /* ------------------------------------------------------------------------
- * The serving operators around the selection: page maps, indexer scores and
- * latent attention. The conventions above hold for them too (device
+ * The serving operators around the selection: page maps, cache writes, indexer
+ * scores and latent attention. The conventions above hold for them too (device
  * pointers, asynchronous, no allocation, only kernel launches). Strides are
  * in elements; a tensor's last dimension is contiguous. Every call reads
  * inputs at its stated bounds only: page numbers and slots outside a cache
@@ -335,6 +335,108 @@ int dsatopk_page_maps(const int32_t* seq_lens, const int32_t* new_lens, int32_t 
                       int32_t page_size, const int32_t* free_pages, int32_t num_free,
                       int32_t num_tokens, int32_t* token_starts, int32_t* slots,
                       int32_t* table_rows, int32_t* row_lens, int32_t* counts, void* stream);
+
+/*
+ * dsatopk_append_latent - a step's new latent vectors into the paged cache,
+ * their rotary part turned by their positions, and the queries' rotary parts
+ * with them:
+ *
+ *   y[t][0 : latent_dim] = x[t] * weight / sqrt(mean(x[t]^2) + eps)  (over the
+ *                          latent part; weight NULL: as it is)
+ *   y[t][latent_dim :]   = the pairs (a, b) of x[t][latent_dim :], each as
+ *                          (a cos - b sin, a sin + b cos)
+ *
+ * with the cosines and sines of position row_lens[t] - 1. Slots and windows
+ * are dsatopk_page_maps' slots and row_lens.
+ *
+ *   latent        type [num_tokens, latent_dim + rope_dim], rows latent_stride
+ *                 apart.
+ *   slots         int32 [num_tokens]: page * page_size + offset, none twice (a
+ *                 slot of two tokens holds parts of either).
+ *   row_lens      int32 [num_tokens]: the token's position + 1.
+ *                 A token whose slot is outside the cache, or whose position
+ *                 is outside [0, num_positions), is not cached; without a
+ *                 position its rotary parts are not turned.
+ *   num_tokens    at most 2^30.
+ *   cos_sin       float [num_positions, rope_dim], rows cos_sin_stride apart:
+ *                 a position's rope_dim / 2 cosines, then as many sines.
+ *   interleaved   pair i is elements 2i and 2i + 1 of the rotary part if not
+ *                 0, i and i + rope_dim / 2 if 0.
+ *   weight        float [latent_dim] or NULL; eps finite, not negative.
+ *   type          DSATOPK_BF16 or DSATOPK_FP16.
+ *   latent_dim    256 or 512; rope_dim 64.
+ *   cache         type [num_pages, page_size, latent_dim + rope_dim], strides
+ *                 page_stride, token_stride, as dsatopk_attend_paged reads it.
+ *   out           type [num_tokens, latent_dim + rope_dim] or NULL: also
+ *                 receives y, of every token (for a prompt's keys and values).
+ *                 May be latent itself.
+ *   q_rope        type [num_tokens, num_heads, rope_dim], the rotary parts of
+ *                 the queries, strides q_row_stride, q_head_stride;
+ *   q_out         type, of the same shape, receives them turned. May be q_rope
+ *                 itself (with its strides), and must not overlap it otherwise.
+ *   num_heads     0 (no queries: q_rope and q_out are not looked at) .. 1024.
+ *
+ * Computed in fp32 and rounded once. Errors: DSATOPK_ERR_INVALID_ARG,
+ * DSATOPK_ERR_ALIGNMENT (a pointer not 16-byte aligned, a stride no multiple
+ * of 16 bytes), DSATOPK_ERR_HIP. num_tokens == 0 is a no-op.
+ */
+int dsatopk_append_latent(const void* latent, int64_t latent_stride, const int32_t* slots,
+                          const int32_t* row_lens, int32_t num_tokens, const float* cos_sin,
+                          int64_t cos_sin_stride, int32_t num_positions, int32_t interleaved,
+                          const float* weight, float eps, int32_t type, int32_t latent_dim,
+                          int32_t rope_dim, void* cache, int64_t num_pages, int64_t page_stride,
+                          int64_t token_stride, int32_t page_size, void* out, int64_t out_stride,
+                          const void* q_rope, int64_t q_row_stride, int64_t q_head_stride,
+                          void* q_out, int64_t q_out_row_stride, int64_t q_out_head_stride,
+                          int32_t num_heads, void* stream);
+
+/*
+ * dsatopk_append_index - a step's new indexer keys into their cache, as
+ * dsatopk_scores_paged reads it, and the indexer's queries made ready with
+ * them:
+ *
+ *   y = (x - mean x) / sqrt(var x + eps) * weight + bias   (keys only; weight
+ *       and bias NULL: as it is), then the first rope_dim elements turned as
+ *       by dsatopk_append_latent.
+ *   index_type = type:         y, rounded.
+ *   index_type = DSATOPK_FP8:  s = max |y| / 448 (of at least 2^-100), and
+ *       y / s rounded to e4m3. A key's s goes to its place of key_scales; a
+ *       query's into its head's weight, weights_out = weights * s.
+ *
+ *   keys          type [num_tokens, head_dim], rows key_stride apart.
+ *   slots, row_lens, num_tokens, cos_sin, num_positions, interleaved
+ *                 as for dsatopk_append_latent; rope_dim 64.
+ *   weight, bias  float [head_dim], both or neither.
+ *   type          DSATOPK_BF16 or DSATOPK_FP16 (keys and q).
+ *   head_dim      64 or 128.
+ *   index_keys    index_type [num_pages, page_size, head_dim], strides
+ *                 page_stride, token_stride.
+ *   key_scales    float [num_pages, page_size], pages scale_page_stride apart
+ *                 (DSATOPK_FP8 only).
+ *   q             type [num_tokens, num_heads, head_dim];
+ *   q_out         index_type, of the same shape. With 16 bits it may be q
+ *                 itself (with its strides), and must not overlap it otherwise.
+ *   weights       float [num_tokens, num_heads], rows weight_stride apart;
+ *   weights_out   the same, rows weight_out_stride apart, may be weights itself
+ *                 (both DSATOPK_FP8 only).
+ *   num_heads     0 (no queries) .. 128.
+ *
+ * What becomes 8 bits has to be finite. Computed in fp32 and rounded once.
+ * Errors: DSATOPK_ERR_INVALID_ARG, DSATOPK_ERR_ALIGNMENT (a pointer not 16-byte
+ * aligned, key_scales and weights not 4-byte; a stride no multiple of 16
+ * bytes), DSATOPK_ERR_HIP. num_tokens == 0 is a no-op.
+ */
+int dsatopk_append_index(const void* keys, int64_t key_stride, const int32_t* slots,
+                         const int32_t* row_lens, int32_t num_tokens, const float* cos_sin,
+                         int64_t cos_sin_stride, int32_t num_positions, int32_t rope_dim,
+                         int32_t interleaved, const float* weight, const float* bias, float eps,
+                         int32_t type, int32_t head_dim, void* index_keys, int32_t index_type,
+                         int64_t num_pages, int64_t page_stride, int64_t token_stride,
+                         int32_t page_size, float* key_scales, int64_t scale_page_stride,
+                         const void* q, int64_t q_row_stride, int64_t q_head_stride, void* q_out,
+                         int64_t q_out_row_stride, int64_t q_out_head_stride, const float* weights,
+                         int64_t weight_stride, float* weights_out, int64_t weight_out_stride,
+                         int32_t num_heads, void* stream);
 
 /*
  * dsatopk_scores_paged - the indexer's scores over a paged key cache:

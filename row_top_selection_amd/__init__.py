@@ -30,7 +30,8 @@ NOALLOC_MAX_ROWS = 262144
 
 EXPORTS = ("dsatopk_status_string", "dsatopk_plan_bytes", "dsatopk_plan", "dsatopk_plan_error",
            "dsatopk_paged", "dsatopk_paged_packed", "dsatopk_ragged", "dsatopk_paged_noalloc",
-           "dsatopk_page_maps", "dsatopk_scores_paged", "dsatopk_scores_ragged",
+           "dsatopk_page_maps", "dsatopk_append_latent", "dsatopk_append_index",
+           "dsatopk_scores_paged", "dsatopk_scores_ragged",
            "dsatopk_attend_bytes", "dsatopk_attend_selected", "dsatopk_attend_paged",
            "dsatopk_attend_expanded", "dsatopk_expanded_bytes")
 
@@ -78,13 +79,21 @@ def _lib():
         lib.dsatopk_page_maps.argtypes = [P, P, i32, P, i64, i32, i32, P, i32, i32, P, P, P, P, P,
                                           P]
         lib.dsatopk_page_maps.restype = ctypes.c_int
+        f32 = ctypes.c_float
+        lib.dsatopk_append_latent.argtypes = [P, i64, P, P, i32, P, i64, i32, i32, P, f32, i32, i32,
+                                              i32, P, i64, i64, i64, i32, P, i64, P, i64, i64, P,
+                                              i64, i64, i32, P]
+        lib.dsatopk_append_latent.restype = ctypes.c_int
+        lib.dsatopk_append_index.argtypes = [P, i64, P, P, i32, P, i64, i32, i32, i32, P, P, f32,
+                                             i32, i32, P, i32, i64, i64, i64, i32, P, i64, P, i64,
+                                             i64, P, i64, i64, P, i64, P, i64, i32, P]
+        lib.dsatopk_append_index.restype = ctypes.c_int
         lib.dsatopk_scores_paged.argtypes = [P, i64, i64, P, i64, P, i64, i64, i64, P, i64, i32,
                                              i32, i32, P, P, i64, i32, i32, P, i32, P, i64, i64, P]
         lib.dsatopk_scores_paged.restype = ctypes.c_int
         lib.dsatopk_scores_ragged.argtypes = [P, i64, i64, P, i64, P, i64, i64, P, i32, i32, i32,
                                               P, P, i32, P, i64, i64, P]
         lib.dsatopk_scores_ragged.restype = ctypes.c_int
-        f32 = ctypes.c_float
         lib.dsatopk_attend_bytes.argtypes = [i32, i32, i32, i64]
         lib.dsatopk_attend_bytes.restype = sz
         lib.dsatopk_attend_selected.argtypes = [P, i64, i64, P, i64, i64, i64, i32, i32, i32, i32,
@@ -324,7 +333,7 @@ def expanded_bytes(num_requests: int, num_heads: int, num_queries: int, num_keys
 
 
 # The serving operators' calls (csrc/serve_binding.cpp), loaded at first use.
-_SERVE = ("page_maps", "scores_paged", "scores_ragged", "attend_selected", "attend_paged",
+_SERVE = ("page_maps", "append_latent", "append_index", "scores_paged", "scores_ragged", "attend_selected", "attend_paged",
           "attend_expanded")
 
 

@@ -12,7 +12,7 @@ from pathlib import Path
 PKG = Path(__file__).resolve().parent
 ROOT = PKG.parent
 SOURCES = [PKG / "csrc" / name for name in (
-    "dsatopk.hip", "page_maps.hip", "index_scores.hip", "latent_attend.hip",
+    "dsatopk.hip", "page_maps.hip", "append_cache.hip", "index_scores.hip", "latent_attend.hip",
     "expanded_attend.hip")]
 HEADERS = [PKG / "csrc" / "select_device.h", PKG / "csrc" / "serve_common.h",
            ROOT / "include" / "dsatopk.h"]

@@ -307,6 +307,164 @@ PyObject* page_maps(PyObject* const* args, Py_ssize_t n, PyObject* kw) {
   return PyObject_Vectorcall(g_page_maps, fields_of, 5, nullptr);
 }
 
+// What both cache writes know of the tokens.
+struct Tokens {
+  const at::Tensor &slots, &lens, &angles;
+  int32_t count, positions;
+  float eps;
+  int near;
+  Tokens(const at::Tensor& x, PyObject* slots_, PyObject* lens_, PyObject* angles_, PyObject* eps_, PyObject* near_)
+      : slots(vector(slots_, x.size(0), &x, "slots")),
+        lens(vector(lens_, x.size(0), &x, "row_lens")),
+        angles(shaped(angles_, 2, &x, "cos_sin")),
+        count(size32(x.size(0), "slots")),
+        positions(size32(angles.size(0), "cos_sin")),
+        eps(eps_ ? number(eps_, "eps") : 1e-6f),
+        near(near_ ? PyObject_IsTrue(near_) : 0) {
+    if (near < 0) throw Failed{};
+    if (angles.scalar_type() != at::kFloat || angles.size(1) != 64)
+      refuse("cos_sin must be float32 [positions, 64]");
+  }
+};
+
+// A contiguous float32 vector of length n, or null.
+const float* floats_or_null(PyObject* o, int64_t n, const at::Tensor& like, const char* name) {
+  if (!o || o == Py_None) return nullptr;
+  const at::Tensor& t = tensor(o, name);
+  if (t.scalar_type() != at::kFloat || t.dim() != 1 || t.size(0) != n || !t.is_contiguous())
+    refuse(std::string(name) + " must be a contiguous float32 vector of length " + std::to_string(n));
+  on_device(t, &like, name);
+  return static_cast<const float*>(t.data_ptr());
+}
+
+// The caller's output of x's shape, or a new one.
+at::Tensor result_like(const On& on, PyObject* o, const at::Tensor& x, at::ScalarType type, const char* name) {
+  if (!o || o == Py_None) return on.empty(x.sizes(), type, x);
+  const at::Tensor& t = shaped(o, (int)x.dim(), &x, name);
+  if (t.scalar_type() != type || t.sizes() != x.sizes())
+    refuse(std::string(name) + " does not have the type and shape of what it is to hold");
+  return t;
+}
+
+// A written tensor's rows must not share memory.
+void apart(const at::Tensor& t, const char* name) {
+  for (int64_t d = 0; d + 1 < t.dim(); ++d)
+    if (t.size(d) > 1 && t.stride(d) < t.size(t.dim() - 1))
+      refuse(std::string(name) + " must not be expanded: it is written");
+}
+
+PyObject* append_latent(PyObject* const* args, Py_ssize_t n, PyObject* kw) {
+  static const char* const names[] = {"latent", "cache", "slots", "row_lens", "cos_sin", "weight", "eps",
+                                      "q_rope", "q_out", "out", "interleaved", "stream"};
+  const Args<12> a("append_latent", names, 5, args, n, kw);
+  const at::Tensor& x = shaped(a.at[0], 2, nullptr, "latent");
+  const int32_t type = element_type(x, "latent", false);
+  const at::Tensor& cache = shaped(a.at[1], 3, &x, "cache");
+  if (cache.scalar_type() != x.scalar_type() || cache.size(2) != x.size(1))
+    refuse("cache must have latent's type and last dimension");
+  apart(cache, "cache");
+  const Tokens t(x, a.at[2], a.at[3], a.at[4], a.at[6], a.at[10]);
+  const int32_t dim = size32(x.size(1) - 64, "latent");
+  const float* weight = floats_or_null(a.at[5], dim, x, "weight");
+  const On on(x, a.at[11]);
+  const at::Tensor* q = nullptr;
+  at::Tensor q_out, out;
+  if (a.given(7)) {
+    q = &shaped(a.at[7], 3, &x, "q_rope");
+    if (q->scalar_type() != x.scalar_type() || q->size(0) != x.size(0) || q->size(2) != 64)
+      refuse("q_rope must have latent's type and shape (" + std::to_string(x.size(0)) + ", heads, 64)");
+    q_out = result_like(on, a.at[8], *q, q->scalar_type(), "q_out");
+    apart(q_out, "q_out");
+  } else if (a.given(8)) {
+    refuse("q_out is for q_rope");
+  }
+  if (a.given(9)) {
+    out = result_like(on, a.at[9], x, x.scalar_type(), "out");
+    apart(out, "out");
+  }
+  check_status(
+      dsatopk_append_latent(
+          x.data_ptr(), stride(x, 0), ints(t.slots), ints(t.lens), t.count,
+          static_cast<const float*>(t.angles.data_ptr()), row_stride(t.angles), t.positions, t.near, weight,
+          t.eps, type, dim, 64, cache.data_ptr(), cache.size(0), stride(cache, 0), stride(cache, 1),
+          size32(cache.size(1), "cache"), out.defined() ? out.data_ptr() : nullptr,
+          out.defined() ? stride(out, 0) : 0, q ? q->data_ptr() : nullptr, q ? stride(*q, 0) : 0,
+          q ? stride(*q, 1) : 0, q ? q_out.data_ptr() : nullptr, q ? stride(q_out, 0) : 0,
+          q ? stride(q_out, 1) : 0, q ? size32(q->size(1), "q_rope") : 0, on.stream),
+      "dsatopk_append_latent");
+  if (!q) Py_RETURN_NONE;
+  return THPVariable_Wrap(q_out);
+}
+
+PyObject* append_index(PyObject* const* args, Py_ssize_t n, PyObject* kw) {
+  static const char* const names[] = {"keys", "index_keys", "slots", "row_lens", "cos_sin", "key_scales",
+                                      "weight", "bias", "eps", "q", "weights", "q_out", "weights_out",
+                                      "interleaved", "stream"};
+  const Args<15> a("append_index", names, 5, args, n, kw);
+  const at::Tensor& x = shaped(a.at[0], 2, nullptr, "keys");
+  const int32_t type = element_type(x, "keys", false);
+  const at::Tensor& cache = shaped(a.at[1], 3, &x, "index_keys");
+  const int32_t to = element_type(cache, "index_keys", true);
+  if ((to != DSATOPK_FP8 && to != type) || cache.size(2) != x.size(1))
+    refuse("index_keys must be float8_e4m3fn or of keys' type, with keys' last dimension");
+  apart(cache, "index_keys");
+  const Tokens t(x, a.at[2], a.at[3], a.at[4], a.at[8], a.at[13]);
+  const at::Tensor* scales = nullptr;
+  if (a.given(5)) {
+    scales = &shaped(a.at[5], 2, &x, "key_scales");
+    if (to != DSATOPK_FP8 || scales->scalar_type() != at::kFloat ||
+        scales->sizes() != cache.sizes().slice(0, 2))
+      refuse("key_scales must be float32, one per key, of float8_e4m3fn index_keys");
+    apart(*scales, "key_scales");
+  } else if (to == DSATOPK_FP8) {
+    refuse("float8_e4m3fn index_keys need key_scales");
+  }
+  const float* weight = floats_or_null(a.at[6], x.size(1), x, "weight");
+  const float* bias = floats_or_null(a.at[7], x.size(1), x, "bias");
+  if (!weight != !bias) refuse("weight and bias are given together");
+  const On on(x, a.at[14]);
+  const at::Tensor *q = nullptr, *weights = nullptr;
+  at::Tensor q_out, weights_out;
+  if (a.given(9)) {
+    q = &shaped(a.at[9], 3, &x, "q");
+    if (q->scalar_type() != x.scalar_type() || q->size(0) != x.size(0) || q->size(2) != x.size(1))
+      refuse("q must have keys' type and shape (" + std::to_string(x.size(0)) + ", heads, " +
+             std::to_string(x.size(1)) + ")");
+    q_out = result_like(on, a.at[11], *q, cache.scalar_type(), "q_out");
+    apart(q_out, "q_out");
+    if (to == DSATOPK_FP8) {
+      if (!a.given(10)) refuse("8-bit queries need weights");
+      weights = &shaped(a.at[10], 2, &x, "weights");
+      if (weights->scalar_type() != at::kFloat || weights->size(0) != q->size(0) || weights->size(1) != q->size(1))
+        refuse("weights must be float32 of shape (" + std::to_string(q->size(0)) + ", " +
+               std::to_string(q->size(1)) + ")");
+      weights_out = result_like(on, a.at[12], *weights, at::kFloat, "weights_out");
+      apart(weights_out, "weights_out");
+    }
+  }
+  if ((a.given(10) || a.given(12)) && !weights) refuse("weights and weights_out are for 8-bit queries");
+  if (a.given(11) && !q) refuse("q_out is for q");
+  check_status(
+      dsatopk_append_index(
+          x.data_ptr(), stride(x, 0), ints(t.slots), ints(t.lens), t.count,
+          static_cast<const float*>(t.angles.data_ptr()), row_stride(t.angles), t.positions, 64, t.near,
+          weight, bias, t.eps, type, size32(x.size(1), "keys"), cache.data_ptr(), to, cache.size(0),
+          stride(cache, 0), stride(cache, 1), size32(cache.size(1), "index_keys"),
+          scales ? static_cast<float*>(scales->data_ptr()) : nullptr, scales ? stride(*scales, 0) : 0,
+          q ? q->data_ptr() : nullptr, q ? stride(*q, 0) : 0, q ? stride(*q, 1) : 0,
+          q ? q_out.data_ptr() : nullptr, q ? stride(q_out, 0) : 0, q ? stride(q_out, 1) : 0,
+          weights ? static_cast<const float*>(weights->data_ptr()) : nullptr,
+          weights ? stride(*weights, 0) : 0,
+          weights ? static_cast<float*>(weights_out.data_ptr()) : nullptr,
+          weights ? stride(weights_out, 0) : 0, q ? size32(q->size(1), "q") : 0, on.stream),
+      "dsatopk_append_index");
+  if (!q) Py_RETURN_NONE;
+  if (weights) return pair(q_out, weights_out);
+  const Ref made(THPVariable_Wrap(q_out));
+  if (!made.is) throw Failed{};
+  return PyTuple_Pack(2, made.is, Py_None);
+}
+
 struct Scores {
   const at::Tensor &q, &weights, &keys;
   const at::Tensor* scales = nullptr;
@@ -587,6 +745,36 @@ instead of the current one, as if it were the current one: inputs have to be
 ready on it, and what the call allocates is of it. None of the calls has a
 gradient: tensors that require one are refused where gradients are recorded.)doc";
 
+const char append_latent_doc[] = R"doc(append_latent(latent, cache, slots, row_lens, cos_sin, weight=None, eps=1e-6, q_rope=None, q_out=None, out=None, interleaved=False, stream=None)
+--
+
+New tokens' latent vectors into the paged cache, normalised and turned.
+
+latent [tokens, latent_dim + 64] in bfloat16 or float16, as the projection
+leaves it: its latent part is divided by its root mean square and multiplied
+by weight (float32 [latent_dim]; None: left as it is), its last 64 elements are
+turned by the angles of position row_lens - 1 (cos_sin float32 [positions, 64]:
+32 cosines, then 32 sines; pairs of neighbours if interleaved, else of halves).
+slots and row_lens are page_maps'; a token without a slot in the cache or a
+position in the table is not cached. out: like latent, also receives the
+vectors (may be latent). q_rope [tokens, heads, 64]: the queries' rotary parts,
+turned likewise into q_out (a view of absorbed queries, or q_rope itself;
+allocated when None), which is returned; None without q_rope.)doc";
+
+const char append_index_doc[] = R"doc(append_index(keys, index_keys, slots, row_lens, cos_sin, key_scales=None, weight=None, bias=None, eps=1e-6, q=None, weights=None, q_out=None, weights_out=None, interleaved=False, stream=None)
+--
+
+New tokens' indexer keys into their paged cache, as scores_paged() reads it.
+
+keys [tokens, dim] in bfloat16 or float16: normalised (layer norm with weight
+and bias, float32 [dim]; None: left as they are), their first 64 elements turned
+as by append_latent. index_keys [pages, page_size, dim] of the same type, or
+float8_e4m3fn with key_scales float32 [pages, page_size], which get the largest
+element / 448. q [tokens, heads, dim]: the indexer's queries, turned and rounded
+likewise, with their scales multiplied into weights (float32 [tokens, heads],
+8 bits only). Returns (q_out, weights_out), None without q; weights_out is None
+with 16 bits.)doc";
+
 const char scores_paged_doc[] = R"doc(scores_paged(q, weights, keys, seq_lens, page_table, key_scales=None, table_rows=None, out=None, stream=None)
 --
 
@@ -644,7 +832,8 @@ queries, keys, max_queries) (allocated when None).)doc";
    METH_FASTCALL | METH_KEYWORDS, name##_doc}
 
 PyMethodDef methods[] = {
-    SERVE_CALL(page_maps),       SERVE_CALL(scores_paged), SERVE_CALL(scores_ragged),
+    SERVE_CALL(page_maps),       SERVE_CALL(append_latent), SERVE_CALL(append_index),
+    SERVE_CALL(scores_paged),    SERVE_CALL(scores_ragged),
     SERVE_CALL(attend_selected), SERVE_CALL(attend_paged), SERVE_CALL(attend_expanded),
     {"setup", setup, METH_VARARGS, nullptr},
     {nullptr, nullptr, 0, nullptr},

@@ -64,6 +64,10 @@ struct Bf16 {
     bf16x2 v = {(__bf16)x, (__bf16)y};
     return __builtin_bit_cast(uint32_t, v);
   }
+  static __device__ __forceinline__ void unpack(uint32_t w, float& x, float& y) {
+    x = __builtin_bit_cast(float, w << 16);
+    y = __builtin_bit_cast(float, w & 0xffff0000u);
+  }
 };
 
 struct Fp16 {
@@ -83,6 +87,11 @@ struct Fp16 {
   static __device__ __forceinline__ uint32_t pack(float x, float y) {
     fp16x2 v = {(_Float16)x, (_Float16)y};
     return __builtin_bit_cast(uint32_t, v);
+  }
+  static __device__ __forceinline__ void unpack(uint32_t w, float& x, float& y) {
+    const fp16x2 v = __builtin_bit_cast(fp16x2, w);
+    x = (float)v[0];
+    y = (float)v[1];
   }
 };
 
