@@ -66,8 +66,8 @@ enum {
     DSATOPK_ERR_HIP = 4,
     /* dsatopk_paged_noalloc: num_rows above DSATOPK_NOALLOC_MAX_ROWS. */
     DSATOPK_ERR_TOO_LARGE = 5,
-    /* workspace missing or smaller than dsatopk_attend_bytes(...) or
-       dsatopk_expanded_bytes(...). */
+    /* workspace missing or smaller than dsatopk_attend_bytes(...),
+       dsatopk_shared_bytes(...) or dsatopk_expanded_bytes(...). */
     DSATOPK_ERR_WORKSPACE_TOO_SMALL = 6
 };
 
@@ -562,6 +562,53 @@ int dsatopk_attend_paged(const void* q, int64_t q_row_stride, int64_t q_head_str
                          const int32_t* table_rows, int64_t max_seq_len, int32_t num_rows,
                          void* out, float* lse, void* workspace, size_t workspace_bytes,
                          void* stream);
+
+/*
+ * dsatopk_attend_shared - dsatopk_attend_paged for rows in groups whose first
+ * tokens are the same cached ones (requests behind one prompt, samples of one
+ * context, drafted tokens of one request): these are read once for all rows of
+ * a group.
+ *
+ *   group_starts  int32 [num_groups + 1], rising: group g is rows
+ *                 group_starts[g] .. group_starts[g + 1] - 1. The first entry is
+ *                 taken as 0 and the last as num_rows, so that every row is in a
+ *                 group. A group may be a single row, or empty.
+ *   shared_lens   int32 [num_groups]: positions 0 .. shared_lens[g] - 1 of a
+ *                 group's rows are those of its first row's page table (what
+ *                 other rows' tables have there is not looked at). Row b reads
+ *                 the first min(seq_lens[b], shared_lens[g]) there, and the
+ *                 following ones, up to seq_lens[b], in its own table.
+ *                 Negative values are read as 0, those past the table are cut.
+ *   max_shared_len, max_own_len  upper bounds on shared_lens and on the tokens
+ *                 that a row reads by itself, at most 2^31 - 65. They set how
+ *                 the tokens are split over workgroups (and the workspace's
+ *                 size); longer ones are read whole all the same, but a bound of 0
+ *                 is taken at its word: with max_shared_len 0 rows read all
+ *                 of their tokens by themselves, with max_own_len 0 none past
+ *                 their group's shared ones.
+ *   workspace     at least dsatopk_shared_bytes(num_rows, num_heads,
+ *                 latent_dim, num_groups, max_shared_len, max_own_len) bytes,
+ *                 16-byte aligned (NULL where that is 0).
+ *
+ * The other arguments are those of dsatopk_attend_paged, as are the rounding
+ * and the errors. A shared position that some but not all rows of its group see
+ * has to hold finite values (its weight is 0 in the others, which infinities
+ * and NaN turn into NaN); what no row sees may hold anything. num_groups 0 is
+ * refused unless num_rows is 0.
+ */
+size_t dsatopk_shared_bytes(int32_t num_rows, int32_t num_heads, int32_t latent_dim,
+                            int32_t num_groups, int64_t max_shared_len, int64_t max_own_len);
+
+int dsatopk_attend_shared(const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                          const void* cache, int64_t num_pages, int64_t page_stride,
+                          int64_t token_stride, int32_t page_size, int32_t type, int32_t num_heads,
+                          int32_t latent_dim, int32_t rope_dim, float scale,
+                          const int32_t* seq_lens, const int32_t* page_table,
+                          int64_t page_table_stride, int32_t page_table_width,
+                          const int32_t* table_rows, const int32_t* group_starts,
+                          const int32_t* shared_lens, int32_t num_groups, int64_t max_shared_len,
+                          int64_t max_own_len, int32_t num_rows, void* out, float* lse,
+                          void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * dsatopk_attend_expanded - latent attention in its expanded form, for

@@ -33,6 +33,7 @@ EXPORTS = ("dsatopk_status_string", "dsatopk_plan_bytes", "dsatopk_plan", "dsato
            "dsatopk_page_maps", "dsatopk_append_latent", "dsatopk_append_index",
            "dsatopk_scores_paged", "dsatopk_scores_ragged",
            "dsatopk_attend_bytes", "dsatopk_attend_selected", "dsatopk_attend_paged",
+           "dsatopk_attend_shared", "dsatopk_shared_bytes",
            "dsatopk_attend_expanded", "dsatopk_expanded_bytes")
 
 
@@ -102,6 +103,12 @@ def _lib():
         lib.dsatopk_attend_paged.argtypes = [P, i64, i64, P, i64, i64, i64, i32, i32, i32, i32,
                                              i32, f32, P, P, i64, i32, P, i64, i32, P, P, P, sz, P]
         lib.dsatopk_attend_paged.restype = ctypes.c_int
+        lib.dsatopk_shared_bytes.argtypes = [i32, i32, i32, i32, i64, i64]
+        lib.dsatopk_shared_bytes.restype = sz
+        lib.dsatopk_attend_shared.argtypes = [P, i64, i64, P, i64, i64, i64, i32, i32, i32, i32,
+                                              i32, f32, P, P, i64, i32, P, P, P, i32, i64, i64, i32,
+                                              P, P, P, sz, P]
+        lib.dsatopk_attend_shared.restype = ctypes.c_int
         lib.dsatopk_attend_expanded.argtypes = [P, i64, i64, P, i64, i64, P, i64, i64, P, i64, i32,
                                                 i32, i32, i32, i32, f32, i32, P, P, i32, i32, i32,
                                                 i32, P, P, P, sz, P]
@@ -325,6 +332,14 @@ def attend_bytes(num_rows: int, num_heads: int, latent_dim: int, max_tokens: int
                                            int(max_tokens)))
 
 
+def shared_bytes(num_rows: int, num_heads: int, latent_dim: int, num_groups: int,
+                 max_shared_len: int, max_own_len: int) -> int:
+    """Workspace bytes of ``attend_shared``."""
+    return int(_lib().dsatopk_shared_bytes(int(num_rows), int(num_heads), int(latent_dim),
+                                           int(num_groups), int(max_shared_len),
+                                           int(max_own_len)))
+
+
 def expanded_bytes(num_requests: int, num_heads: int, num_queries: int, num_keys: int,
                    max_queries: int) -> int:
     """Workspace bytes of ``attend_expanded``."""
@@ -334,7 +349,7 @@ def expanded_bytes(num_requests: int, num_heads: int, num_queries: int, num_keys
 
 # The serving operators' calls (csrc/serve_binding.cpp), loaded at first use.
 _SERVE = ("page_maps", "append_latent", "append_index", "scores_paged", "scores_ragged", "attend_selected", "attend_paged",
-          "attend_expanded")
+          "attend_shared", "attend_expanded")
 
 
 def __getattr__(name):

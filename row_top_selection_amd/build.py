@@ -13,8 +13,9 @@ PKG = Path(__file__).resolve().parent
 ROOT = PKG.parent
 SOURCES = [PKG / "csrc" / name for name in (
     "dsatopk.hip", "page_maps.hip", "append_cache.hip", "index_scores.hip", "latent_attend.hip",
-    "expanded_attend.hip")]
+    "shared_attend.hip", "expanded_attend.hip")]
 HEADERS = [PKG / "csrc" / "select_device.h", PKG / "csrc" / "serve_common.h",
+           PKG / "csrc" / "latent_tiles.h",
            ROOT / "include" / "dsatopk.h"]
 LIB = PKG / "libdsatopk.so"
 EXT_SOURCE = PKG / "csrc" / "serve_binding.cpp"

@@ -610,6 +610,11 @@ struct Absorbed {
   void room(PyObject* given, int64_t tokens) {
     workspace = workspace_of(on, given, dsatopk_attend_bytes(rows, heads, latent, tokens), q);
   }
+  // A bound on a row's tokens; a table may have more positions than the largest, 2^31 - 65.
+  int64_t bound(PyObject* given, const at::Tensor& tab, const char* name) const {
+    return given && given != Py_None ? integer(given, name)
+                                     : std::min<int64_t>(tab.size(1) * cache.size(1), INT32_MAX - 64);
+  }
 };
 
 PyObject* attend_selected(PyObject* const* args, Py_ssize_t n, PyObject* kw) {
@@ -646,10 +651,7 @@ PyObject* attend_paged(PyObject* const* args, Py_ssize_t n, PyObject* kw) {
   if (!rows && tab.size(0) != s.rows)
     refuse("page_table must have one row per query row without table_rows");
   const float scale = number(a.at[5], "scale");
-  // a table may have more positions than the largest bound, 2^31 - 65
-  const int64_t longest =
-      a.given(7) ? integer(a.at[7], "max_seq_len")
-                 : std::min<int64_t>(tab.size(1) * s.cache.size(1), INT32_MAX - 64);
+  const int64_t longest = s.bound(a.at[7], tab, "max_seq_len");
   s.room(a.at[10], longest);
   check_status(
       dsatopk_attend_paged(s.q.data_ptr(), stride(s.q, 0), stride(s.q, 1), s.cache.data_ptr(),
@@ -660,6 +662,40 @@ PyObject* attend_paged(PyObject* const* args, Py_ssize_t n, PyObject* kw) {
                            s.results.out.data_ptr(), static_cast<float*>(s.results.lse.data_ptr()),
                            room_ptr(s.workspace), room_bytes(s.workspace), s.on.stream),
       "dsatopk_attend_paged");
+  return pair(s.results.out, s.results.lse);
+}
+
+PyObject* attend_shared(PyObject* const* args, Py_ssize_t n, PyObject* kw) {
+  static const char* const names[] = {"q", "cache", "seq_lens", "page_table", "group_starts", "shared_lens",
+                                      "latent_dim", "scale", "table_rows", "max_shared_len", "max_own_len",
+                                      "out", "lse", "workspace", "stream"};
+  const Args<15> a("attend_shared", names, 8, args, n, kw);
+  Absorbed s(a.at[0], a.at[1], a.at[6], a.at[11], a.at[12], a.at[14]);
+  const at::Tensor& lens = vector(a.at[2], s.rows, &s.q, "seq_lens");
+  const int32_t* rows = vector_or_null(a.at[8], s.rows, &s.q, "table_rows");
+  const at::Tensor& tab = table(a.at[3], &s.q);
+  if (!rows && tab.size(0) != s.rows)
+    refuse("page_table must have one row per query row without table_rows");
+  const at::Tensor& starts = vector(a.at[4], -1, &s.q, "group_starts");
+  if (starts.size(0) < 1 || (s.rows && starts.size(0) < 2))
+    refuse("group_starts must have an entry more than there are groups, one group at least");
+  const int32_t groups = size32(starts.size(0) - 1, "group_starts");
+  const at::Tensor& shared = vector(a.at[5], groups, &s.q, "shared_lens");
+  const float scale = number(a.at[7], "scale");
+  const int64_t most_shared = s.bound(a.at[9], tab, "max_shared_len");
+  const int64_t most_own = s.bound(a.at[10], tab, "max_own_len");
+  s.workspace = workspace_of(s.on, a.at[13],
+                             dsatopk_shared_bytes(s.rows, s.heads, s.latent, groups, most_shared, most_own), s.q);
+  check_status(
+      dsatopk_attend_shared(s.q.data_ptr(), stride(s.q, 0), stride(s.q, 1), s.cache.data_ptr(),
+                            s.cache.size(0), stride(s.cache, 0), stride(s.cache, 1),
+                            size32(s.cache.size(1), "cache"), s.type, s.heads, s.latent,
+                            size32(s.q.size(2) - s.latent, "q"), scale, ints(lens), ints(tab),
+                            row_stride(tab), size32(tab.size(1), "page_table"), rows, ints(starts),
+                            ints(shared), groups, most_shared, most_own, s.rows,
+                            s.results.out.data_ptr(), static_cast<float*>(s.results.lse.data_ptr()),
+                            room_ptr(s.workspace), room_bytes(s.workspace), s.on.stream),
+      "dsatopk_attend_shared");
   return pair(s.results.out, s.results.lse);
 }
 
@@ -815,6 +851,21 @@ page table.
 Arguments as for attend_selected and paged(); max_seq_len bounds seq_lens (the
 table's positions when None) and sets how rows are split.)doc";
 
+const char attend_shared_doc[] = R"doc(attend_shared(q, cache, seq_lens, page_table, group_starts, shared_lens, latent_dim, scale, table_rows=None, max_shared_len=None, max_own_len=None, out=None, lse=None, workspace=None, stream=None)
+--
+
+attend_paged for rows in groups whose first tokens are the same cached ones,
+read once for all rows of a group.
+
+group_starts int32 [groups + 1]: a group's first row (the first one is taken as
+0, the last as the number of rows); shared_lens int32 [groups]: how many
+positions its rows share, those of its first row's page table. A row reads what
+it sees of them there and its other positions in its own table. max_shared_len
+and max_own_len bound the shared positions and those that a row reads by
+itself (the table's positions when None; 0: there are none). workspace: uint8 of
+shared_bytes(rows, heads, latent_dim, groups, max_shared_len, max_own_len)
+(allocated when None).)doc";
+
 const char attend_expanded_doc[] = R"doc(attend_expanded(q, k, v, k_rope, q_starts, k_starts, max_queries, scale, causal=True, out=None, lse=None, workspace=None, stream=None)
 --
 
@@ -834,7 +885,8 @@ queries, keys, max_queries) (allocated when None).)doc";
 PyMethodDef methods[] = {
     SERVE_CALL(page_maps),       SERVE_CALL(append_latent), SERVE_CALL(append_index),
     SERVE_CALL(scores_paged),    SERVE_CALL(scores_ragged),
-    SERVE_CALL(attend_selected), SERVE_CALL(attend_paged), SERVE_CALL(attend_expanded),
+    SERVE_CALL(attend_selected), SERVE_CALL(attend_paged), SERVE_CALL(attend_shared),
+    SERVE_CALL(attend_expanded),
     {"setup", setup, METH_VARARGS, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
