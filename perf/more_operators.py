@@ -256,7 +256,7 @@ def _run_own(s):
         out, lse = dt.attend_shared(s["q"], s["cache"], s["seq_lens"], s["table"], s["group_starts"], s["shared_lens"], s["latent"], s["scale"], table_rows=s["table_rows"],
                                     max_shared_len=s["shared"], max_own_len=s["own"])
         return dict(out=out, lse=lse)
-    out, lse = dt.attend_expanded_shared(s["q"], s["k"], s["v"], s["k_rope"], s["q_starts"], s["k_starts"], s["shared_starts"], s["shared_lens"], s["max_q"], s["scale"],
+    out, lse = dt.attend_expanded_shared(s["q"], s["k"], s["v"], s["k_rope"], s["q_starts"], s["k_starts"], s["shared_starts"], s["shared_lens"], s["scale"],
                                          max_keys=s["max_shared"] + s["max_q"])
     return dict(out=out, lse=lse)
 
