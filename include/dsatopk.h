@@ -67,7 +67,8 @@ enum {
     /* dsatopk_paged_noalloc: num_rows above DSATOPK_NOALLOC_MAX_ROWS. */
     DSATOPK_ERR_TOO_LARGE = 5,
     /* workspace missing or smaller than dsatopk_attend_bytes(...),
-       dsatopk_shared_bytes(...) or dsatopk_expanded_bytes(...). */
+       dsatopk_shared_bytes(...), dsatopk_expanded_bytes(...) or
+       dsatopk_expanded_shared_bytes(...). */
     DSATOPK_ERR_WORKSPACE_TOO_SMALL = 6
 };
 
@@ -668,6 +669,43 @@ int dsatopk_attend_expanded(const void* q, int64_t q_row_stride, int64_t q_head_
                             int32_t num_requests, int32_t num_queries, int32_t num_keys,
                             int32_t max_queries, void* out, float* lse, void* workspace,
                             size_t workspace_bytes, void* stream);
+
+/*
+ * dsatopk_attend_expanded_shared - dsatopk_attend_expanded for prompts behind
+ * keys that several of them share, which are there once: request r has the
+ * keys shared_starts[r] .. shared_starts[r] + shared_lens[r] - 1, all of which
+ * every query of it sees, and behind them its own, k_starts[r] .. k_starts[r +
+ * 1] - 1, which it sees as in dsatopk_attend_expanded.
+ *
+ *   shared_starts, shared_lens  int32 [num_requests], negative values read as
+ *                 0, lengths cut at num_keys. Neighbouring requests (apart from
+ *                 those without queries) with the same two values share the work
+ *                 on these keys, too; equal values further apart do not. Length 0:
+ *                 none are shared.
+ *   num_queries, num_keys  at most 2^30.
+ *   max_keys      an upper bound on a request's keys, shared and own; it sets how
+ *                 few rows of many keys are split (and the workspace's size),
+ *                 and nothing else.
+ *   workspace     at least dsatopk_expanded_shared_bytes(num_heads,
+ *                 num_queries, max_keys) bytes, 16-byte aligned (NULL where
+ *                 that is 0).
+ *
+ * The other arguments, the rounding and the errors are those of
+ * dsatopk_attend_expanded, but there is no max_queries: all rows are
+ * computed. Values must be finite here, too, also the shared ones and the
+ * neighbouring requests' own: those of a key that any of 256 queries standing
+ * together sees.
+ */
+size_t dsatopk_expanded_shared_bytes(int32_t num_heads, int32_t num_queries, int32_t max_keys);
+
+int dsatopk_attend_expanded_shared(
+    const void* q, int64_t q_row_stride, int64_t q_head_stride, const void* k,
+    int64_t k_row_stride, int64_t k_head_stride, const void* v, int64_t v_row_stride,
+    int64_t v_head_stride, const void* k_rope, int64_t rope_row_stride, int32_t type,
+    int32_t num_heads, int32_t nope_dim, int32_t rope_dim, int32_t value_dim, float scale,
+    int32_t causal, const int32_t* q_starts, const int32_t* k_starts, const int32_t* shared_starts,
+    const int32_t* shared_lens, int32_t num_requests, int32_t num_queries, int32_t num_keys,
+    int32_t max_keys, void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

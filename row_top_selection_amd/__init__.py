@@ -34,7 +34,8 @@ EXPORTS = ("dsatopk_status_string", "dsatopk_plan_bytes", "dsatopk_plan", "dsato
            "dsatopk_scores_paged", "dsatopk_scores_ragged",
            "dsatopk_attend_bytes", "dsatopk_attend_selected", "dsatopk_attend_paged",
            "dsatopk_attend_shared", "dsatopk_shared_bytes",
-           "dsatopk_attend_expanded", "dsatopk_expanded_bytes")
+           "dsatopk_attend_expanded", "dsatopk_expanded_bytes",
+           "dsatopk_attend_expanded_shared", "dsatopk_expanded_shared_bytes")
 
 
 class DsatopkError(RuntimeError):
@@ -115,6 +116,12 @@ def _lib():
         lib.dsatopk_expanded_bytes.argtypes = [i32, i32, i32, i32, i32]
         lib.dsatopk_expanded_bytes.restype = sz
         lib.dsatopk_attend_expanded.restype = ctypes.c_int
+        lib.dsatopk_expanded_shared_bytes.argtypes = [i32, i32, i32]
+        lib.dsatopk_expanded_shared_bytes.restype = sz
+        lib.dsatopk_attend_expanded_shared.argtypes = [P, i64, i64, P, i64, i64, P, i64, i64, P, i64,
+                                                       i32, i32, i32, i32, i32, f32, i32, P, P, P,
+                                                       P, i32, i32, i32, i32, P, P, P, sz, P]
+        lib.dsatopk_attend_expanded_shared.restype = ctypes.c_int
         _handle = lib
     return _handle
 
@@ -347,9 +354,15 @@ def expanded_bytes(num_requests: int, num_heads: int, num_queries: int, num_keys
                                              int(num_keys), int(max_queries)))
 
 
+def expanded_shared_bytes(num_heads: int, num_queries: int, max_keys: int) -> int:
+    """Workspace bytes of ``attend_expanded_shared``."""
+    return int(_lib().dsatopk_expanded_shared_bytes(int(num_heads), int(num_queries),
+                                                    int(max_keys)))
+
+
 # The serving operators' calls (csrc/serve_binding.cpp), loaded at first use.
 _SERVE = ("page_maps", "append_latent", "append_index", "scores_paged", "scores_ragged", "attend_selected", "attend_paged",
-          "attend_shared", "attend_expanded")
+          "attend_shared", "attend_expanded", "attend_expanded_shared")
 
 
 def __getattr__(name):

@@ -1,5 +1,6 @@
 // expanded_attend.hip - latent attention in its expanded form
-// (dsatopk_attend_expanded in include/dsatopk.h), for prompts:
+// (dsatopk_attend_expanded and dsatopk_attend_expanded_shared in
+// include/dsatopk.h), for prompts:
 //
 //   s[i, j] = scale * (q[i, h][:128] . k[j, h] + q[i, h][128:] . k_rope[j])
 //   out[i, h] = sum_j softmax(s[i, :])[j] * v[j, h]
@@ -22,6 +23,13 @@
 //
 // Few rows of many keys are split over workgroups by keys; a second kernel
 // joins the parts.
+//
+// With shared keys a workgroup takes the next 32 queries a wave of the batch,
+// whichever requests they are of, and goes over segments of keys: those that
+// the requests share, once for all of them that stand together, then each
+// request's own. A lane counts the keys of a segment that its query sees; waves
+// none of whose queries are in a segment only copy. Prompts of 16 tokens fill
+// tiles that way, which would be nearly empty if every request had its own.
 //
 // 4 x 1024 queries behind 15360 earlier tokens, 16 heads: 620 us, 1.07 PFLOP/s
 // (a large library product of random numbers reaches 1.37 here). The clock
@@ -71,6 +79,8 @@ struct ExpandParams {
   int64_t rope_row;
   const int32_t* q_starts;
   const int32_t* k_starts;
+  const int32_t* shared_starts;  // shared form
+  const int32_t* shared_lens;
   int32_t requests, heads, tiles, num_q, num_k, causal, splits;
   float scale2;
   char* out;
@@ -266,6 +276,39 @@ __device__ __forceinline__ void keys_step(const ExpandParams& p, State& st, f32x
   }
 }
 
+// What the wave's sums come to, for the lane's query `at`: the result, or part `split`.
+template <class T>
+__device__ __forceinline__ void put(const ExpandParams& p, const State& st, int64_t at, int head, int split,
+                                    int half) {
+  const float sum = st.sum + other_half(st.sum);
+  if (p.splits > 1) {
+    const int64_t to = ((int64_t)split * p.num_q + at) * p.heads + head;
+    if (half == 0) {
+      p.state[to * 2] = st.top;
+      p.state[to * 2 + 1] = sum;
+    }
+    if (st.top == -INFINITY && sum == 0.0f) return;  // nothing seen: the join skips it
+    float* part = p.part + to * kValue + 4 * half;
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4)
+        *reinterpret_cast<f32x4*>(part + b * 32 + 2 * i) =
+            f32x4{st.o[b][i], st.o[b][i + 1], st.o[b][i + 2], st.o[b][i + 3]};
+    return;
+  }
+  const float by = sum == 0.0f ? 0.0f : 1.0f / sum;
+  char* to = p.out + ((at * p.heads + head) * kValue + 4 * half) * 2;
+#pragma unroll
+  for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+    for (int i = 0; i < 16; i += 4)
+      *reinterpret_cast<u32x2*>(to + (b * 32 + 2 * i) * 2) =
+          u32x2{T::pack(st.o[b][i] * by, st.o[b][i + 1] * by),
+                T::pack(st.o[b][i + 2] * by, st.o[b][i + 3] * by)};
+  if (p.lse && half == 0) p.lse[at * p.heads + head] = (st.top + log2f(sum)) * kLn2;
+}
+
 template <class T, class S>
 __global__ __launch_bounds__(S::kBlock, 2) void expand_kernel(ExpandParams p) {
   constexpr int kRows = S::kRows, kTile = S::kTile, kRing = S::kRing, kBuffer = S::kBuffer;
@@ -353,34 +396,193 @@ __global__ __launch_bounds__(S::kBlock, 2) void expand_kernel(ExpandParams p) {
       }
     }
   }
-  if (row >= rows) return;
-  const float sum = st.sum + other_half(st.sum);
-  if (p.splits > 1) {
-    const int64_t to = ((int64_t)split * p.num_q + at) * p.heads + head;
-    if (half == 0) {
-      p.state[to * 2] = st.top;
-      p.state[to * 2 + 1] = sum;
-    }
-    if (st.top == -INFINITY && sum == 0.0f) return;  // nothing seen: the join skips it
-    float* part = p.part + to * kValue + 4 * half;
-#pragma unroll
-    for (int b = 0; b < kBlocks; ++b)
-#pragma unroll
-      for (int i = 0; i < 16; i += 4)
-        *reinterpret_cast<f32x4*>(part + b * 32 + 2 * i) =
-            f32x4{st.o[b][i], st.o[b][i + 1], st.o[b][i + 2], st.o[b][i + 3]};
-    return;
+  if (row < rows) put<T>(p, st, at, head, split, half);
+}
+
+// Keys that some queries see: rows base .. base + len - 1 of the keys, for the
+// queries from .. to - 1, of which query i sees the first i + diag (not fewer than
+// 0, nor more than len).
+struct Segment {
+  int32_t base, len, from, to, diag;
+
+  __device__ __forceinline__ int32_t seen(int32_t i) const {
+    return i >= from && i < to ? min(max(i + diag, 0), len) : 0;
   }
-  const float by = sum == 0.0f ? 0.0f : 1.0f / sum;
-  char* to = p.out + ((at * p.heads + head) * kValue + 4 * half) * 2;
+};
+
+// The segments of the queries q0 .. q1 - 1, a tile of keys at a time. The same in
+// all lanes.
+template <class S>
+struct Walk {
+  const ExpandParams& p;
+  int32_t q0, q1;
+  int32_t request;  // whose own keys come next, or with whom a new run begins
+  int32_t run;      // the first request behind those that share with it
+  Segment at;
+  int32_t j;  // first key of the tile, in the segment
+  bool done;
+
+  __device__ __forceinline__ Walk(const ExpandParams& params, int32_t first, int32_t last, int32_t r)
+      : p(params), q0(first), q1(last), request(r), run(r), at{}, j(0), done(false) {
+    next();
+  }
+  __device__ __forceinline__ int32_t starts(int32_t r) const { return max(p.q_starts[r], 0); }
+  __device__ __forceinline__ int32_t ends(int32_t r) const { return min(p.q_starts[r + 1], p.num_q); }
+
+  __device__ __forceinline__ void next() {
+    j = 0;
+    while (true) {
+      if (request >= run) {
+        while (request < p.requests && starts(request) >= ends(request)) ++request;
+        if (request >= p.requests || starts(request) >= q1) {
+          done = true;
+          return;
+        }
+        const int32_t first = p.shared_starts[request], len = p.shared_lens[request];
+        run = request + 1;
+        while (run < p.requests && starts(run) < q1 &&
+               (starts(run) >= ends(run) || (p.shared_starts[run] == first && p.shared_lens[run] == len)))
+          ++run;
+        at.base = min(max(first, 0), p.num_k);
+        at.len = min(max(len, 0), p.num_k - at.base);
+        at.from = max(starts(request), q0);
+        at.to = min(ends(run - 1), q1);
+        at.diag = at.len;
+        if (at.len > 0 && at.from < at.to) return;
+      }
+      const int32_t r = request++;
+      const int32_t first = starts(r), rows = ends(r) - first;
+      at.base = min(max(p.k_starts[r], 0), p.num_k);
+      const int32_t keys = max(min(p.k_starts[r + 1], p.num_k) - at.base, 0);
+      at.from = max(first, q0);
+      at.to = min(first + rows, q1);
+      if (at.from >= at.to) continue;
+      at.diag = p.causal ? keys - rows + 1 - first : keys;
+      at.len = min(max(at.to - 1 + at.diag, 0), keys);
+      if (at.len > 0) return;
+    }
+  }
+  __device__ __forceinline__ void advance() {
+    j += S::kTile;
+    if (j >= at.len) next();
+  }
+  // n tiles on.
+  __device__ __forceinline__ void skip(int32_t n) {
+    while (n > 0 && !done) {
+      const int32_t here = (at.len - j + S::kTile - 1) / S::kTile;
+      if (here > n) {
+        j += n * S::kTile;
+        return;
+      }
+      n -= here;
+      next();
+    }
+  }
+  __device__ __forceinline__ int32_t tiles() {
+    int32_t n = 0;
+    for (; !done; next()) n += (at.len + S::kTile - 1) / S::kTile;
+    return n;
+  }
+};
+
+template <class T, class S>
+__global__ __launch_bounds__(S::kBlock, 2) void expand_shared_kernel(ExpandParams p) {
+  constexpr int kRows = S::kRows, kTile = S::kTile, kRing = S::kRing, kBuffer = S::kBuffer;
+  constexpr int kAheadTiles = kRing - 1, kParts = kTile / kKeys;
+  __shared__ __attribute__((aligned(1024))) char tiles[kRing * kBuffer];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int col = lane & 31, half = lane >> 5;
+
+  // Workgroup -> (head, queries), as above: those of one head are 8 apart.
+  const uint32_t id = blockIdx.x;
+  const int split = blockIdx.y;
+  const int head = id / (8 * p.tiles) * 8 + id % 8;
+  if (head >= p.heads) return;
+  const int32_t q0 = (p.tiles - 1 - (int32_t)(id / 8 % p.tiles)) * kRows, q1 = min(q0 + kRows, p.num_q);
+  const int32_t r = last_below(p.requests, q0, lane, [&](int32_t i) { return (int64_t)p.q_starts[i]; });
+  const int32_t w0 = q0 + wave * 32, mine = w0 + col;
+  const bool real = mine < q1 && mine >= p.q_starts[0] && mine < p.q_starts[p.requests];
+  const int64_t at = min(mine, q1 - 1);
+
+  u32x4 q[kSteps];
+  const char* qh = p.q + at * p.q_row + head * p.q_head;
 #pragma unroll
-  for (int b = 0; b < kBlocks; ++b)
+  for (int i = 0; i < kSteps; ++i) q[i] = load16(qh + (2 * i + half) * 16);
+
+  State st;
+  st.top = -INFINITY;
+  st.sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; i += 4)
-      *reinterpret_cast<u32x2*>(to + (b * 32 + 2 * i) * 2) =
-          u32x2{T::pack(st.o[b][i] * by, st.o[b][i + 1] * by),
-                T::pack(st.o[b][i + 2] * by, st.o[b][i + 3] * by)};
-  if (p.lse && half == 0) p.lse[at * p.heads + head] = (st.top + log2f(sum)) * kLn2;
+  for (int b = 0; b < kBlocks; ++b) st.o[b] = f32x16{};
+
+  Walk<S> use(p, q0, q1, r);
+  int32_t most = INT32_MAX;
+  if (p.splits > 1) {
+    const int32_t all = Walk<S>(use).tiles();
+    const int32_t per = (all + p.splits - 1) / p.splits;
+    most = per;
+    use.skip(split * per);
+  }
+  Walk<S> copy(use);
+  const Places<S> places(p, lane);
+  int32_t copied = 0;
+  auto keys_at = [&](const char* base, int64_t head_bytes, int64_t row_bytes) {
+    return base + copy.at.base * row_bytes + head * head_bytes;
+  };
+  while (copied < kAheadTiles && copied < most && !copy.done) {
+    copy_tile<S>(p, tiles + copied * kBuffer, keys_at(p.k, p.k_head, p.k_row), keys_at(p.v, p.v_head, p.v_row),
+                 keys_at(p.rope, 0, p.rope_row), copy.j, copy.at.len, places, wave, lane);
+    copy.advance();
+    ++copied;
+  }
+  if (copied) {
+    copies_barrier();
+    f32x16 s = {};
+    bool have = false;  // s holds the scores of the next 32 keys
+    for (int32_t n = 0; n < copied; ++n) {
+      const Segment seg = use.at;
+      const int32_t j0 = use.j;
+      use.advance();
+      // what the wave's queries see of the segment, at most and at least
+      const int32_t top = w0 < seg.to ? seg.seen(min(w0 + 31, seg.to - 1)) : 0;
+      const int32_t low = w0 + 31 < seg.to ? seg.seen(w0) : 0;
+      const int32_t sees = seg.seen((int32_t)at);  // lanes past the last query do as that does
+#pragma unroll
+      for (int part = 0; part < kParts; ++part) {
+        const bool last = part + 1 == kParts;
+        if (last) {
+          // tile n + 1 has arrived, and all waves are done with tile n - 1
+          if (kAheadTiles > 2 && copied - n >= kAheadTiles)
+            wait_copies_but<(kAheadTiles - 2) * kCopies>();
+          else
+            wait_copies();
+          __syncthreads();
+        }
+        const bool more = last && copied < most && !copy.done;
+        const int32_t j = j0 + part * kKeys;
+        const char* cur = tiles + n % kRing * kBuffer;
+        char* to = tiles + (n + kAheadTiles) % kRing * kBuffer;
+        const char* k = keys_at(p.k, p.k_head, p.k_row);
+        const char* v = keys_at(p.v, p.v_head, p.v_row);
+        const char* rope = keys_at(p.rope, 0, p.rope_row);
+        if (j < top) {
+          if (!have)
+            s = scores_of<T, S>(cur, part, q, places, nullptr, 0.0f, 0.0f, nullptr, nullptr);
+          keys_step<T, S>(p, st, s, q, cur, part, tiles + (n + last) % kRing * kBuffer, last ? 0 : part + 1, to,
+                          k, v, rope, more, copy.j, copy.at.len, sees - j, low >= j + kKeys, places, wave, lane);
+        } else if (more) {
+          copy_tile<S>(p, to, k, v, rope, copy.j, copy.at.len, places, wave, lane);
+        }
+        have = j < top;
+        if (more) {
+          copy.advance();
+          ++copied;
+        }
+      }
+    }
+  }
+  if (real) put<T>(p, st, at, head, split, half);
 }
 
 // Joins the parts of the rows' heads: 32 threads for each, 4 elements a
@@ -471,6 +673,25 @@ int launch_expand(ExpandParams p, const Cut& c, void* stream) {
                 stream);
 }
 
+// The same for the shared form, whose queries stand together: as for one request.
+Cut shared_cut_of(int32_t heads, int32_t queries, int32_t max_keys) {
+  return cut_of(1, heads, queries, max_keys, queries);
+}
+
+template <class T, class S>
+int launch_shared(ExpandParams p, const Cut& c, void* stream) {
+  p.tiles = (p.num_q + S::kRows - 1) / S::kRows;
+  p.splits = c.splits;
+  const int st = launch(expand_shared_kernel<T, S>, dim3((unsigned)(c.pairs * p.tiles), (unsigned)c.splits),
+                        dim3(S::kBlock), p, stream);
+  if (st != DSATOPK_OK || c.splits == 1) return st;
+  p.tiles = INT32_MAX / Shape<4>::kRows;  // every row of a request has been computed
+  const int64_t each = (int64_t)p.num_q * p.heads;
+  constexpr int kPer = kJoinBlock / kJoinEach;
+  return launch(expand_join_kernel<T>, dim3((unsigned)((each + kPer - 1) / kPer)), dim3(kJoinBlock), p,
+                stream);
+}
+
 size_t part_floats(const Cut& c, int32_t queries, int32_t heads) {
   return c.splits == 1 ? 0 : (size_t)c.splits * queries * heads * (kValue + 2);
 }
@@ -487,6 +708,68 @@ extern "C" size_t dsatopk_expanded_bytes(int32_t num_requests, int32_t num_heads
                      num_heads) * sizeof(float);
 }
 
+namespace dsatopk_serve {
+namespace {
+
+// Checks and fills what both forms share.
+int check_expanded(ExpandParams& p, const void* q, int64_t q_row, int64_t q_head, const void* k,
+                   int64_t k_row, int64_t k_head, const void* v, int64_t v_row, int64_t v_head,
+                   const void* k_rope, int64_t rope_row, int32_t type, int32_t heads, int32_t nope,
+                   int32_t rope, int32_t value, float scale, int32_t causal, const int32_t* q_starts,
+                   const int32_t* k_starts, int32_t requests, int32_t queries, int32_t keys,
+                   int32_t max_queries, void* out, float* lse) {
+  if (requests < 0 || queries < 0 || keys < 0 || max_queries < 0 || heads < 1 || heads > 1024 ||
+      nope != kNope || rope != kRope || value != kValue ||
+      (type != DSATOPK_BF16 && type != DSATOPK_FP16) || !(scale > 0.0f) || !(scale < INFINITY) ||
+      q_row < 0 || q_head < 0 || k_row < 0 || k_head < 0 || v_row < 0 || v_head < 0 || rope_row < 0 ||
+      k_row > kMostStride || v_row > kMostStride || rope_row > kMostStride)
+    return DSATOPK_ERR_INVALID_ARG;
+  if (requests == 0 || queries == 0 || max_queries == 0) return DSATOPK_OK;
+  if (!q || !out || !q_starts || !k_starts || (keys && (!k || !v || !k_rope)))
+    return DSATOPK_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(k_rope) ||
+      (reinterpret_cast<uintptr_t>(out) & 7u) || !aligned4(lse) || q_row % 8 || q_head % 8 || k_row % 8 ||
+      k_head % 8 || v_row % 8 || v_head % 8 || rope_row % 8)
+    return DSATOPK_ERR_ALIGNMENT;
+  p.q = static_cast<const char*>(q);
+  p.q_row = q_row * 2;
+  p.q_head = q_head * 2;
+  p.k = static_cast<const char*>(k);
+  p.k_row = k_row * 2;
+  p.k_head = k_head * 2;
+  p.v = static_cast<const char*>(v);
+  p.v_row = v_row * 2;
+  p.v_head = v_head * 2;
+  p.rope = static_cast<const char*>(k_rope);
+  p.rope_row = rope_row * 2;
+  p.q_starts = q_starts;
+  p.k_starts = k_starts;
+  p.requests = requests;
+  p.heads = heads;
+  p.num_q = queries;
+  p.num_k = keys;
+  p.causal = causal != 0;
+  p.scale2 = scale * kLog2e;
+  p.out = static_cast<char*>(out);
+  p.lse = lse;
+  return DSATOPK_OK;
+}
+
+// The workspace of a call that is cut as `c`.
+int check_room(ExpandParams& p, const Cut& c, void* workspace, size_t workspace_bytes) {
+  if (c.pairs * ((c.longest + 127) / 128) > INT32_MAX) return DSATOPK_ERR_INVALID_ARG;
+  if (c.splits == 1) return DSATOPK_OK;
+  if (!workspace || workspace_bytes < part_floats(c, p.num_q, p.heads) * sizeof(float))
+    return DSATOPK_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned16(workspace)) return DSATOPK_ERR_ALIGNMENT;
+  p.part = static_cast<float*>(workspace);
+  p.state = p.part + (size_t)c.splits * p.num_q * p.heads * kValue;
+  return DSATOPK_OK;
+}
+
+}  // namespace
+}  // namespace dsatopk_serve
+
 extern "C" int dsatopk_attend_expanded(
     const void* q, int64_t q_row_stride, int64_t q_head_stride, const void* k,
     int64_t k_row_stride, int64_t k_head_stride, const void* v, int64_t v_row_stride,
@@ -495,55 +778,54 @@ extern "C" int dsatopk_attend_expanded(
     int32_t causal, const int32_t* q_starts, const int32_t* k_starts, int32_t num_requests,
     int32_t num_queries, int32_t num_keys, int32_t max_queries, void* out, float* lse,
     void* workspace, size_t workspace_bytes, void* stream) {
-  if (num_requests < 0 || num_queries < 0 || num_keys < 0 || max_queries < 0 || num_heads < 1 ||
-      num_heads > 1024 || nope_dim != kNope || rope_dim != kRope || value_dim != kValue ||
-      (type != DSATOPK_BF16 && type != DSATOPK_FP16) || !(scale > 0.0f) || !(scale < INFINITY) ||
-      q_row_stride < 0 || q_head_stride < 0 || k_row_stride < 0 || k_head_stride < 0 ||
-      v_row_stride < 0 || v_head_stride < 0 || rope_row_stride < 0 ||
-      k_row_stride > kMostStride || v_row_stride > kMostStride || rope_row_stride > kMostStride)
-    return DSATOPK_ERR_INVALID_ARG;
-  if (num_requests == 0 || num_queries == 0 || max_queries == 0) return DSATOPK_OK;
-  if (!q || !out || !q_starts || !k_starts || (num_keys && (!k || !v || !k_rope)))
-    return DSATOPK_ERR_INVALID_ARG;
-  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(k_rope) ||
-      (reinterpret_cast<uintptr_t>(out) & 7u) || !aligned4(lse) || q_row_stride % 8 ||
-      q_head_stride % 8 || k_row_stride % 8 || k_head_stride % 8 || v_row_stride % 8 ||
-      v_head_stride % 8 || rope_row_stride % 8)
-    return DSATOPK_ERR_ALIGNMENT;
   ExpandParams p{};
-  p.q = static_cast<const char*>(q);
-  p.q_row = q_row_stride * 2;
-  p.q_head = q_head_stride * 2;
-  p.k = static_cast<const char*>(k);
-  p.k_row = k_row_stride * 2;
-  p.k_head = k_head_stride * 2;
-  p.v = static_cast<const char*>(v);
-  p.v_row = v_row_stride * 2;
-  p.v_head = v_head_stride * 2;
-  p.rope = static_cast<const char*>(k_rope);
-  p.rope_row = rope_row_stride * 2;
-  p.q_starts = q_starts;
-  p.k_starts = k_starts;
-  p.requests = num_requests;
-  p.heads = num_heads;
-  p.num_q = num_queries;
-  p.num_k = num_keys;
-  p.causal = causal != 0;
-  p.scale2 = scale * kLog2e;
-  p.out = static_cast<char*>(out);
-  p.lse = lse;
+  int st = check_expanded(p, q, q_row_stride, q_head_stride, k, k_row_stride, k_head_stride, v,
+                          v_row_stride, v_head_stride, k_rope, rope_row_stride, type, num_heads,
+                          nope_dim, rope_dim, value_dim, scale, causal, q_starts, k_starts,
+                          num_requests, num_queries, num_keys, max_queries, out, lse);
+  if (st != DSATOPK_OK || !p.q) return st;
   const Cut c = cut_of(num_requests, num_heads, num_queries, num_keys, max_queries);
-  if (c.pairs * ((c.longest + 127) / 128) > INT32_MAX) return DSATOPK_ERR_INVALID_ARG;
-  if (c.splits > 1) {
-    if (!workspace || workspace_bytes < part_floats(c, num_queries, num_heads) * sizeof(float))
-      return DSATOPK_ERR_WORKSPACE_TOO_SMALL;
-    if (!aligned16(workspace)) return DSATOPK_ERR_ALIGNMENT;
-    p.part = static_cast<float*>(workspace);
-    p.state = p.part + (size_t)c.splits * num_queries * num_heads * kValue;
-  }
+  st = check_room(p, c, workspace, workspace_bytes);
+  if (st != DSATOPK_OK) return st;
   const bool bf16 = type == DSATOPK_BF16;
   return c.wide ? bf16 ? launch_expand<Bf16, Shape<8>>(p, c, stream)
                        : launch_expand<Fp16, Shape<8>>(p, c, stream)
          : bf16 ? launch_expand<Bf16, Shape<4>>(p, c, stream)
                 : launch_expand<Fp16, Shape<4>>(p, c, stream);
+}
+
+extern "C" size_t dsatopk_expanded_shared_bytes(int32_t num_heads, int32_t num_queries,
+                                                int32_t max_keys) {
+  if (num_heads < 1 || num_queries < 1 || max_keys < 0) return 0;
+  return part_floats(shared_cut_of(num_heads, num_queries, max_keys), num_queries, num_heads) *
+         sizeof(float);
+}
+
+extern "C" int dsatopk_attend_expanded_shared(
+    const void* q, int64_t q_row_stride, int64_t q_head_stride, const void* k,
+    int64_t k_row_stride, int64_t k_head_stride, const void* v, int64_t v_row_stride,
+    int64_t v_head_stride, const void* k_rope, int64_t rope_row_stride, int32_t type,
+    int32_t num_heads, int32_t nope_dim, int32_t rope_dim, int32_t value_dim, float scale,
+    int32_t causal, const int32_t* q_starts, const int32_t* k_starts, const int32_t* shared_starts,
+    const int32_t* shared_lens, int32_t num_requests, int32_t num_queries, int32_t num_keys,
+    int32_t max_keys, void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  ExpandParams p{};
+  // a query's number and a count of keys are added in 32 bits
+  if (num_queries > (1 << 30) || num_keys > (1 << 30) || max_keys < 0) return DSATOPK_ERR_INVALID_ARG;
+  int st = check_expanded(p, q, q_row_stride, q_head_stride, k, k_row_stride, k_head_stride, v,
+                          v_row_stride, v_head_stride, k_rope, rope_row_stride, type, num_heads,
+                          nope_dim, rope_dim, value_dim, scale, causal, q_starts, k_starts,
+                          num_requests, num_queries, num_keys, num_queries, out, lse);
+  if (st != DSATOPK_OK || !p.q) return st;
+  if (!shared_starts || !shared_lens) return DSATOPK_ERR_INVALID_ARG;
+  p.shared_starts = shared_starts;
+  p.shared_lens = shared_lens;
+  const Cut c = shared_cut_of(num_heads, num_queries, max_keys);
+  st = check_room(p, c, workspace, workspace_bytes);
+  if (st != DSATOPK_OK) return st;
+  const bool bf16 = type == DSATOPK_BF16;
+  return c.wide ? bf16 ? launch_shared<Bf16, Shape<8>>(p, c, stream)
+                       : launch_shared<Fp16, Shape<8>>(p, c, stream)
+         : bf16 ? launch_shared<Bf16, Shape<4>>(p, c, stream)
+                : launch_shared<Fp16, Shape<4>>(p, c, stream);
 }

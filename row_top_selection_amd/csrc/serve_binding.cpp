@@ -699,44 +699,92 @@ PyObject* attend_shared(PyObject* const* args, Py_ssize_t n, PyObject* kw) {
   return pair(s.results.out, s.results.lse);
 }
 
+// The expanded forms' common tensors.
+struct Expanded {
+  const at::Tensor &q, &k, &v, &rope;
+  int32_t type, heads, queries, keys;
+  Expanded(PyObject* q_, PyObject* k_, PyObject* v_, PyObject* rope_)
+      : q(shaped(q_, 3, nullptr, "q")),
+        k(shaped(k_, 3, &q, "k")),
+        v(shaped(v_, 3, &q, "v")),
+        rope(shaped(rope_, 2, &q, "k_rope")),
+        type(element_type(q, "q", false)) {
+    for (const at::Tensor* t : {&k, &v, &rope})
+      if (t->scalar_type() != q.scalar_type() || t->size(0) != k.size(0) ||
+          (t != &rope && t->size(1) != q.size(1)))
+        refuse("k, v and k_rope must have q's type, as many rows as k, and q's heads");
+    if (q.size(2) != k.size(2) + rope.size(1))
+      refuse("q's last dimension must be k's and k_rope's together");
+    heads = size32(q.size(1), "q");
+    queries = size32(q.size(0), "q");
+    keys = size32(k.size(0), "k");
+  }
+};
+
+int truth(PyObject* o, int otherwise) {
+  const int is = o ? PyObject_IsTrue(o) : otherwise;
+  if (is < 0) throw Failed{};
+  return is;
+}
+
 PyObject* attend_expanded(PyObject* const* args, Py_ssize_t n, PyObject* kw) {
   static const char* const names[] = {"q", "k", "v", "k_rope", "q_starts", "k_starts", "max_queries",
                                       "scale", "causal", "out", "lse", "workspace", "stream"};
   const Args<13> a("attend_expanded", names, 8, args, n, kw);
-  const at::Tensor& q = shaped(a.at[0], 3, nullptr, "q");
-  const at::Tensor& k = shaped(a.at[1], 3, &q, "k");
-  const at::Tensor& v = shaped(a.at[2], 3, &q, "v");
-  const at::Tensor& rope = shaped(a.at[3], 2, &q, "k_rope");
-  const int32_t type = element_type(q, "q", false);
-  for (const at::Tensor* t : {&k, &v, &rope})
-    if (t->scalar_type() != q.scalar_type() || t->size(0) != k.size(0) ||
-        (t != &rope && t->size(1) != q.size(1)))
-      refuse("k, v and k_rope must have q's type, as many rows as k, and q's heads");
-  if (q.size(2) != k.size(2) + rope.size(1))
-    refuse("q's last dimension must be k's and k_rope's together");
+  const Expanded e(a.at[0], a.at[1], a.at[2], a.at[3]);
+  const at::Tensor &q = e.q, &k = e.k, &v = e.v, &rope = e.rope;
   const at::Tensor& qs = vector(a.at[4], -1, &q, "q_starts");
   if (qs.size(0) < 1) refuse("q_starts must have an entry more than there are requests");
   const at::Tensor& ks = vector(a.at[5], qs.size(0), &q, "k_starts");
   const int32_t longest = integer32(a.at[6], "max_queries");
   const float scale = number(a.at[7], "scale");
-  const int causal = a.at[8] ? PyObject_IsTrue(a.at[8]) : 1;
-  if (causal < 0) throw Failed{};
+  const int causal = truth(a.at[8], 1);
   const On on(q, a.at[12]);
   const Results r(on, a.at[9], a.at[10], q, v.size(2));
-  const int32_t requests = size32(qs.size(0) - 1, "q_starts"), heads = size32(q.size(1), "q");
-  const int32_t queries = size32(q.size(0), "q"), keys = size32(k.size(0), "k");
+  const int32_t requests = size32(qs.size(0) - 1, "q_starts");
   const at::Tensor room = workspace_of(
-      on, a.at[11], dsatopk_expanded_bytes(requests, heads, queries, keys, longest), q);
+      on, a.at[11], dsatopk_expanded_bytes(requests, e.heads, e.queries, e.keys, longest), q);
   check_status(
       dsatopk_attend_expanded(q.data_ptr(), stride(q, 0), stride(q, 1), k.data_ptr(), stride(k, 0),
                               stride(k, 1), v.data_ptr(), stride(v, 0), stride(v, 1),
-                              rope.data_ptr(), stride(rope, 0), type, heads,
+                              rope.data_ptr(), stride(rope, 0), e.type, e.heads,
                               size32(k.size(2), "k"), size32(rope.size(1), "k_rope"),
                               size32(v.size(2), "v"), scale, causal, ints(qs), ints(ks),
-                              requests, queries, keys, longest, r.out.data_ptr(),
+                              requests, e.queries, e.keys, longest, r.out.data_ptr(),
                               static_cast<float*>(r.lse.data_ptr()), room_ptr(room),
                               room_bytes(room), on.stream),
       "dsatopk_attend_expanded");
+  return pair(r.out, r.lse);
+}
+
+PyObject* attend_expanded_shared(PyObject* const* args, Py_ssize_t n, PyObject* kw) {
+  static const char* const names[] = {"q", "k", "v", "k_rope", "q_starts", "k_starts", "shared_starts",
+                                      "shared_lens", "scale", "max_keys", "causal", "out", "lse",
+                                      "workspace", "stream"};
+  const Args<15> a("attend_expanded_shared", names, 9, args, n, kw);
+  const Expanded e(a.at[0], a.at[1], a.at[2], a.at[3]);
+  const at::Tensor &q = e.q, &k = e.k, &v = e.v, &rope = e.rope;
+  const at::Tensor& qs = vector(a.at[4], -1, &q, "q_starts");
+  if (qs.size(0) < 1) refuse("q_starts must have an entry more than there are requests");
+  const at::Tensor& ks = vector(a.at[5], qs.size(0), &q, "k_starts");
+  const int32_t requests = size32(qs.size(0) - 1, "q_starts");
+  const at::Tensor& ss = vector(a.at[6], requests, &q, "shared_starts");
+  const at::Tensor& sl = vector(a.at[7], requests, &q, "shared_lens");
+  const float scale = number(a.at[8], "scale");
+  const int32_t longest = a.given(9) ? integer32(a.at[9], "max_keys") : e.keys;
+  const int causal = truth(a.at[10], 1);
+  const On on(q, a.at[14]);
+  const Results r(on, a.at[11], a.at[12], q, v.size(2));
+  const at::Tensor room =
+      workspace_of(on, a.at[13], dsatopk_expanded_shared_bytes(e.heads, e.queries, longest), q);
+  check_status(
+      dsatopk_attend_expanded_shared(
+          q.data_ptr(), stride(q, 0), stride(q, 1), k.data_ptr(), stride(k, 0), stride(k, 1), v.data_ptr(),
+          stride(v, 0), stride(v, 1), rope.data_ptr(), stride(rope, 0), e.type, e.heads,
+          size32(k.size(2), "k"), size32(rope.size(1), "k_rope"), size32(v.size(2), "v"), scale, causal,
+          ints(qs), ints(ks), ints(ss), ints(sl), requests, e.queries, e.keys, longest, r.out.data_ptr(),
+          static_cast<float*>(r.lse.data_ptr()), room_ptr(room), room_bytes(room), on.stream),
+      "dsatopk_attend_expanded_shared");
   return pair(r.out, r.lse);
 }
 
@@ -878,6 +926,20 @@ are its last tokens. Returns (out, lse): q's type [queries, heads, 128], and
 float32 [queries, heads]. workspace: uint8 of expanded_bytes(requests, heads,
 queries, keys, max_queries) (allocated when None).)doc";
 
+const char attend_expanded_shared_doc[] = R"doc(attend_expanded_shared(q, k, v, k_rope, q_starts, k_starts, shared_starts, shared_lens, scale, max_keys=None, causal=True, out=None, lse=None, workspace=None, stream=None)
+--
+
+attend_expanded for prompts behind keys that several of them share, which are
+there once.
+
+Request r's keys are rows shared_starts[r] .. shared_starts[r] + shared_lens[r]
+- 1 of k, v and k_rope (int32 [requests] each), which all of its queries see, and
+then its own, k_starts[r] .. k_starts[r + 1] - 1. Neighbouring requests with the
+same shared rows share the work on them. max_keys bounds a request's keys (the
+rows of k when None) and sets how few queries of many keys are split.
+workspace: uint8 of expanded_shared_bytes(heads, queries, max_keys) (allocated
+when None).)doc";
+
 #define SERVE_CALL(name) \
   {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(guarded<name>)), \
    METH_FASTCALL | METH_KEYWORDS, name##_doc}
@@ -886,7 +948,7 @@ PyMethodDef methods[] = {
     SERVE_CALL(page_maps),       SERVE_CALL(append_latent), SERVE_CALL(append_index),
     SERVE_CALL(scores_paged),    SERVE_CALL(scores_ragged),
     SERVE_CALL(attend_selected), SERVE_CALL(attend_paged), SERVE_CALL(attend_shared),
-    SERVE_CALL(attend_expanded),
+    SERVE_CALL(attend_expanded), SERVE_CALL(attend_expanded_shared),
     {"setup", setup, METH_VARARGS, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

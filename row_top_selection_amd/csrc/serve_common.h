@@ -162,6 +162,22 @@ __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_ex
 // The value of lane ^ 32.
 __device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32); }
 
+// The last g with key(g) <= x, of the rising keys of n (n at least 1, key(0) <=
+// x): 64 keys at a time, the same in all lanes of a wave.
+template <class Key>
+__device__ __forceinline__ int32_t last_below(int32_t n, int64_t x, int lane, Key key) {
+  int32_t at = 0;
+  while (n > 1) {
+    const int32_t step = (n + 63) / 64;
+    const int32_t i = lane * step;
+    const int32_t in = (int32_t)__popcll(__ballot(i < n && key(at + i) <= x));
+    const int32_t skip = in > 1 ? (in - 1) * step : 0;
+    at += skip;
+    n = min(step, n - skip);
+  }
+  return __builtin_amdgcn_readfirstlane(at);
+}
+
 // Bytes that stand in for cache entries which a call may not read (no page,
 // past a row's end).
 constexpr int kZeroBytes = 2048;

@@ -40,22 +40,6 @@ struct SharedParams {
   Joined to;
 };
 
-// The last g with key(g) <= x, of the rising keys of n (n at least 1, key(0) <=
-// x): 64 keys at a time, the same in all lanes of a wave.
-template <class Key>
-__device__ __forceinline__ int32_t last_below(int32_t n, int64_t x, int lane, Key key) {
-  int32_t at = 0;
-  while (n > 1) {
-    const int32_t step = (n + 63) / 64;
-    const int32_t i = lane * step;
-    const int32_t in = (int32_t)__popcll(__ballot(i < n && key(at + i) <= x));
-    const int32_t skip = in > 1 ? (in - 1) * step : 0;
-    at += skip;
-    n = min(step, n - skip);
-  }
-  return __builtin_amdgcn_readfirstlane(at);
-}
-
 // First row of group g; the first group starts at row 0 and the last one ends
 // behind the last row, whatever the list says.
 __device__ __forceinline__ int32_t start_of(const SharedParams& p, int32_t g) {
