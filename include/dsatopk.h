@@ -582,14 +582,14 @@ int dsatopk_attend_paged(const void* q, int64_t q_row_stride, int64_t q_head_str
  *                 Negative values are read as 0, those past the table are cut.
  *   max_shared_len, max_own_len  upper bounds on shared_lens and on the tokens
  *                 that a row reads by itself, at most 2^31 - 65. They set how
- *                 the tokens are split over workgroups (and the workspace's
+ *                 many workgroups are started at most (and the workspace's
  *                 size); longer ones are read whole all the same, but a bound of 0
  *                 is taken at its word: with max_shared_len 0 rows read all
- *                 of their tokens by themselves, with max_own_len 0 none past
- *                 their group's shared ones.
+ *                 of their tokens by themselves, with max_own_len 0 (and the
+ *                 other not 0) none past their group's shared ones.
  *   workspace     at least dsatopk_shared_bytes(num_rows, num_heads,
  *                 latent_dim, num_groups, max_shared_len, max_own_len) bytes,
- *                 16-byte aligned (NULL where that is 0).
+ *                 16-byte aligned. Calls that overlap must not share one.
  *
  * The other arguments are those of dsatopk_attend_paged, as are the rounding
  * and the errors. A shared position that some but not all rows of its group see

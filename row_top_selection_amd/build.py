@@ -15,7 +15,7 @@ SOURCES = [PKG / "csrc" / name for name in (
     "dsatopk.hip", "page_maps.hip", "append_cache.hip", "index_scores.hip", "latent_attend.hip",
     "shared_attend.hip", "expanded_attend.hip")]
 HEADERS = [PKG / "csrc" / "select_device.h", PKG / "csrc" / "serve_common.h",
-           PKG / "csrc" / "latent_tiles.h",
+           PKG / "csrc" / "latent_tiles.h", PKG / "csrc" / "wide_tiles.h",
            ROOT / "include" / "dsatopk.h"]
 LIB = PKG / "libdsatopk.so"
 EXT_SOURCE = PKG / "csrc" / "serve_binding.cpp"

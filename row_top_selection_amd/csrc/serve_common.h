@@ -117,8 +117,8 @@ __device__ __forceinline__ void wait_copies() {
 // Until all but this wave's last n loads and copies have arrived.
 template <int n>
 __device__ __forceinline__ void wait_copies_but() {
-  static_assert(n >= 0 && n < 16, "the low four bits of the count");
-  __builtin_amdgcn_s_waitcnt(0x0f70 | n);
+  static_assert(n >= 0 && n < 64, "six bits of the count, the low four first, the others on top");
+  __builtin_amdgcn_s_waitcnt(0x0f70 | (n & 15) | (n >> 4 << 14));
   asm volatile("" ::: "memory");
 }
 

@@ -17,8 +17,18 @@
 // counts how many of the tokens its row sees (drafted tokens, whose rows see
 // one token more each). Tiles, products and softmax are those of one row's heads
 // (latent_tiles.h).
+//
+// How many tokens there are of which kind only the device knows. Each workgroup
+// adds up the tiles of all blocks of lanes (a few thousand lengths at most, from
+// L2) and takes its equal share of them, in their order: the end of one block,
+// blocks as a whole, the beginning of the last one. So the card is full from
+// the first to the last tile whatever the lengths are, and a block has as
+// many parts as workgroups worked on it. What one workgroup did alone it writes as the
+// result.
 
-#include "latent_tiles.h"
+#include <type_traits>
+
+#include "wide_tiles.h"
 
 namespace dsatopk_serve {
 namespace {
@@ -33,33 +43,167 @@ struct SharedParams {
   const int32_t* table_rows;
   const int32_t* group_starts;
   const int32_t* shared_lens;
-  int32_t groups, table_width;
-  int32_t shared_splits, own_splits, own_blocks;
-  uint32_t slots, shared_jobs;  // blocks of lanes that the groups may have, workgroups for them
+  int32_t groups, table_width, rows, heads;
+  int32_t lanes, own_lanes, own_blocks;  // heads of a shared block, of an own one; own blocks of a row
+  bool shares, owns;
   float scale2;
-  Joined to;
+  char* out;
+  float* lse;
+  // Parts: vectors [number, lanes, latent], references and sums [number, lanes, 2];
+  // first and last part of each block [blocks, 2].
+  float* shared_part;
+  float* shared_state;
+  int32_t* shared_numbers;
+  float* own_part;
+  float* own_state;
+  int32_t* own_numbers;
 };
 
-// First row of group g; the first group starts at row 0 and the last one ends
-// behind the last row, whatever the list says.
-__device__ __forceinline__ int32_t start_of(const SharedParams& p, int32_t g) {
-  return g <= 0 ? 0 : g >= p.groups ? p.to.rows : min(max(p.group_starts[g], 0), p.to.rows);
+// The arguments as they are in memory, to be loaded anew: by itself the compiler keeps
+// them all in registers, and spills, across the loops over tokens.
+using Args = const __attribute__((address_space(4))) SharedParams;
+__device__ __forceinline__ Args& args() {
+  Args* p = (Args*)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return *p;
 }
 
-__device__ __forceinline__ int32_t positions(const SharedParams& p) {
-  return (int32_t)min((int64_t)p.table_width << p.cache.page_bits, (int64_t)(INT32_MAX - 64));
-}
+constexpr int kTile = 64;   // tokens of a unit of work
+constexpr int kBegin = 2;   // a block costs its tiles and this many (first loads, last sums, the join)
+constexpr int kLeast = 4;   // units that a workgroup is started for
+constexpr int kStarts = 1024;  // groups whose starts are kept in LDS
 
-__device__ __forceinline__ int32_t shared_of(const SharedParams& p, int32_t g) {
-  return p.shared_splits ? min(max(p.shared_lens[g], 0), positions(p)) : 0;
+__device__ __forceinline__ int32_t positions(Args& p) {
+  return (int32_t)min((int64_t)p.table_width << p.cache.page_bits, (int64_t)(INT32_MAX - kTile));
 }
-
-__device__ __forceinline__ int32_t length_of(const SharedParams& p, int64_t row) {
+__device__ __forceinline__ int32_t shared_of(Args& p, int32_t g) {
+  return p.shares ? min(max(p.shared_lens[g], 0), positions(p)) : 0;
+}
+__device__ __forceinline__ int32_t length_of(Args& p, int64_t row) {
   return min(max(p.seq_lens[row], 0), positions(p));
 }
-
-__device__ __forceinline__ const int32_t* pages_of(const SharedParams& p, int64_t row) {
+__device__ __forceinline__ const int32_t* pages_of(Args& p, int64_t row) {
   return p.table + (p.table_rows ? p.table_rows[row] : row) * p.table_stride;
+}
+
+// First rows of the groups: of the first one 0, and the last one ends behind the last
+// row, whatever the list says.
+__device__ __forceinline__ int32_t start_of(Args& p, int32_t g) {
+  return g <= 0 ? 0 : g >= p.groups ? p.rows : min(max(p.group_starts[g], 0), p.rows);
+}
+struct Starts {
+  Args& p;
+  const int32_t* kept;  // in LDS, if they fit
+  __device__ __forceinline__ int32_t operator()(int32_t g) const {
+    return p.groups <= kStarts && g < p.groups ? kept[max(g, 0)] : start_of(p, g);
+  }
+  // The group of a row, a lane by itself.
+  __device__ __forceinline__ int32_t of(int32_t row) const {
+    int32_t lo = 0, hi = p.groups;
+    while (hi - lo > 1) {
+      const int32_t mid = (lo + hi) >> 1;
+      if ((*this)(mid) <= row)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    return lo;
+  }
+};
+
+// Group g's blocks of lanes are numbered from here on, which leaves room for all
+// of those of the groups before it.
+__device__ __forceinline__ int64_t first_block(Args& p, int32_t start, int32_t g) {
+  return (int64_t)start * p.heads / p.lanes + g;
+}
+
+// The work in its order: the shared tokens of each group, then the own ones of
+// each row; `blocks` times `tiles`.
+struct Entry {
+  int32_t tiles, blocks;
+  __device__ __forceinline__ int64_t units() const { return tiles > 0 ? (int64_t)blocks * (tiles + kBegin) : 0; }
+};
+__device__ __forceinline__ Entry entry_of(Args& p, const Starts& starts, int32_t e, int32_t& g) {
+  if (e < p.groups) {
+    const int64_t lanes = (int64_t)max(starts(e + 1) - starts(e), 0) * p.heads;
+    return {lanes ? (shared_of(p, e) + kTile - 1) / kTile : 0, (int32_t)((lanes + p.lanes - 1) / p.lanes)};
+  }
+  const int32_t row = e - p.groups;
+  if (g < 0 || starts(g) > row) g = starts.of(row);
+  while (g + 1 < p.groups && starts(g + 1) <= row) ++g;
+  const int32_t own = length_of(p, row) - shared_of(p, g);
+  return {p.owns && own > 0 ? (own + kTile - 1) / kTile : 0, p.own_blocks};
+}
+
+// This lane's head of a part: into the result if the part is all that there is, else to its place.
+template <class T, class P>
+__device__ __forceinline__ void put_part(Args& p, const State<P>& st, float top, float sum,
+                                         bool whole, int64_t row, int32_t head, float* part, float* state,
+                                         int64_t place, int lane) {
+  const int group = lane >> 4;
+  if (whole) {
+    Joined to{};
+    to.heads = p.heads;
+    to.splits = 1;
+    to.out = p.out;
+    to.lse = p.lse;
+    put<T, P>(st, top, sum, to, row, head, 0, lane);
+    return;
+  }
+  if (group == 0) {
+    state[place * 2] = top;
+    state[place * 2 + 1] = sum;
+  }
+  if (top == -INFINITY && sum == 0.0f) return;  // nothing seen: the join skips it
+  float* to = part + place * P::kLatent + 4 * group;
+#pragma unroll
+  for (int b = 0; b < P::kBlocks; ++b) *reinterpret_cast<f32x4*>(to + b * 16) = st.o[b];
+}
+
+// The same for 32 heads a wave, where register i of block b holds element 32 * b + 8 * (i / 4) + 4 *
+// (lane / 32) + i % 4. `more`: the sums go on by another reference, and these are put to their place until then;
+// `some`: some have been put there before.
+template <class T>
+__device__ __forceinline__ void put_wide(Args& p, WideState& st, bool more, bool some, bool whole, int64_t row,
+                                         int32_t head, float* part, float* state, int64_t place, int lane) {
+  const int half = lane >> 5;
+  float top = st.top, sum = st.sum, by = 1.0f, before = 0.0f;
+  float* to = part + place * Wide::kLatent + 4 * half;
+  bool kept = false;
+  if (some) {
+    const float x = state[place * 2], n = state[place * 2 + 1];
+    kept = !(x == -INFINITY && n == 0.0f);
+    const float ref = fmaxf(x, top);
+    before = kept ? exp2_fast(x - (ref == -INFINITY ? 0.0f : ref)) : 0.0f;
+    by = top == -INFINITY ? 0.0f : exp2_fast(top - ref);
+    sum = sum * by + n * before;
+    top = ref;
+  }
+  const bool result = whole && !more;
+  if (result) by *= sum == 0.0f ? 0.0f : 1.0f / sum, before *= sum == 0.0f ? 0.0f : 1.0f / sum;
+  char* out = p.out + ((row * p.heads + head) * Wide::kLatent + 4 * half) * 2;
+  if (result) {
+    if (p.lse && half == 0) p.lse[row * p.heads + head] = (top + log2f(sum)) * kLn2;
+  } else {
+    // (both halves have read the state before one writes it)
+    if (half == 0) {
+      state[place * 2] = top;
+      state[place * 2 + 1] = sum;
+    }
+    if (top == -INFINITY && sum == 0.0f) return;  // nothing seen: the join skips it
+  }
+#pragma unroll
+  for (int b = 0; b < Wide::kBlocks; ++b)
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      f32x4 v = {st.o[b][i], st.o[b][i + 1], st.o[b][i + 2], st.o[b][i + 3]};
+      v *= by;
+      if (kept) v += *reinterpret_cast<const f32x4*>(to + b * 32 + 2 * i) * before;
+      if (result)
+        *reinterpret_cast<u32x2*>(out + (b * 32 + 2 * i) * 2) = u32x2{T::pack(v[0], v[1]), T::pack(v[2], v[3])};
+      else
+        *reinterpret_cast<f32x4*>(to + b * 32 + 2 * i) = v;
+    }
 }
 
 template <class P>
@@ -69,190 +213,405 @@ __device__ __forceinline__ void clear(State<P>& st) {
 #pragma unroll
   for (int b = 0; b < P::kBlocks; ++b) st.o[b] = f32x4{};
 }
+// What a workgroup is at, in LDS, for the same reason.
+struct Job {
+  int64_t at, end;     // units, of all
+  int64_t in;          // units into the entry
+  int64_t number;      // of the part
+  int32_t entry;
+  int32_t row0, rows;  // of the group; the row, of own tokens
+  int32_t shared, block, first, last;
+  int32_t whole;       // the block's only part
+};
 
-// This workgroup's share of `tiles` tiles, part `split` of `splits`.
-__device__ __forceinline__ void share(int32_t tiles, int32_t splits, int32_t split, int32_t& first,
-                                      int32_t& last) {
-  const int32_t per = (tiles + splits - 1) / splits;
-  first = min(split * per, tiles);
-  last = min(first + per, tiles);
+__device__ __forceinline__ Cache cache_of(Args& p) {
+  return Cache{p.cache.at, p.cache.page, p.cache.token, p.cache.pages, p.cache.page_bits};
+}
+__device__ __forceinline__ int32_t uniform(int32_t x) { return __builtin_amdgcn_readfirstlane(x); }
+
+// The block of lanes of a job: lane i's row, its head, the tokens that it sees; and where its part goes.
+struct Block {
+  Args& p;
+  bool own;
+  int32_t row, head, heads, count, shared;
+  __device__ __forceinline__ Block(Args& args, const Job& job, int32_t lanes)
+      : p(args), own(uniform(job.entry) >= args.groups), heads(args.heads), shared(uniform(job.shared)) {
+    const int64_t begin = (int64_t)uniform(job.block) * (own ? p.own_lanes : lanes);
+    row = uniform(job.row0) + (int32_t)(begin / heads);
+    head = (int32_t)(begin % heads);
+    count = (int32_t)min((int64_t)uniform(job.rows) * heads - begin, (int64_t)(own ? p.own_lanes : lanes));
+  }
+  __device__ __forceinline__ int32_t row_of(int32_t i) const { return row + (head + i) / heads; }
+  __device__ __forceinline__ int32_t head_of(int32_t i) const { return (head + i) % heads; }
+  // Of a group's shared tokens; of a row's own ones, all.
+  __device__ __forceinline__ int32_t sees(int32_t i) const {
+    const int32_t len = length_of(p, row_of(i));
+    return own ? len - shared : min(len, shared);
+  }
+  __device__ __forceinline__ const char* queries(int32_t i) const {
+    return i < count ? p.q + row_of(i) * p.q_row + head_of(i) * p.q_head : zero_row();
+  }
+  // Whether the job's part, if it is the block's only one, is all that there is of the row.
+  __device__ __forceinline__ bool alone(int32_t i) const {
+    return own ? shared == 0 : !p.owns || length_of(p, row_of(i)) <= shared;
+  }
+  __device__ __forceinline__ float* part() const { return own ? p.own_part : p.shared_part; }
+  __device__ __forceinline__ float* state() const { return own ? p.own_state : p.shared_state; }
+  __device__ __forceinline__ int64_t place(const Job& job, int32_t lanes, int32_t i) const {
+    return job.number * (own ? p.own_lanes : lanes) + i;
+  }
+};
+
+// A job's tiles: of a group's shared tokens, or of a row's own.
+template <class T, class P, bool kOwn>
+__device__ __forceinline__ void attend_job(const Job& job, char* tiles, uint32_t (*masks)[P::kWaves],
+                                           float (*joined)[P::kWaves][16], int wave, int lane) {
+  constexpr int kLanes = P::kLanes, kPer = kTile / P::kTile;
+  int32_t len = 0, base, first, last;  // tokens that any lane sees, and where they begin
+  {
+    const Block block(args(), job, kLanes);
+#pragma unroll
+    for (int i = 0; i < kLanes; i += 64)
+      if (i + lane < block.count) len = max(len, block.sees(i + lane));
+#pragma unroll
+    for (int d = 32; d; d >>= 1) len = max(len, __shfl_xor(len, d));
+    len = uniform(len);
+    base = block.own ? block.shared : 0;
+    first = uniform(job.first) * kPer;
+    last = min(uniform(job.last) * kPer, (len + P::kTile - 1) / P::kTile);
+  }
+  // What the lane's head is, and sees, from its place in the workgroup: when it is needed.
+  auto queries = [&](int32_t i) { return Block(args(), job, kLanes).queries(i); };
+  auto mine = [&](int32_t i) {
+    const Block block(args(), job, kLanes);
+    return i < block.count ? block.sees(i) : INT32_MAX;
+  };
+  if constexpr (std::is_same_v<P, Wide>) {
+    auto done = [&](WideState& st, bool more, bool some) {
+      const Block block(args(), job, kLanes);
+      const int32_t now = here(lane), i = wave * 32 + now % 32;
+      if (i < block.count)
+        put_wide<T>(block.p, st, more, some, job.whole && block.alone(i), block.row_of(i), block.head_of(i),
+                    block.part(), block.state(), block.place(job, kLanes, i), now);
+    };
+    Args& p = args();
+    attend_wide<T>(tiles, masks, cache_of(p), pages_of(p, uniform(job.row0)), base, len, first, last,
+                   [&](int now) { return queries(wave * 32 + now % 32); },
+                   [&](int now) { return mine(wave * 32 + now % 32); }, done, wave, lane, p.scale2);
+  } else {
+    State<P> st;
+    clear<P>(st);
+    {
+      const int32_t i = wave % P::kWH * 16 + (lane & 15);
+      // a lane that sees nothing of these tokens must not ask for a reference at every tile
+      if (!kOwn && mine(i) <= first * P::kTile) st.top = 0.0f;
+      Args& p = args();
+      const Places<P> places(wave, lane);
+      attend_range<T, P, true, !kOwn>(st, tiles, masks, cache_of(p), pages_of(p, uniform(job.row0)), base, len,
+                                      first, last, queries(i), kOwn ? 0 : mine(i), places, wave, lane, p.scale2);
+    }
+    const int32_t now = here(lane), i = wave % P::kWH * 16 + (now & 15);
+    float sum = head_sum(st.sum);
+    float top = !kOwn && mine(i) <= job.first * kTile ? -INFINITY : st.top;
+    if constexpr (P::kWT > 1) join_groups<P>(st, top, sum, tiles, joined, wave, now);
+    const Block block(args(), job, kLanes);
+    if (wave / P::kWH == 0 && i < block.count)
+      put_part<T, P>(block.p, st, top, sum, job.whole && block.alone(i), block.row_of(i), block.head_of(i),
+                     block.part(), block.state(), block.place(job, kLanes, i), now);
+  }
 }
 
-// Part `split` of a group's shared tokens, for block `slot` of lanes. Group g's
-// blocks begin at number start_g * heads / lanes + g, which leaves room
-// for all of them.
-template <class T, class P>
-__device__ __forceinline__ void shared_part(const SharedParams& p, char* tiles,
-                                            uint32_t (*masks)[P::kWaves], float (*joined)[P::kWaves][16],
-                                            uint32_t slot, int32_t split, int wave, int lane) {
-  constexpr int kLanes = P::kWH * 16;
-  const int32_t heads = p.to.heads;
-  auto first_slot = [&](int32_t g) { return (int64_t)start_of(p, g) * heads / kLanes + g; };
-  const int32_t g = last_below(p.groups, slot, lane, first_slot);
-  const int32_t row0 = start_of(p, g), rows = start_of(p, g + 1) - row0;
-  const int64_t begin = ((int64_t)slot - first_slot(g)) * kLanes, lanes = (int64_t)rows * heads;
-  if (begin < 0 || begin >= lanes) return;  // starts that do not rise may say anything
-  const int32_t shared = shared_of(p, g);
-
-  // Lane i of the block: its row, its head, the tokens that it sees.
-  const int32_t row1 = row0 + (int32_t)(begin / heads), head1 = (int32_t)(begin % heads);
-  const int32_t count = (int32_t)min(lanes - begin, (int64_t)kLanes);
-  auto row_of = [&](int32_t i) { return row1 + (head1 + i) / heads; };
-  auto sees = [&](int32_t i) { return min(length_of(p, row_of(i)), shared); };
-  int32_t most = 0;
-#pragma unroll
-  for (int i = 0; i < kLanes; i += 64)
-    if (i + lane < count) most = max(most, sees(i + lane));
-#pragma unroll
-  for (int d = 32; d; d >>= 1) most = max(most, __shfl_xor(most, d));
-  most = __builtin_amdgcn_readfirstlane(most);
-
-  int32_t first, last;
-  share((most + P::kTile - 1) / P::kTile, p.shared_splits, split, first, last);
-  State<P> st;
-  clear<P>(st);
-  {
-    const int32_t i = wave % P::kWH * 16 + (lane & 15);
-    const bool real = i < count;
-    const int32_t mine = real ? sees(i) : INT32_MAX;
-    const char* qh = real ? p.q + row_of(i) * p.q_row + (head1 + i) % heads * p.q_head : zero_row();
-    // a lane that sees nothing of these tokens must not ask for a reference at every tile
-    if (mine <= first * P::kTile) st.top = 0.0f;
-    const Places<P> places(wave, lane);
-    attend_range<T, P, true, true>(st, tiles, masks, p.cache, pages_of(p, row0), 0, most, first, last,
-                                   qh, mine, places, wave, lane, p.scale2);
-  }
-  // which lane this is, anew: until here the registers are the tokens'
-  const int32_t i = wave % P::kWH * 16 + (here(lane) & 15);
-  const bool real = i < count;
-  const int64_t row = row_of(i);
-  const int head = (head1 + i) % heads;
-  float sum = head_sum(st.sum);
-  float top = real && sees(i) <= first * P::kTile ? -INFINITY : st.top;
-  if constexpr (P::kWT > 1) {
-    join_groups<P>(st, top, sum, tiles, joined, wave, lane);
-    if (wave / P::kWH > 0) return;
-  }
-  if (real) put<T, P>(st, top, sum, p.to, row, head, split, lane);
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+  return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int32_t)(x >> 32)) << 32 |
+                   (uint32_t)__builtin_amdgcn_readfirstlane((int32_t)x));
+}
+__device__ __forceinline__ int64_t from_below(int64_t x, int d) {
+  return (int64_t)((uint64_t)(uint32_t)__shfl_up((int32_t)(x >> 32), d) << 32 | (uint32_t)__shfl_up((int32_t)x, d));
 }
 
-// Part `split` of a row's own tokens, for block `block` of its heads.
-template <class T, class P>
-__device__ __forceinline__ void own_part(const SharedParams& p, char* tiles, uint32_t (*masks)[P::kWaves],
-                                         float (*joined)[P::kWaves][16], int64_t row, int32_t block,
-                                         int32_t split, int wave, int lane) {
-  const int32_t g = last_below(p.groups, row, lane, [&](int32_t i) { return (int64_t)start_of(p, i); });
-  const int32_t len = length_of(p, row), base = min(shared_of(p, g), len);
-  int32_t first, last;
-  share((len - base + P::kTile - 1) / P::kTile, p.own_splits, split, first, last);
-  State<P> st;
-  clear<P>(st);
-  {
-    const int head = (block * P::kWH + wave % P::kWH) * 16 + (lane & 15);
-    const char* qh = head < p.to.heads ? p.q + row * p.q_row + head * p.q_head : zero_row();
-    const Places<P> places(wave, lane);
-    attend_range<T, P, true, false>(st, tiles, masks, p.cache, pages_of(p, row), base, len - base, first,
-                                    last, qh, 0, places, wave, lane, p.scale2);
+// The next job of a workgroup, from its units: false if there is none. The same in all lanes.
+__device__ __forceinline__ bool next_job(Job& job, const Starts& starts, int tid, int lane) {
+  Args& p = args();
+  const int32_t entries = p.groups + (p.owns ? p.rows : 0);
+  int32_t e = uniform(job.entry);
+  int64_t in = uniform(job.in), at = uniform(job.at);
+  const int64_t end = uniform(job.end);
+  while (at < end) {
+    int32_t g = -1;
+    const Entry x = entry_of(p, starts, e, g);
+    if (in >= x.units()) {
+      // the next entry that has any work, 64 at a time
+      in = 0;
+      uint64_t some = 0;
+      for (++e; e < entries; e += 64) {
+        int32_t mine = -1;
+        some = __ballot(e + lane < entries && entry_of(p, starts, min(e + lane, entries - 1), mine).units() > 0);
+        if (some) break;
+      }
+      if (!some) return false;
+      e += __builtin_ctzll(some);
+      continue;
+    }
+    const int32_t each = x.tiles + kBegin;
+    const int32_t block = (int32_t)(in / each), unit = (int32_t)(in - (int64_t)block * each);
+    const int32_t n = (int32_t)min((int64_t)(each - unit), end - at);
+    const int32_t first = max(unit - kBegin, 0), last = unit + n - kBegin;
+    in += n;
+    at += n;
+    if (last <= first) continue;
+    // The parts of a block are numbered as its workgroups are: by the workgroup's
+    // number and the block's, of which one at least grows from part to part.
+    const bool own = e >= p.groups;
+    const int32_t row0 = own ? e - p.groups : starts(e);
+    const int64_t which = own ? (int64_t)row0 * p.own_blocks + block : first_block(p, row0, e) + block;
+    const int64_t number = which + blockIdx.x;
+    if (tid == 0) {
+      int32_t* numbers = (own ? p.own_numbers : p.shared_numbers) + which * 2;
+      if (first == 0) numbers[0] = (int32_t)number;
+      if (last == x.tiles) numbers[1] = (int32_t)number;
+      job = Job{at, end, in, number, e, row0, own ? 1 : starts(e + 1) - row0, shared_of(p, own ? g : e), block,
+                first, last, first == 0 && last == x.tiles};
+    }
+    return true;
   }
-  const int head = (block * P::kWH + wave % P::kWH) * 16 + (here(lane) & 15);
-  float sum = head_sum(st.sum);
-  float top = st.top;
-  if constexpr (P::kWT > 1) {
-    join_groups<P>(st, top, sum, tiles, joined, wave, lane);
-    if (wave / P::kWH > 0) return;
-  }
-  if (head < p.to.heads) put<T, P>(st, top, sum, p.to, row, head, p.shared_splits + split, lane);
+  return false;
 }
 
 // PS for the shared parts, PO for the own ones: workgroups of the same size.
 template <class T, class PS, class PO>
-__global__ __launch_bounds__(PS::kBlock, 2) void shared_kernel(SharedParams p) {
-  static_assert(PS::kBlock == PO::kBlock && PS::kBuffer == PO::kBuffer, "one launch for both");
-  __shared__ __attribute__((aligned(1024))) char tiles[2 * PS::kBuffer];
-  __shared__ uint32_t masks[2][PS::kWaves];
-  __shared__ float joined[2][PS::kWaves][16];
+__global__ __launch_bounds__(PS::kBlock, (std::is_same_v<PS, Wide> ? 1 : 2)) void shared_kernel(SharedParams) {
+  constexpr int kWaves = PS::kWaves;
+  constexpr int kSpace = std::is_same_v<PS, Wide> ? Wide::kRing * Wide::kBuffer : 2 * PS::kBuffer;
+  static_assert(PS::kBlock == PO::kBlock && 2 * PO::kBuffer <= kSpace, "one launch for both");
+  struct Rest {
+    Job job;
+    int64_t sums[kWaves];
+    float joined[2][kWaves][16];
+    int32_t kept[kStarts];
+    uint32_t masks[Wide::kRing][kWaves];
+  };
+  __shared__ __attribute__((aligned(1024))) char tiles[kSpace + sizeof(Rest)];
+  Rest& rest = *reinterpret_cast<Rest*>(tiles + kSpace);
+  auto& job = rest.job;
+  auto& sums = rest.sums;
+  auto& joined = rest.joined;
+  auto& kept = rest.kept;
+  auto& masks = rest.masks;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  uint32_t id = blockIdx.x;
-  if (id < p.shared_jobs) {
-    // Blocks that read the same tokens are 8 apart, on one XCD, where there
-    // are that many parts.
-    const uint32_t each = p.shared_splits % 8 ? p.shared_splits : 8;
-    const uint32_t slot = id / each % p.slots;
-    const int32_t split = id / each / p.slots * each + id % each;
-    shared_part<T, PS>(p, tiles, masks, joined, slot, split, wave, lane);
-  } else {
-    id -= p.shared_jobs;
-    const int32_t split = id % p.own_splits, block = id / p.own_splits % p.own_blocks;
-    own_part<T, PO>(p, tiles, masks, joined, id / p.own_splits / p.own_blocks, block, split, wave, lane);
-  }
-}
+  {
+    Args& p = args();
+    if (p.groups <= kStarts)
+      for (int g = tid; g < p.groups; g += PS::kBlock) kept[g] = start_of(p, g);
+    __syncthreads();
+    const Starts starts{p, kept};
 
-// How a call is cut: heads packed into a workgroup for the shared tokens, and
-// parts of the token axes.
-struct Cut {
-  int32_t lanes, shared_splits, own_splits;
-};
-
-int head_block(int32_t heads) { return heads <= 32 ? 32 : heads <= 64 ? 64 : 128; }
-
-Cut cut_of(int32_t rows, int32_t heads, int32_t groups, int64_t max_shared, int64_t max_own) {
-  constexpr int kUnit = 64;
-  constexpr double kPart = 4;
-  constexpr int kTry[] = {1, 2, 4, 8, 16, 24, 32, 40, 48, 64, 96, 128};
-  const int64_t each = ((int64_t)rows + groups - 1) / groups * heads;  // lanes of a mean group
-  Cut c;
-  c.lanes = each <= 32 ? 32 : each <= 64 ? 64 : 128;
-  const int hb = head_block(heads) < c.lanes ? head_block(heads) : c.lanes;
-  const double places = c.lanes == 128 ? 256 : 512;
-  const double blocks = (double)groups * ((each + c.lanes - 1) / c.lanes);
-  const double own = (double)rows * ((heads + hb - 1) / hb);
-  const int64_t shared_tiles = (max_shared + kUnit - 1) / kUnit, own_tiles = (max_own + kUnit - 1) / kUnit;
-  double least = -1;
-  c.shared_splits = 0;
-  c.own_splits = 1;
-  for (const int s : kTry) {
-    if (s > 1 && s > shared_tiles) break;
-    for (const int o : kTry) {
-      if (o > 1 && o > own_tiles) break;
-      const double a = max_shared ? (double)((shared_tiles + s - 1) / s) + kPart : 0;
-      const double b = max_own ? (double)((own_tiles + o - 1) / o) + kPart : 0;
-      const double work = blocks * s * a + own * o * b;
-      const double cost = work / places + (a > b ? a : b);
-      if (least < 0 || cost < least) {
-        least = cost;
-        c.shared_splits = max_shared ? s : 0;
-        c.own_splits = max_own || !max_shared ? o : 0;
+    // all units, and those before this thread's entries
+    const int32_t entries = p.groups + (p.owns ? p.rows : 0);
+    const int32_t chunk = (entries + PS::kBlock - 1) / PS::kBlock;
+    const int32_t e0 = min(tid * chunk, entries), e1 = min(e0 + chunk, entries);
+    int64_t units = 0;
+    int32_t g = -1;
+    for (int32_t e = e0; e < e1; ++e) units += entry_of(p, starts, e, g).units();
+    int64_t below = units;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int64_t o = from_below(below, d);
+      if (lane >= d) below += o;
+    }
+    if (lane == 63) sums[wave] = below;
+    __syncthreads();
+    int64_t all = 0;
+    below -= units;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      if (w < wave) below += sums[w];
+      all += sums[w];
+    }
+    const int64_t per = max((all + gridDim.x - 1) / gridDim.x, (int64_t)kLeast);
+    const int64_t at = blockIdx.x * per, end = min(at + per, all);
+    if (uniform(at) >= uniform(end)) return;
+    if (at >= below && at < below + units) {
+      g = -1;
+      for (int32_t e = e0; e < e1; ++e) {
+        const int64_t n = entry_of(p, starts, e, g).units();
+        if (at < below + n) {
+          job.at = at;
+          job.end = end;
+          job.in = at - below;
+          job.entry = e;
+          break;
+        }
+        below += n;
       }
     }
   }
-  return c;
+  while (true) {
+    __syncthreads();  // the job is there, the tiles' space is free
+    const int now = here(tid);  // what is made of it is made in every round, not kept across them
+    if (!next_job(job, Starts{args(), kept}, now, now & 63)) return;
+    __syncthreads();
+    if (!std::is_same_v<PS, PO> && uniform(job.entry) >= args().groups)
+      attend_job<T, PO, true>(job, tiles, masks, joined, wave, now & 63);
+    else
+      attend_job<T, PS, false>(job, tiles, masks, joined, wave, now & 63);
+  }
 }
 
+// Joins the parts of 4 * kEach elements of one row's head: the shared ones, then
+// the row's own. First the common maximum and the parts' factors; then kEach
+// threads for each of kJoinBlock / kEach sets of parts, 4 elements each. What
+// is a single part has been written as the result.
+constexpr int kPlaces = 512;  // workgroups at most, and so parts of a block but one
+
+template <class T, int kLatent, int kEach>
+__global__ __launch_bounds__(kJoinBlock) void shared_join_kernel(SharedParams) {
+  Args& p = args();
+  constexpr int kSides = kJoinBlock / kEach, kSlices = kLatent / (4 * kEach), kWaves = kJoinBlock / 64;
+  __shared__ float tops[kWaves], sums[kWaves];
+  __shared__ float factor[2 * (kPlaces + 1)];
+  __shared__ __attribute__((aligned(16))) float half[kJoinBlock * 4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const uint32_t which = blockIdx.x / kSlices, slice = blockIdx.x % kSlices;
+  const int32_t row = which / p.heads, head = which % p.heads;
+  const int32_t g = last_below(p.groups, row, lane, [&](int32_t i) { return (int64_t)start_of(p, i); });
+  const int32_t shared = shared_of(p, g);
+  int32_t n = 0, m = 0;  // shared parts, own parts
+  int64_t first = 0, own = 0;
+  if (shared > 0) {
+    const int32_t start = start_of(p, g);
+    const int64_t i = (int64_t)(row - start) * p.heads + head;
+    const int32_t* numbers = p.shared_numbers + (first_block(p, start, g) + i / p.lanes) * 2;
+    n = numbers[1] - numbers[0] + 1;
+    first = (int64_t)numbers[0] * p.lanes + i % p.lanes;
+  }
+  if (p.owns && length_of(p, row) > shared) {
+    const int32_t* numbers = p.own_numbers + ((int64_t)row * p.own_blocks + head / p.own_lanes) * 2;
+    m = numbers[1] - numbers[0] + 1;
+    own = (int64_t)numbers[0] * p.own_lanes + head % p.own_lanes;
+  }
+  const int32_t parts = n + m;
+  if (parts == 1) return;
+  auto state_of = [&](int32_t s) {
+    return s < n ? p.shared_state + (first + (int64_t)s * p.lanes) * 2
+                 : p.own_state + (own + (int64_t)(s - n) * p.own_lanes) * 2;
+  };
+  auto part_of = [&](int32_t s) {
+    return s < n ? p.shared_part + (first + (int64_t)s * p.lanes) * kLatent
+                 : p.own_part + (own + (int64_t)(s - n) * p.own_lanes) * kLatent;
+  };
+  float top = -INFINITY;
+  for (int32_t s = tid; s < parts; s += kJoinBlock) top = fmaxf(top, state_of(s)[0]);
+#pragma unroll
+  for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
+  if (lane == 0) tops[wave] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) top = fmaxf(top, tops[w]);
+  float sum = 0.0f;
+  for (int32_t s = tid; s < parts; s += kJoinBlock) {
+    const float x = state_of(s)[0], y = state_of(s)[1];
+    const bool empty = x == -INFINITY && y == 0.0f;  // such a part has written no vector
+    const float by = empty ? 0.0f : exp2_fast(x - (top == -INFINITY ? 0.0f : top));
+    factor[s] = empty ? -1.0f : by;
+    sum += y * by;
+  }
+#pragma unroll
+  for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
+  if (lane == 0) sums[wave] = sum;
+  __syncthreads();
+  sum = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) sum += sums[w];
+
+  const int side = tid / kEach;
+  const int e = (slice * kEach + tid % kEach) * 4;
+  f32x4 o = {};
+#pragma unroll 4
+  for (int32_t s = side; s < parts; s += kSides) {
+    const float f = factor[s];
+    if (f < 0.0f) continue;
+    o += *reinterpret_cast<const f32x4*>(part_of(s) + e) * f;
+  }
+  *reinterpret_cast<f32x4*>(half + tid * 4) = o;
+  __syncthreads();
+  if (side) return;
+#pragma unroll
+  for (int s = 1; s < kSides; ++s) o += *reinterpret_cast<const f32x4*>(half + (s * kEach + tid) * 4);
+  const float scale = sum == 0.0f ? 0.0f : 1.0f / sum;
+  *reinterpret_cast<u32x2*>(p.out + (((int64_t)row * p.heads + head) * kLatent + e) * 2) =
+      u32x2{T::pack(o[0] * scale, o[1] * scale), T::pack(o[2] * scale, o[3] * scale)};
+  if (p.lse && e == 0) p.lse[(int64_t)row * p.heads + head] = (top + log2f(sum)) * kLn2;
+}
+
+// How a call is cut: heads packed into a workgroup for the shared tokens and for a
+// row's own, workgroups, and numbers that blocks and parts may have.
+struct Cut {
+  int32_t lanes, own_lanes, own_blocks, places;
+  int64_t shared_blocks, own;
+  size_t shared_parts, own_parts;  // lanes of all parts
+
+  Cut(int32_t rows, int32_t heads, int32_t groups, int64_t max_shared, int64_t max_own) {
+    const bool shares = max_shared > 0, owns = max_own > 0 || !shares;
+    const int64_t each = ((int64_t)rows + groups - 1) / groups * heads;  // lanes of a mean group
+    lanes = each <= 32 ? 32 : each <= 64 ? 64 : 128;
+    const int32_t most = heads <= 32 ? 32 : heads <= 64 ? 64 : 128;
+    own_lanes = heads < most ? heads : most;
+    own_blocks = (heads + most - 1) / most;
+    shared_blocks = shares ? (int64_t)rows * heads / lanes + groups : 0;
+    own = owns ? (int64_t)rows * own_blocks : 0;
+    // as many as run at once, or as the bounds have work for
+    const double units = (double)shared_blocks * (double)((max_shared + kTile - 1) / kTile + kBegin) +
+                         (double)own * (double)((max_own + kTile - 1) / kTile + kBegin);
+    const int32_t most_places = lanes == 128 ? 256 : kPlaces;
+    places = units / kLeast >= most_places ? most_places : 1 + (int32_t)(units / kLeast);
+    shared_parts = shares ? (size_t)(shared_blocks + places) * lanes : 0;
+    own_parts = owns ? (size_t)(own + places) * own_lanes : 0;
+  }
+  size_t bytes(int32_t latent) const {
+    return (shared_parts + own_parts) * (latent + 2) * sizeof(float) +
+           ((size_t)(shared_blocks + own) * 2 * sizeof(int32_t) + 15) / 16 * 16;
+  }
+};
+
 template <class T, class PS, class PO>
-int launch_parts(SharedParams p, void* stream) {
-  const int64_t slots = (int64_t)p.to.rows * p.to.heads / (PS::kWH * 16) + p.groups;
-  p.own_blocks = (p.to.heads + PO::kWH * 16 - 1) / (PO::kWH * 16);
-  const int64_t shared = slots * p.shared_splits;
-  const int64_t own = (int64_t)p.to.rows * p.own_blocks * p.own_splits;
-  if (shared + own > INT32_MAX) return DSATOPK_ERR_INVALID_ARG;
-  p.slots = (uint32_t)slots;
-  p.shared_jobs = (uint32_t)shared;
-  return launch(shared_kernel<T, PS, PO>, dim3((unsigned)(shared + own)), dim3(PS::kBlock), p, stream);
+int launch_parts(const SharedParams& p, const Cut& c, void* stream) {
+  return launch(shared_kernel<T, PS, PO>, dim3((unsigned)c.places), dim3(PS::kBlock), p, stream);
 }
 
 template <class T, int kLatent>
-int launch_shared(const SharedParams& p, int32_t lanes, void* stream) {
-  const int hb = head_block(p.to.heads);
-  const int st =
-      lanes == 32 ? launch_parts<T, Plan<2, 2, 32, kLatent>, Plan<2, 2, 32, kLatent>>(p, stream)
-      : lanes == 64 ? hb == 32 ? launch_parts<T, Plan<4, 1, 32, kLatent>, Plan<2, 2, 32, kLatent>>(p, stream)
-                               : launch_parts<T, Plan<4, 1, 32, kLatent>, Plan<4, 1, 32, kLatent>>(p, stream)
-      : hb == 32 ? launch_parts<T, Plan<8, 1, 64, kLatent>, Plan<2, 4, 64, kLatent>>(p, stream)
-      : hb == 64 ? launch_parts<T, Plan<8, 1, 64, kLatent>, Plan<4, 2, 64, kLatent>>(p, stream)
-                 : launch_parts<T, Plan<8, 1, 64, kLatent>, Plan<8, 1, 64, kLatent>>(p, stream);
-  if (st != DSATOPK_OK || p.to.splits == 1) return st;
-  return launch_join<T, kLatent>(p.to, stream);
+int launch_cut(const SharedParams& p, const Cut& c, void* stream) {
+  using Two = Plan<2, 2, 32, kLatent>;
+  using Four = Plan<4, 1, 32, kLatent>;
+  if (c.lanes == 32) return launch_parts<T, Two, Two>(p, c, stream);
+  if (c.lanes == 64)
+    return p.heads <= 32 ? launch_parts<T, Four, Two>(p, c, stream) : launch_parts<T, Four, Four>(p, c, stream);
+  if constexpr (kLatent == Wide::kLatent)
+    return launch_parts<T, Wide, Wide>(p, c, stream);
+  else
+    return p.heads <= 32   ? launch_parts<T, Plan<8, 1, 64, kLatent>, Plan<2, 4, 64, kLatent>>(p, c, stream)
+           : p.heads <= 64 ? launch_parts<T, Plan<8, 1, 64, kLatent>, Plan<4, 2, 64, kLatent>>(p, c, stream)
+                           : launch_parts<T, Plan<8, 1, 64, kLatent>, Plan<8, 1, 64, kLatent>>(p, c, stream);
+}
+
+template <class T, int kLatent>
+int launch_shared(SharedParams p, const Cut& c, void* workspace, void* stream) {
+  p.lanes = c.lanes;
+  p.own_lanes = c.own_lanes;
+  p.own_blocks = c.own_blocks;
+  p.shared_part = static_cast<float*>(workspace);
+  p.own_part = p.shared_part + c.shared_parts * kLatent;
+  p.shared_state = p.own_part + c.own_parts * kLatent;
+  p.own_state = p.shared_state + c.shared_parts * 2;
+  p.shared_numbers = reinterpret_cast<int32_t*>(p.own_state + c.own_parts * 2);
+  p.own_numbers = p.shared_numbers + c.shared_blocks * 2;
+  const int st = launch_cut<T, kLatent>(p, c, stream);
+  if (st != DSATOPK_OK) return st;
+  const int64_t heads = (int64_t)p.rows * p.heads;
+  return heads >= 512 ? launch(shared_join_kernel<T, kLatent, kLatent / 4>, dim3((unsigned)heads), dim3(kJoinBlock),
+                               p, stream)
+                      : launch(shared_join_kernel<T, kLatent, 32>, dim3((unsigned)(heads * (kLatent / 128))),
+                               dim3(kJoinBlock), p, stream);
 }
 
 }  // namespace
@@ -267,8 +626,7 @@ size_t dsatopk_shared_bytes(int32_t num_rows, int32_t num_heads, int32_t latent_
   if (num_rows < 1 || num_heads < 1 || latent_dim < 1 || num_groups < 1 || max_shared_len < 0 ||
       max_own_len < 0)
     return 0;
-  const Cut c = cut_of(num_rows, num_heads, num_groups, max_shared_len, max_own_len);
-  return part_floats(num_rows, num_heads, latent_dim, c.shared_splits + c.own_splits) * sizeof(float);
+  return Cut(num_rows, num_heads, num_groups, max_shared_len, max_own_len).bytes(latent_dim);
 }
 
 int dsatopk_attend_shared(const void* q, int64_t q_row_stride, int64_t q_head_stride,
@@ -297,18 +655,15 @@ int dsatopk_attend_shared(const void* q, int64_t q_row_stride, int64_t q_head_st
   if (!aligned16(q) || !aligned16(cache) || (reinterpret_cast<uintptr_t>(out) & 7u) ||
       !aligned4(lse) || q_row_stride % 8 || q_head_stride % 8 || page_stride % 8 || token_stride % 8)
     return DSATOPK_ERR_ALIGNMENT;
-  const Cut c = cut_of(num_rows, num_heads, num_groups, max_shared_len, max_own_len);
-  p.shared_splits = c.shared_splits;
-  p.own_splits = c.own_splits;
-  p.to.splits = c.shared_splits + c.own_splits;
-  if (p.to.splits > 1) {
-    if (!workspace ||
-        workspace_bytes < part_floats(num_rows, num_heads, latent_dim, p.to.splits) * sizeof(float))
-      return DSATOPK_ERR_WORKSPACE_TOO_SMALL;
-    if (!aligned16(workspace)) return DSATOPK_ERR_ALIGNMENT;
-    p.to.part = static_cast<float*>(workspace);
-    p.to.state = p.to.part + (size_t)num_rows * p.to.splits * num_heads * latent_dim;
-  }
+  p.shares = max_shared_len > 0;
+  p.owns = max_own_len > 0 || !p.shares;
+  const Cut c(num_rows, num_heads, num_groups, max_shared_len, max_own_len);
+  // parts are numbered, and heads counted, in 32 bits
+  if ((int64_t)num_rows * num_heads * (latent_dim / 128) > INT32_MAX || c.shared_blocks + kPlaces > INT32_MAX ||
+      c.own + kPlaces > INT32_MAX || (int64_t)num_groups + num_rows > INT32_MAX)
+    return DSATOPK_ERR_INVALID_ARG;
+  if (!workspace || workspace_bytes < c.bytes(latent_dim)) return DSATOPK_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned16(workspace)) return DSATOPK_ERR_ALIGNMENT;
   p.q = static_cast<const char*>(q);
   p.q_row = q_row_stride * 2;
   p.q_head = q_head_stride * 2;
@@ -326,15 +681,15 @@ int dsatopk_attend_shared(const void* q, int64_t q_row_stride, int64_t q_head_st
   p.shared_lens = shared_lens;
   p.groups = num_groups;
   p.scale2 = scale * kLog2e;
-  p.to.rows = num_rows;
-  p.to.heads = num_heads;
-  p.to.out = static_cast<char*>(out);
-  p.to.lse = lse;
+  p.rows = num_rows;
+  p.heads = num_heads;
+  p.out = static_cast<char*>(out);
+  p.lse = lse;
   if (type == DSATOPK_BF16)
-    return latent_dim == 256 ? launch_shared<Bf16, 256>(p, c.lanes, stream)
-                             : launch_shared<Bf16, 512>(p, c.lanes, stream);
-  return latent_dim == 256 ? launch_shared<Fp16, 256>(p, c.lanes, stream)
-                           : launch_shared<Fp16, 512>(p, c.lanes, stream);
+    return latent_dim == 256 ? launch_shared<Bf16, 256>(p, c, workspace, stream)
+                             : launch_shared<Bf16, 512>(p, c, workspace, stream);
+  return latent_dim == 256 ? launch_shared<Fp16, 256>(p, c, workspace, stream)
+                           : launch_shared<Fp16, 512>(p, c, workspace, stream);
 }
 
 }  // extern "C"

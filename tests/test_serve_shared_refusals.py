@@ -36,7 +36,7 @@ SHARED = dict(q=A16, q_row=9216, q_head=576, cache=A16, pages=10, page=36864, to
     (dict(q=None), 1), (dict(cache=None), 1), (dict(out=None), 1), (dict(q_head=-576), 1), (dict(lens=None), 1),
     (dict(table=None), 1), (dict(width=0), 1), (dict(stride=39), 1), (dict(starts=None), 1), (dict(shared=None), 1),
     (dict(groups=0), 1), (dict(groups=-1), 1), (dict(max_shared=-1), 1), (dict(max_own=-1), 1),
-    (dict(max_shared=1 << 31), 1), (dict(max_own=(1 << 31) - 64), 1), (dict(q=A8), 2), (dict(cache=A4), 2),
+    (dict(max_shared=1 << 31), 1), (dict(max_own=(1 << 31) - 64), 1), (dict(rows=1 << 30), 1), (dict(groups=2 ** 31 - 1), 1), (dict(q=A8), 2), (dict(cache=A4), 2),
     (dict(out=A4), 2), (dict(lse=0x10002), 2), (dict(q_row=9220), 2), (dict(token=580), 2), (dict(page=36868), 2),
     (dict(), 6), (dict(work=A16, bytes=100), 6), (dict(work=A4, bytes=1 << 40), 2),
 ])
@@ -53,11 +53,11 @@ def test_shared_bytes(lib):
     assert dt.shared_bytes(0, 16, 512, 1, 1000, 10) == 0
     assert dt.shared_bytes(4, 16, 512, 0, 1000, 10) == 0
     assert dt.shared_bytes(4, 16, 512, 1, -1, 10) == 0
-    few = dt.shared_bytes(4, 16, 512, 1, 100000, 10)
-    assert few >= 2 * 4 * 16 * 514 * 4 and few % (4 * 16 * 514 * 4) == 0
-    assert dt.shared_bytes(4, 16, 512, 1, 0, 64) == 0  # one part: nothing to join
-    assert dt.shared_bytes(4, 16, 512, 1, 64, 0) == 0
-    assert dt.shared_bytes(4, 16, 512, 1, 0, 0) == 0
+    few, many = dt.shared_bytes(4, 16, 512, 1, 100000, 10), dt.shared_bytes(400, 16, 512, 1, 100000, 10)
+    assert 0 < few < many and few % 16 == 0
+    # a part is the heads of a workgroup; no more of them than the bounds have work for
+    assert 0 < dt.shared_bytes(4, 16, 512, 1, 64, 0) < dt.shared_bytes(4, 16, 512, 1, 6400, 0)
+    assert dt.shared_bytes(4, 16, 512, 1, 0, 0) > 0
     assert dt.shared_bytes(2 ** 31 - 1, 1024, 512, 2 ** 31 - 1, 2 ** 31 - 65, 2 ** 31 - 65) > 0
 
 
