@@ -35,7 +35,7 @@ struct Joined {
 // Waves of a workgroup: WH groups of 16 heads by WT groups of tokens.
 template <int kWH_, int kWT_, int kTile_, int kLatent_>
 struct Plan {
-  static constexpr int kWH = kWH_, kWT = kWT_, kWaves = kWH * kWT, kLanes = kWH * 16;
+  static constexpr int kWH = kWH_, kWT = kWT_, kWaves = kWH * kWT, kCols = 16, kLanes = kWH * kCols;
   static constexpr int kTile = kTile_;          // tokens
   static constexpr int kBlock = kWaves * 64;
   static constexpr int kLatent = kLatent_;

@@ -49,8 +49,9 @@ struct SharedParams {
   float scale2;
   char* out;
   float* lse;
-  // Parts: vectors [number, lanes, latent], references and sums [number, lanes, 2];
-  // first and last part of each block [blocks, 2].
+  // Parts: vectors [number, lanes / cols, latent / 4, cols, 4], as the lanes of a product hold them; references
+  // and sums [number, lanes, 2]; first and last part of each block [blocks, 2].
+  int32_t cols;
   float* shared_part;
   float* shared_state;
   int32_t* shared_numbers;
@@ -69,7 +70,7 @@ __device__ __forceinline__ Args& args() {
 }
 
 constexpr int kTile = 64;   // tokens of a unit of work
-constexpr int kBegin = 2;   // a block costs its tiles and this many (first loads, last sums, the join)
+constexpr int kBegin = 6;   // a block costs its tiles and this many (first loads, last sums, the join)
 constexpr int kLeast = 4;   // units that a workgroup is started for
 constexpr int kStarts = 1024;  // groups whose starts are kept in LDS
 
@@ -135,29 +136,34 @@ __device__ __forceinline__ Entry entry_of(Args& p, const Starts& starts, int32_t
   return {p.owns && own > 0 ? (own + kTile - 1) / kTile : 0, p.own_blocks};
 }
 
+// Where a lane's part goes: its vector (4 elements of each `step` floats), and its reference and sum.
+struct Slot {
+  float *part, *state;
+  int32_t step;
+};
+
 // This lane's head of a part: into the result if the part is all that there is, else to its place.
 template <class T, class P>
 __device__ __forceinline__ void put_part(Args& p, const State<P>& st, float top, float sum,
-                                         bool whole, int64_t row, int32_t head, float* part, float* state,
-                                         int64_t place, int lane) {
+                                         bool whole, int64_t row, int32_t head, const Slot& to, int lane) {
   const int group = lane >> 4;
   if (whole) {
-    Joined to{};
-    to.heads = p.heads;
-    to.splits = 1;
-    to.out = p.out;
-    to.lse = p.lse;
-    put<T, P>(st, top, sum, to, row, head, 0, lane);
+    Joined out{};
+    out.heads = p.heads;
+    out.splits = 1;
+    out.out = p.out;
+    out.lse = p.lse;
+    put<T, P>(st, top, sum, out, row, head, 0, lane);
     return;
   }
   if (group == 0) {
-    state[place * 2] = top;
-    state[place * 2 + 1] = sum;
+    to.state[0] = top;
+    to.state[1] = sum;
   }
   if (top == -INFINITY && sum == 0.0f) return;  // nothing seen: the join skips it
-  float* to = part + place * P::kLatent + 4 * group;
+  float* part = to.part + group * to.step;
 #pragma unroll
-  for (int b = 0; b < P::kBlocks; ++b) *reinterpret_cast<f32x4*>(to + b * 16) = st.o[b];
+  for (int b = 0; b < P::kBlocks; ++b) *reinterpret_cast<f32x4*>(part + b * 4 * to.step) = st.o[b];
 }
 
 // The same for 32 heads a wave, where register i of block b holds element 32 * b + 8 * (i / 4) + 4 *
@@ -165,13 +171,13 @@ __device__ __forceinline__ void put_part(Args& p, const State<P>& st, float top,
 // `some`: some have been put there before.
 template <class T>
 __device__ __forceinline__ void put_wide(Args& p, WideState& st, bool more, bool some, bool whole, int64_t row,
-                                         int32_t head, float* part, float* state, int64_t place, int lane) {
+                                         int32_t head, const Slot& to, int lane) {
   const int half = lane >> 5;
   float top = st.top, sum = st.sum, by = 1.0f, before = 0.0f;
-  float* to = part + place * Wide::kLatent + 4 * half;
+  float* part = to.part + half * to.step;
   bool kept = false;
   if (some) {
-    const float x = state[place * 2], n = state[place * 2 + 1];
+    const float x = to.state[0], n = to.state[1];
     kept = !(x == -INFINITY && n == 0.0f);
     const float ref = fmaxf(x, top);
     before = kept ? exp2_fast(x - (ref == -INFINITY ? 0.0f : ref)) : 0.0f;
@@ -187,8 +193,8 @@ __device__ __forceinline__ void put_wide(Args& p, WideState& st, bool more, bool
   } else {
     // (both halves have read the state before one writes it)
     if (half == 0) {
-      state[place * 2] = top;
-      state[place * 2 + 1] = sum;
+      to.state[0] = top;
+      to.state[1] = sum;
     }
     if (top == -INFINITY && sum == 0.0f) return;  // nothing seen: the join skips it
   }
@@ -197,12 +203,13 @@ __device__ __forceinline__ void put_wide(Args& p, WideState& st, bool more, bool
 #pragma unroll
     for (int i = 0; i < 16; i += 4) {
       f32x4 v = {st.o[b][i], st.o[b][i + 1], st.o[b][i + 2], st.o[b][i + 3]};
+      float* at = part + (8 * b + i / 2) * to.step;
       v *= by;
-      if (kept) v += *reinterpret_cast<const f32x4*>(to + b * 32 + 2 * i) * before;
+      if (kept) v += *reinterpret_cast<const f32x4*>(at) * before;
       if (result)
         *reinterpret_cast<u32x2*>(out + (b * 32 + 2 * i) * 2) = u32x2{T::pack(v[0], v[1]), T::pack(v[2], v[3])};
       else
-        *reinterpret_cast<f32x4*>(to + b * 32 + 2 * i) = v;
+        *reinterpret_cast<f32x4*>(at) = v;
     }
 }
 
@@ -255,10 +262,12 @@ struct Block {
   __device__ __forceinline__ bool alone(int32_t i) const {
     return own ? shared == 0 : !p.owns || length_of(p, row_of(i)) <= shared;
   }
-  __device__ __forceinline__ float* part() const { return own ? p.own_part : p.shared_part; }
-  __device__ __forceinline__ float* state() const { return own ? p.own_state : p.shared_state; }
-  __device__ __forceinline__ int64_t place(const Job& job, int32_t lanes, int32_t i) const {
-    return job.number * (own ? p.own_lanes : lanes) + i;
+  template <class P>
+  __device__ __forceinline__ Slot slot(const Job& job, int32_t i) const {
+    const int64_t at = job.number * (own ? p.own_lanes : P::kLanes);
+    return {(own ? p.own_part : p.shared_part) + at * P::kLatent +
+                ((int64_t)(i / P::kCols) * (P::kLatent / 4) * P::kCols + i % P::kCols) * 4,
+            (own ? p.own_state : p.shared_state) + (at + i) * 2, P::kCols * 4};
   }
 };
 
@@ -292,10 +301,11 @@ __device__ __forceinline__ void attend_job(const Job& job, char* tiles, uint32_t
       const int32_t now = here(lane), i = wave * 32 + now % 32;
       if (i < block.count)
         put_wide<T>(block.p, st, more, some, job.whole && block.alone(i), block.row_of(i), block.head_of(i),
-                    block.part(), block.state(), block.place(job, kLanes, i), now);
+                    block.slot<P>(job, i), now);
     };
     Args& p = args();
-    attend_wide<T>(tiles, masks, cache_of(p), pages_of(p, uniform(job.row0)), base, len, first, last,
+    const bool idle = wave * 32 >= Block(p, job, kLanes).count;
+    attend_wide<T>(tiles, masks, cache_of(p), pages_of(p, uniform(job.row0)), base, len, first, last, idle,
                    [&](int now) { return queries(wave * 32 + now % 32); },
                    [&](int now) { return mine(wave * 32 + now % 32); }, done, wave, lane, p.scale2);
   } else {
@@ -317,7 +327,7 @@ __device__ __forceinline__ void attend_job(const Job& job, char* tiles, uint32_t
     const Block block(args(), job, kLanes);
     if (wave / P::kWH == 0 && i < block.count)
       put_part<T, P>(block.p, st, top, sum, job.whole && block.alone(i), block.row_of(i), block.head_of(i),
-                     block.part(), block.state(), block.place(job, kLanes, i), now);
+                     block.slot<P>(job, i), now);
   }
 }
 
@@ -458,29 +468,37 @@ __global__ __launch_bounds__(PS::kBlock, (std::is_same_v<PS, Wide> ? 1 : 2)) voi
   }
 }
 
-// Joins the parts of 4 * kEach elements of one row's head: the shared ones, then
-// the row's own. First the common maximum and the parts' factors; then kEach
-// threads for each of kJoinBlock / kEach sets of parts, 4 elements each. What
-// is a single part has been written as the result.
+// Joins the parts of 32 heads, 8 elements of each: a lane's are 4 elements of its head, and wave w of kSides takes
+// every kSides-th part from w on, four at a time, by the largest reference so far; then wave 0 joins
+// the waves' sums. Parts are as the products' lanes left them, so that a load of a wave is of
+// whole lines. What is a single part has been written as the result.
 constexpr int kPlaces = 512;  // workgroups at most, and so parts of a block but one
+constexpr int kXcds = 8;
 
-template <class T, int kLatent, int kEach>
-__global__ __launch_bounds__(kJoinBlock) void shared_join_kernel(SharedParams) {
+template <class T, int kLatent, int kSides>
+__global__ __launch_bounds__(kSides * 64) void shared_join_kernel(SharedParams) {
   Args& p = args();
-  constexpr int kSides = kJoinBlock / kEach, kSlices = kLatent / (4 * kEach), kWaves = kJoinBlock / 64;
-  __shared__ float tops[kWaves], sums[kWaves];
-  __shared__ float factor[2 * (kPlaces + 1)];
-  __shared__ __attribute__((aligned(16))) float half[kJoinBlock * 4];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const uint32_t which = blockIdx.x / kSlices, slice = blockIdx.x % kSlices;
-  const int32_t row = which / p.heads, head = which % p.heads;
-  const int32_t g = last_below(p.groups, row, lane, [&](int32_t i) { return (int64_t)start_of(p, i); });
+  constexpr int kPairs = kLatent / 8;
+  __shared__ __attribute__((aligned(16))) char space[kSides * 64 * 24];
+  f32x4* vectors = reinterpret_cast<f32x4*>(space);
+  float* tops = reinterpret_cast<float*>(space + kSides * 64 * 16);
+  float* sums = tops + kSides * 64;
+  const int tid = threadIdx.x, lane = tid & 63, side = tid >> 6;
+  // workgroups of the same heads on the same die, whose cache puts their results together
+  const uint32_t set = blockIdx.x / kXcds;
+  const int64_t heads = (int64_t)p.rows * p.heads, x0 = ((int64_t)(set / kPairs) * kXcds + blockIdx.x % kXcds) * 32;
+  const int32_t e4 = (set % kPairs) * 2 + (lane >> 5);
+  if (x0 >= heads) return;
+  const int64_t x = min(x0 + (lane & 31), heads - 1);
+  const int32_t row = (int32_t)(x / p.heads), head = (int32_t)(x - (int64_t)row * p.heads);
+  int32_t g = last_below(p.groups, (int32_t)(x0 / p.heads), lane, [&](int32_t i) { return (int64_t)start_of(p, i); });
+  while (g + 1 < p.groups && start_of(p, g + 1) <= row) ++g;
   const int32_t shared = shared_of(p, g);
   int32_t n = 0, m = 0;  // shared parts, own parts
   int64_t first = 0, own = 0;
   if (shared > 0) {
     const int32_t start = start_of(p, g);
-    const int64_t i = (int64_t)(row - start) * p.heads + head;
+    const int64_t i = x - (int64_t)start * p.heads;
     const int32_t* numbers = p.shared_numbers + (first_block(p, start, g) + i / p.lanes) * 2;
     n = numbers[1] - numbers[0] + 1;
     first = (int64_t)numbers[0] * p.lanes + i % p.lanes;
@@ -490,73 +508,91 @@ __global__ __launch_bounds__(kJoinBlock) void shared_join_kernel(SharedParams) {
     m = numbers[1] - numbers[0] + 1;
     own = (int64_t)numbers[0] * p.own_lanes + head % p.own_lanes;
   }
-  const int32_t parts = n + m;
-  if (parts == 1) return;
-  auto state_of = [&](int32_t s) {
-    return s < n ? p.shared_state + (first + (int64_t)s * p.lanes) * 2
-                 : p.own_state + (own + (int64_t)(s - n) * p.own_lanes) * 2;
+  const int32_t parts = n + m, cols = p.cols;
+  // (lanes of a block are a multiple of cols)
+  auto vector = [&](const float* part, int64_t at) {
+    return part + (at / cols * cols * (kLatent / 4) + (int64_t)e4 * cols + at % cols) * 4;
   };
-  auto part_of = [&](int32_t s) {
-    return s < n ? p.shared_part + (first + (int64_t)s * p.lanes) * kLatent
-                 : p.own_part + (own + (int64_t)(s - n) * p.own_lanes) * kLatent;
-  };
-  float top = -INFINITY;
-  for (int32_t s = tid; s < parts; s += kJoinBlock) top = fmaxf(top, state_of(s)[0]);
-#pragma unroll
-  for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
-  if (lane == 0) tops[wave] = top;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) top = fmaxf(top, tops[w]);
-  float sum = 0.0f;
-  for (int32_t s = tid; s < parts; s += kJoinBlock) {
-    const float x = state_of(s)[0], y = state_of(s)[1];
-    const bool empty = x == -INFINITY && y == 0.0f;  // such a part has written no vector
-    const float by = empty ? 0.0f : exp2_fast(x - (top == -INFINITY ? 0.0f : top));
-    factor[s] = empty ? -1.0f : by;
-    sum += y * by;
-  }
-#pragma unroll
-  for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
-  if (lane == 0) sums[wave] = sum;
-  __syncthreads();
-  sum = 0.0f;
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) sum += sums[w];
+  const float* shared_part = vector(p.shared_part, first);
+  const float* own_part = vector(p.own_part, own);
+  const float *shared_state = p.shared_state + first * 2, *own_state = p.own_state + own * 2;
 
-  const int side = tid / kEach;
-  const int e = (slice * kEach + tid % kEach) * 4;
+  float top = -INFINITY, sum = 0.0f;
   f32x4 o = {};
-#pragma unroll 4
-  for (int32_t s = side; s < parts; s += kSides) {
-    const float f = factor[s];
-    if (f < 0.0f) continue;
-    o += *reinterpret_cast<const f32x4*>(part_of(s) + e) * f;
-  }
-  *reinterpret_cast<f32x4*>(half + tid * 4) = o;
-  __syncthreads();
-  if (side) return;
+  auto join = [&](float (&tops)[4], const float (&ns)[4], const f32x4 (&v)[4]) {
+    const float most = fmaxf(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])), top);
+    const float ref = most == -INFINITY ? 0.0f : most;
+    const float by = exp2_fast(top - ref);
+    o *= by;
+    sum *= by;
 #pragma unroll
-  for (int s = 1; s < kSides; ++s) o += *reinterpret_cast<const f32x4*>(half + (s * kEach + tid) * 4);
+    for (int k = 0; k < 4; ++k) {
+      if (tops[k] == -INFINITY && ns[k] == 0.0f) continue;  // such a part has no vector
+      const float f = exp2_fast(tops[k] - ref);
+      o += v[k] * f;
+      sum += ns[k] * f;
+    }
+    top = most;
+  };
+  for (int32_t s = side; s < parts; s += 4 * kSides) {
+    float xs[4], ns[4];
+    f32x4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int32_t i = s + k * kSides;
+      xs[k] = -INFINITY;
+      ns[k] = 0.0f;
+      v[k] = f32x4{};
+      if (i >= parts) continue;
+      const int64_t skip = i < n ? (int64_t)i * p.lanes : (int64_t)(i - n) * p.own_lanes;
+      const float* state = (i < n ? shared_state : own_state) + skip * 2;
+      xs[k] = state[0];
+      ns[k] = state[1];
+      v[k] = *reinterpret_cast<const f32x4*>((i < n ? shared_part : own_part) + skip * kLatent);
+    }
+    join(xs, ns, v);
+  }
+  if (side) {
+    vectors[tid] = o;
+    tops[tid] = top;
+    sums[tid] = sum;
+  }
+  __syncthreads();
+  if (side || parts == 1 || x0 + (lane & 31) >= heads) return;
+  for (int s = 1; s < kSides; s += 4) {
+    float xs[4], ns[4];
+    f32x4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const bool is = s + k < kSides;
+      xs[k] = is ? tops[(s + k) * 64 + lane] : -INFINITY;
+      ns[k] = is ? sums[(s + k) * 64 + lane] : 0.0f;
+      v[k] = is ? vectors[(s + k) * 64 + lane] : f32x4{};
+    }
+    join(xs, ns, v);
+  }
   const float scale = sum == 0.0f ? 0.0f : 1.0f / sum;
-  *reinterpret_cast<u32x2*>(p.out + (((int64_t)row * p.heads + head) * kLatent + e) * 2) =
+  *reinterpret_cast<u32x2*>(p.out + (x * kLatent + e4 * 4) * 2) =
       u32x2{T::pack(o[0] * scale, o[1] * scale), T::pack(o[2] * scale, o[3] * scale)};
-  if (p.lse && e == 0) p.lse[(int64_t)row * p.heads + head] = (top + log2f(sum)) * kLn2;
+  if (p.lse && e4 == 0) p.lse[x] = (top + log2f(sum)) * kLn2;
 }
 
 // How a call is cut: heads packed into a workgroup for the shared tokens and for a
 // row's own, workgroups, and numbers that blocks and parts may have.
 struct Cut {
-  int32_t lanes, own_lanes, own_blocks, places;
+  int32_t lanes, cols, own_lanes, own_blocks, places;
   int64_t shared_blocks, own;
   size_t shared_parts, own_parts;  // lanes of all parts
+  int32_t latent;
 
-  Cut(int32_t rows, int32_t heads, int32_t groups, int64_t max_shared, int64_t max_own) {
+  Cut(int32_t rows, int32_t heads, int32_t latent, int32_t groups, int64_t max_shared, int64_t max_own)
+      : latent(latent) {
     const bool shares = max_shared > 0, owns = max_own > 0 || !shares;
     const int64_t each = ((int64_t)rows + groups - 1) / groups * heads;  // lanes of a mean group
     lanes = each <= 32 ? 32 : each <= 64 ? 64 : 128;
     const int32_t most = heads <= 32 ? 32 : heads <= 64 ? 64 : 128;
-    own_lanes = heads < most ? heads : most;
+    cols = lanes == 128 && latent == Wide::kLatent ? Wide::kCols : 16;
+    own_lanes = heads < most ? (heads + cols - 1) / cols * cols : most;
     own_blocks = (heads + most - 1) / most;
     shared_blocks = shares ? (int64_t)rows * heads / lanes + groups : 0;
     own = owns ? (int64_t)rows * own_blocks : 0;
@@ -568,7 +604,7 @@ struct Cut {
     shared_parts = shares ? (size_t)(shared_blocks + places) * lanes : 0;
     own_parts = owns ? (size_t)(own + places) * own_lanes : 0;
   }
-  size_t bytes(int32_t latent) const {
+  size_t bytes() const {
     return (shared_parts + own_parts) * (latent + 2) * sizeof(float) +
            ((size_t)(shared_blocks + own) * 2 * sizeof(int32_t) + 15) / 16 * 16;
   }
@@ -599,6 +635,7 @@ int launch_shared(SharedParams p, const Cut& c, void* workspace, void* stream) {
   p.lanes = c.lanes;
   p.own_lanes = c.own_lanes;
   p.own_blocks = c.own_blocks;
+  p.cols = c.cols;
   p.shared_part = static_cast<float*>(workspace);
   p.own_part = p.shared_part + c.shared_parts * kLatent;
   p.shared_state = p.own_part + c.own_parts * kLatent;
@@ -607,11 +644,11 @@ int launch_shared(SharedParams p, const Cut& c, void* workspace, void* stream) {
   p.own_numbers = p.shared_numbers + c.shared_blocks * 2;
   const int st = launch_cut<T, kLatent>(p, c, stream);
   if (st != DSATOPK_OK) return st;
-  const int64_t heads = (int64_t)p.rows * p.heads;
-  return heads >= 512 ? launch(shared_join_kernel<T, kLatent, kLatent / 4>, dim3((unsigned)heads), dim3(kJoinBlock),
-                               p, stream)
-                      : launch(shared_join_kernel<T, kLatent, 32>, dim3((unsigned)(heads * (kLatent / 128))),
-                               dim3(kJoinBlock), p, stream);
+  const int64_t tiles = ((int64_t)p.rows * p.heads + 31) / 32;
+  const dim3 grid((unsigned)((tiles + kXcds - 1) / kXcds * kXcds * (kLatent / 8)));
+  // few heads, and so few waves, with up to a part from every workgroup
+  return tiles >= 16 ? launch(shared_join_kernel<T, kLatent, 4>, grid, dim3(256), p, stream)
+                     : launch(shared_join_kernel<T, kLatent, 16>, grid, dim3(1024), p, stream);
 }
 
 }  // namespace
@@ -626,7 +663,7 @@ size_t dsatopk_shared_bytes(int32_t num_rows, int32_t num_heads, int32_t latent_
   if (num_rows < 1 || num_heads < 1 || latent_dim < 1 || num_groups < 1 || max_shared_len < 0 ||
       max_own_len < 0)
     return 0;
-  return Cut(num_rows, num_heads, num_groups, max_shared_len, max_own_len).bytes(latent_dim);
+  return Cut(num_rows, num_heads, latent_dim, num_groups, max_shared_len, max_own_len).bytes();
 }
 
 int dsatopk_attend_shared(const void* q, int64_t q_row_stride, int64_t q_head_stride,
@@ -657,12 +694,12 @@ int dsatopk_attend_shared(const void* q, int64_t q_row_stride, int64_t q_head_st
     return DSATOPK_ERR_ALIGNMENT;
   p.shares = max_shared_len > 0;
   p.owns = max_own_len > 0 || !p.shares;
-  const Cut c(num_rows, num_heads, num_groups, max_shared_len, max_own_len);
+  const Cut c(num_rows, num_heads, latent_dim, num_groups, max_shared_len, max_own_len);
   // parts are numbered, and heads counted, in 32 bits
   if ((int64_t)num_rows * num_heads * (latent_dim / 128) > INT32_MAX || c.shared_blocks + kPlaces > INT32_MAX ||
       c.own + kPlaces > INT32_MAX || (int64_t)num_groups + num_rows > INT32_MAX)
     return DSATOPK_ERR_INVALID_ARG;
-  if (!workspace || workspace_bytes < c.bytes(latent_dim)) return DSATOPK_ERR_WORKSPACE_TOO_SMALL;
+  if (!workspace || workspace_bytes < c.bytes()) return DSATOPK_ERR_WORKSPACE_TOO_SMALL;
   if (!aligned16(workspace)) return DSATOPK_ERR_ALIGNMENT;
   p.q = static_cast<const char*>(q);
   p.q_row = q_row_stride * 2;

@@ -17,7 +17,7 @@ namespace {
 
 struct Wide {
   static constexpr int kLatent = 512, kRow = kLatent * 2;
-  static constexpr int kWaves = 4, kBlock = kWaves * 64, kLanes = kWaves * 32;
+  static constexpr int kWaves = 4, kBlock = kWaves * 64, kCols = 32, kLanes = kWaves * kCols;
   static constexpr int kTile = 32, kRing = 4;  // tokens of a tile, tiles in LDS
   static constexpr int kRopeAt = kTile * kRow;
   static constexpr int kBuffer = kRopeAt + kTile * kRopeBytes;
@@ -233,12 +233,13 @@ __device__ __forceinline__ void wide_step(f32x16 (&o)[Wide::kBlocks], Weights& w
 // was given before (`some`): weights are taken by a reference that holds until they
 // outgrow it, which is seldom; the sums are then put down, and begun anew by
 // another one. (If they were brought to it in their registers, the compiler would move
-// them out of the accumulation registers and back at every tile.)
+// them out of the accumulation registers and back at every tile.) An `idle` wave, which
+// has no heads, only copies.
 template <class T, class Queries, class Mine, class Done>
 __device__ __forceinline__ void attend_wide(char* tiles, uint32_t (*masks)[Wide::kWaves], const Cache& c,
                                             const int32_t* list, int32_t base, int32_t len, int32_t first,
-                                            int32_t last, Queries queries, Mine mine_of, Done done, int wave,
-                                            int lane, float scale2) {
+                                            int32_t last, bool idle, Queries queries, Mine mine_of, Done done,
+                                            int wave, int lane, float scale2) {
   constexpr int kTile = Wide::kTile, kRing = Wide::kRing, kAheadTiles = kRing - 1, kBuffer = Wide::kBuffer;
   const WideTokens tokens{c, list, base, len, last};
   int32_t pages[kAheadTiles + 1];
@@ -261,6 +262,21 @@ __device__ __forceinline__ void attend_wide(char* tiles, uint32_t (*masks)[Wide:
   // (for all of them: the compiler lets reads in the loop go ahead of copies only if none are under way when it begins)
   copies_barrier();
 
+  if (idle) {
+#pragma unroll 1
+    for (int32_t t = first; t < last; ++t) {
+      const int n = t - first + kAheadTiles, now = here(lane);
+      wait_copies_but<Wide::kCopies>();
+      __syncthreads();
+      const WideCopy copy(tokens, page, first + n, wave, now);
+#pragma unroll
+      for (int k = 0; k < Wide::kCopies; ++k) copy.piece(tiles + n % kRing * kBuffer, k, wave, now);
+      if (now == 0) masks[n % kRing][wave] = copy.there;
+      page = tokens.page_of(first + n + 1, wave, now);
+    }
+    wait_copies();
+    return;
+  }
   int32_t t = first;
 #pragma unroll 1
   for (bool some = false;; some = true) {
