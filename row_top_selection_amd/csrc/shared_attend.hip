@@ -646,9 +646,11 @@ int launch_shared(SharedParams p, const Cut& c, void* workspace, void* stream) {
   if (st != DSATOPK_OK) return st;
   const int64_t tiles = ((int64_t)p.rows * p.heads + 31) / 32;
   const dim3 grid((unsigned)((tiles + kXcds - 1) / kXcds * kXcds * (kLatent / 8)));
-  // few heads, and so few waves, with up to a part from every workgroup
-  return tiles >= 16 ? launch(shared_join_kernel<T, kLatent, 4>, grid, dim3(256), p, stream)
-                     : launch(shared_join_kernel<T, kLatent, 16>, grid, dim3(1024), p, stream);
+  // A wave by itself for many heads (2112 heads of 16 parts: 12.6 us, 20.4 by four); few are too few waves to have
+  // the memory busy (1024 heads of 33 parts: 11.7 us by four, 14.5 by eight), and may have a part of every workgroup.
+  return tiles >= 64   ? launch(shared_join_kernel<T, kLatent, 1>, grid, dim3(64), p, stream)
+         : tiles >= 16 ? launch(shared_join_kernel<T, kLatent, 4>, grid, dim3(256), p, stream)
+                       : launch(shared_join_kernel<T, kLatent, 16>, grid, dim3(1024), p, stream);
 }
 
 }  // namespace
