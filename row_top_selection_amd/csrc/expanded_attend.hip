@@ -24,10 +24,9 @@
 // Few rows of many keys are split over workgroups by keys; a second kernel
 // joins the parts.
 //
-// With shared keys a workgroup takes the next 32 queries a wave of the batch,
-// whichever requests they are of, and goes over segments of keys: those that
-// the requests share, once for all of them that stand together, then each
-// request's own. A lane counts the keys of a segment that its query sees; waves
+// With shared keys a workgroup takes the next 32 queries a wave of those that
+// stand together and share them, whichever requests they are of, and goes over
+// segments of keys: the shared ones, once for all, then each request's own. A lane counts the keys of a segment that its query sees; waves
 // none of whose queries are in a segment only copy. Prompts of 16 tokens fill
 // tiles that way, which would be nearly empty if every request had its own.
 //
@@ -410,48 +409,114 @@ struct Segment {
   }
 };
 
-// The segments of the queries q0 .. q1 - 1, a tile of keys at a time. The same in
-// all lanes.
+// A workgroup's queries, which share their first keys: tile `index` of the runs of
+// requests with the same shared keys, each cut into tiles from its own first
+// query on. (In tiles of the batch, one that two runs meet in goes over both runs' keys,
+// twice what the others take: 2 x 4 prompts of up to 777 tokens behind 2000, 16
+// heads, took 200 us.) Threads take chunks of the requests: the last
+// beginning of a run before a chunk, and the tiles that end before it, from those of the others.
+struct Run {
+  int32_t q0, q1, first;  // queries; the run's first request
+};
+template <class S>
+__device__ __forceinline__ Run run_of(const ExpandParams& p, int32_t index, char* space, int tid, int wave, int lane) {
+  struct Room {
+    int32_t begins[S::kWaves], tiles[S::kWaves];
+    Run run;
+  };
+  Room& room = *reinterpret_cast<Room*>(space);
+  auto start = [&](int32_t r) { return min(max(p.q_starts[r], 0), p.num_q); };
+  auto begins = [&](int32_t r) {
+    return r == 0 || p.shared_starts[r] != p.shared_starts[r - 1] || p.shared_lens[r] != p.shared_lens[r - 1];
+  };
+  auto count = [&](int32_t from, int32_t to) { return (max(start(to) - start(from), 0) + S::kRows - 1) / S::kRows; };
+  const int32_t chunk = p.requests / S::kBlock + 1;
+  const int32_t r0 = min(tid * chunk, p.requests), r1 = min(r0 + chunk, p.requests);
+  int32_t begin = 0;
+  for (int32_t r = r0; r < r1; ++r)
+    if (begins(r)) begin = r;
+  // the largest of the threads up to this one, then of those before it
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int32_t o = __shfl_up(begin, d);
+    if (lane >= d) begin = max(begin, o);
+  }
+  if (lane == 63) room.begins[wave] = begin;
+  if (tid == 0) room.run = Run{0, 0, 0};
+  __syncthreads();
+  begin = __shfl_up(begin, 1);
+  if (lane == 0) begin = 0;
+#pragma unroll
+  for (int w = 0; w < S::kWaves; ++w)
+    if (w < wave) begin = max(begin, room.begins[w]);
+  // Runs that end in the chunk: where the next one begins, or behind the last request.
+  auto each = [&](auto&& what) {
+    int32_t from = begin;
+    for (int32_t r = r0; r < r1; ++r) {
+      if (r > 0 && begins(r)) {
+        what(from, r);
+        from = r;
+      }
+      if (r + 1 == p.requests) what(from, r + 1);
+    }
+  };
+  int32_t tiles = 0;
+  each([&](int32_t from, int32_t to) { tiles += count(from, to); });
+  int32_t below = tiles;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int32_t o = __shfl_up(below, d);
+    if (lane >= d) below += o;
+  }
+  if (lane == 63) room.tiles[wave] = below;
+  __syncthreads();
+  below -= tiles;
+#pragma unroll
+  for (int w = 0; w < S::kWaves; ++w)
+    if (w < wave) below += room.tiles[w];
+  if (index >= below && index < below + tiles)
+    each([&](int32_t from, int32_t to) {
+      const int32_t n = count(from, to);
+      if (index >= below && index < below + n) {
+        const int32_t q0 = start(from) + (index - below) * S::kRows;
+        room.run = Run{q0, min(q0 + S::kRows, start(to)), from};
+      }
+      below += n;
+    });
+  __syncthreads();
+  const Run run{__builtin_amdgcn_readfirstlane(room.run.q0), __builtin_amdgcn_readfirstlane(room.run.q1),
+                __builtin_amdgcn_readfirstlane(room.run.first)};
+  __syncthreads();  // before the space is taken for tiles
+  return run;
+}
+
+// The segments of the queries q0 .. q1 - 1, of one run, a tile of keys at a time: the
+// shared keys, then the requests' own. The same in all lanes.
 template <class S>
 struct Walk {
   const ExpandParams& p;
   int32_t q0, q1;
-  int32_t request;  // whose own keys come next, or with whom a new run begins
-  int32_t run;      // the first request behind those that share with it
+  int32_t request;  // whose own keys come next
   Segment at;
   int32_t j;  // first key of the tile, in the segment
   bool done;
 
   __device__ __forceinline__ Walk(const ExpandParams& params, int32_t first, int32_t last, int32_t r)
-      : p(params), q0(first), q1(last), request(r), run(r), at{}, j(0), done(false) {
-    next();
+      : p(params), q0(first), q1(last), request(r), at{}, j(0), done(false) {
+    at.base = min(max(p.shared_starts[r], 0), p.num_k);
+    at.len = min(max(p.shared_lens[r], 0), p.num_k - at.base);
+    at.from = q0;
+    at.to = q1;
+    at.diag = at.len;
+    if (at.len == 0) next();
   }
-  __device__ __forceinline__ int32_t starts(int32_t r) const { return max(p.q_starts[r], 0); }
-  __device__ __forceinline__ int32_t ends(int32_t r) const { return min(p.q_starts[r + 1], p.num_q); }
 
   __device__ __forceinline__ void next() {
     j = 0;
-    while (true) {
-      if (request >= run) {
-        while (request < p.requests && starts(request) >= ends(request)) ++request;
-        if (request >= p.requests || starts(request) >= q1) {
-          done = true;
-          return;
-        }
-        const int32_t first = p.shared_starts[request], len = p.shared_lens[request];
-        run = request + 1;
-        while (run < p.requests && starts(run) < q1 &&
-               (starts(run) >= ends(run) || (p.shared_starts[run] == first && p.shared_lens[run] == len)))
-          ++run;
-        at.base = min(max(first, 0), p.num_k);
-        at.len = min(max(len, 0), p.num_k - at.base);
-        at.from = max(starts(request), q0);
-        at.to = min(ends(run - 1), q1);
-        at.diag = at.len;
-        if (at.len > 0 && at.from < at.to) return;
-      }
+    while (request < p.requests) {
       const int32_t r = request++;
-      const int32_t first = starts(r), rows = ends(r) - first;
+      const int32_t first = max(p.q_starts[r], 0), rows = min(p.q_starts[r + 1], p.num_q) - first;
+      if (first >= q1) break;
       at.base = min(max(p.k_starts[r], 0), p.num_k);
       const int32_t keys = max(min(p.k_starts[r + 1], p.num_k) - at.base, 0);
       at.from = max(first, q0);
@@ -461,6 +526,7 @@ struct Walk {
       at.len = min(max(at.to - 1 + at.diag, 0), keys);
       if (at.len > 0) return;
     }
+    done = true;
   }
   __device__ __forceinline__ void advance() {
     j += S::kTile;
@@ -499,10 +565,11 @@ __global__ __launch_bounds__(S::kBlock, 2) void expand_shared_kernel(ExpandParam
   const int split = blockIdx.y;
   const int head = id / (8 * p.tiles) * 8 + id % 8;
   if (head >= p.heads) return;
-  const int32_t q0 = (p.tiles - 1 - (int32_t)(id / 8 % p.tiles)) * kRows, q1 = min(q0 + kRows, p.num_q);
-  const int32_t r = last_below(p.requests, q0, lane, [&](int32_t i) { return (int64_t)p.q_starts[i]; });
+  const Run run = run_of<S>(p, p.tiles - 1 - (int32_t)(id / 8 % p.tiles), tiles, tid, wave, lane);
+  const int32_t q0 = run.q0, q1 = run.q1;
+  if (q0 >= q1) return;
+  const int32_t r = max(run.first, last_below(p.requests, q0, lane, [&](int32_t i) { return (int64_t)p.q_starts[i]; }));
   const int32_t w0 = q0 + wave * 32, mine = w0 + col;
-  const bool real = mine < q1 && mine >= p.q_starts[0] && mine < p.q_starts[p.requests];
   const int64_t at = min(mine, q1 - 1);
 
   u32x4 q[kSteps];
@@ -582,7 +649,7 @@ __global__ __launch_bounds__(S::kBlock, 2) void expand_shared_kernel(ExpandParam
       }
     }
   }
-  if (real) put<T>(p, st, at, head, split, half);
+  if (mine < q1) put<T>(p, st, at, head, split, half);
 }
 
 // Joins the parts of the rows' heads: 32 threads for each, 4 elements a
@@ -673,14 +740,24 @@ int launch_expand(ExpandParams p, const Cut& c, void* stream) {
                 stream);
 }
 
-// The same for the shared form, whose queries stand together: as for one request.
+// The same for the shared form, whose queries stand together: as for one request, but eight
+// waves from 160 workgroups of them on (8 x 341 queries behind 2001 keys, 16 heads, 160 whole
+// ones: 104 us, by four waves 119; 128 and 192 above).
 Cut shared_cut_of(int32_t heads, int32_t queries, int32_t max_keys) {
-  return cut_of(1, heads, queries, max_keys, queries);
+  Cut c = cut_of(1, heads, queries, max_keys, queries);
+  c.wide = (int64_t)heads * (queries / 256) >= 160;
+  if (c.wide) c.splits = 1;
+  return c;
+}
+// Tiles that its runs of requests may have.
+int64_t shared_tiles(int32_t queries, int32_t requests, int rows) {
+  const int64_t n = (int64_t)queries / rows + requests;
+  return n < queries ? n : queries;
 }
 
 template <class T, class S>
 int launch_shared(ExpandParams p, const Cut& c, void* stream) {
-  p.tiles = (p.num_q + S::kRows - 1) / S::kRows;
+  p.tiles = (int32_t)shared_tiles(p.num_q, p.requests, S::kRows);
   p.splits = c.splits;
   const int st = launch(expand_shared_kernel<T, S>, dim3((unsigned)(c.pairs * p.tiles), (unsigned)c.splits),
                         dim3(S::kBlock), p, stream);
@@ -821,6 +898,7 @@ extern "C" int dsatopk_attend_expanded_shared(
   p.shared_starts = shared_starts;
   p.shared_lens = shared_lens;
   const Cut c = shared_cut_of(num_heads, num_queries, max_keys);
+  if (c.pairs * shared_tiles(num_queries, num_requests, 128) > INT32_MAX) return DSATOPK_ERR_INVALID_ARG;
   st = check_room(p, c, workspace, workspace_bytes);
   if (st != DSATOPK_OK) return st;
   const bool bf16 = type == DSATOPK_BF16;
