@@ -1,11 +1,13 @@
 """One layer of sparse latent attention, from prompts to tokens.
 
-A batch of prompts is read with the expanded form, which leaves their latent
-vectors and indexer keys in paged caches. Then tokens are decoded, each step
+A batch of prompts is read with the expanded form; their latent vectors and
+indexer keys are left in paged caches. Then tokens are decoded, each step
 captured once in a HIP graph and replayed:
 
     page_maps        pages and slots of the step's tokens, the top-k's row arguments
-    (cache writes)   the new tokens' latent vectors and indexer keys, by slot
+    append_latent    the new tokens' latent vectors, normalised and turned, into their
+                     slots, and the queries' rotary parts
+    append_index     the same for the indexer's keys and queries
     scores_paged     the indexer's scores of every cached token
     plan, paged      the top-k, as cache slots
     attend_selected  attention over the selected slots
@@ -47,25 +49,30 @@ class Layer:
         self.to_index_k = weight(hidden, INDEX_DIM)
         self.to_index_w = weight(hidden, INDEX_HEADS)
         self.scale = (NOPE + ROPE) ** -0.5
-        # one page more than there are to hand out: rows without a token write there
+        self.norm = 1 + 0.1 * torch.randn(LATENT, generator=g, device=device)
+        self.index_norm = 1 + 0.1 * torch.randn(INDEX_DIM, generator=g, device=device)
+        self.index_bias = 0.1 * torch.randn(INDEX_DIM, generator=g, device=device)
+        angles = torch.arange(pages * PAGE, device=device)[:, None] * 10000.0 ** (-torch.arange(32, device=device) / 32)
+        self.angles = torch.cat([angles.cos(), angles.sin()], dim=1)
         bf = dict(dtype=torch.bfloat16, device=device)
-        self.cache = torch.zeros(pages + 1, PAGE, LATENT + ROPE, **bf)
-        self.index_keys = torch.zeros(pages + 1, PAGE, INDEX_DIM, **bf)
-        self.nowhere = pages * PAGE
+        self.cache = torch.zeros(pages, PAGE, LATENT + ROPE, **bf)
+        self.index_keys = torch.zeros(pages, PAGE, INDEX_DIM, **bf)
 
-    def write(self, x, slots):
-        """The tokens' latent vectors and indexer keys go to their slots."""
+    def write(self, x, maps, q_rope, q_out, index_q=None):
+        """The tokens' latent vectors and indexer keys go to their slots, and the queries' rotary parts to q_out:
+        the vectors, and the indexer's queries."""
         latent = x @ self.to_latent
-        to = torch.where(slots < 0, self.nowhere, slots).long()
-        self.cache.view(-1, LATENT + ROPE).index_copy_(0, to, latent)
-        self.index_keys.view(-1, INDEX_DIM).index_copy_(0, to, x @ self.to_index_k)
-        return latent
+        dt.append_latent(latent, self.cache, maps.slots, maps.row_lens, self.angles, weight=self.norm, q_rope=q_rope,
+                         q_out=q_out, out=latent)
+        index = dt.append_index(x @ self.to_index_k, self.index_keys, maps.slots, maps.row_lens, self.angles,
+                                weight=self.index_norm, bias=self.index_bias, q=index_q)
+        return latent, index and index[0]
 
     def prompt(self, x, starts, longest, maps):
         """Causal attention of whole prompts, expanded: [tokens, heads, VALUE]."""
-        latent = self.write(x, maps.slots)
         tokens = x.shape[0]
         q = (x @ self.to_q).view(tokens, self.heads, NOPE + ROPE)
+        latent, _ = self.write(x, maps, q[..., NOPE:], q[..., NOPE:])
         up = torch.cat([self.up_k, self.up_v.transpose(1, 2)], dim=1)  # [heads, NOPE + VALUE, LATENT]
         kv = (latent[:, :LATENT] @ up.reshape(-1, LATENT).t().contiguous()).view(tokens, self.heads, NOPE + VALUE)
         out, _ = dt.attend_expanded(q, kv[..., :NOPE], kv[..., NOPE:], latent[:, LATENT:], starts,
@@ -76,23 +83,37 @@ class Layer:
         """One token for every request: [requests, heads, VALUE], and what was selected."""
         n = x.shape[0]
         maps = dt.page_maps(lens, table, PAGE, free, n)
-        self.write(x, maps.slots)
-        scores = dt.scores_paged((x @ self.to_index_q).view(n, INDEX_HEADS, INDEX_DIM),
-                                 (x @ self.to_index_w).float(), self.index_keys, maps.row_lens, table,
+        q = (x @ self.to_q).view(n, self.heads, NOPE + ROPE)
+        absorbed = torch.empty(n, self.heads, LATENT + ROPE, dtype=x.dtype, device=x.device)
+        _, index_q = self.write(x, maps, q[..., NOPE:], absorbed[..., LATENT:],
+                                (x @ self.to_index_q).view(n, INDEX_HEADS, INDEX_DIM))
+        scores = dt.scores_paged(index_q, (x @ self.to_index_w).float(), self.index_keys, maps.row_lens, table,
                                  table_rows=maps.table_rows, out=buffers["scores"])
         plan = dt.plan(maps.row_lens, k)
         slots = dt.paged(scores, maps.row_lens, table, PAGE, k, plan=plan, table_rows=maps.table_rows)
-        q = (x @ self.to_q).view(n, self.heads, NOPE + ROPE)
         # the keys' projection is absorbed into the queries, the values' into the output
-        q_latent = torch.bmm(q[..., :NOPE].transpose(0, 1).contiguous(), self.up_k).transpose(0, 1)
-        absorbed = torch.cat([q_latent, q[..., NOPE:]], dim=-1)
+        absorbed[..., :LATENT] = torch.bmm(q[..., :NOPE].transpose(0, 1).contiguous(), self.up_k).transpose(0, 1)
         out, _ = dt.attend_selected(absorbed, self.cache, slots, LATENT, self.scale)
         return torch.bmm(out.transpose(0, 1).contiguous(), self.up_v).transpose(0, 1), slots
+
+
+def turned(layer, x, position):
+    """x [..., ROPE] by the position's angles: element i and i + 32 are a pair."""
+    cos, sin = layer.angles[position].split(32)
+    a, b = x.split(32, dim=-1)
+    return torch.cat([a * cos - b * sin, a * sin + b * cos], dim=-1)
 
 
 def plain_step(layer, x, length, table_row, slots):
     """The step of one request from the definition, in fp32, over the given slots."""
     q = (x @ layer.to_q).view(layer.heads, NOPE + ROPE).float()
+    q[:, NOPE:] = turned(layer, q[:, NOPE:], length - 1)
+    # the new token's vector has been cached
+    new = (x[None] @ layer.to_latent)[0].float()
+    body = new[:LATENT] * (new[:LATENT].square().mean() + 1e-6).rsqrt() * layer.norm
+    new = torch.cat([body, turned(layer, new[LATENT:], length - 1)])
+    cached = layer.cache[table_row[(length - 1) // PAGE].long(), (length - 1) % PAGE].float()
+    assert float((cached - new).abs().max() / new.abs().max()) < 0.02
     vectors = layer.cache.view(-1, LATENT + ROPE)[slots[slots >= 0].long()].float()
     keys = torch.einsum("tc,hdc->thd", vectors[:, :LATENT], layer.up_k.float())
     logits = torch.einsum("hd,thd->ht", q[:, :NOPE], keys) + q[:, NOPE:] @ vectors[:, LATENT:].t()
