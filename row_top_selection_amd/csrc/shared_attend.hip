@@ -70,8 +70,11 @@ __device__ __forceinline__ Args& args() {
 }
 
 constexpr int kTile = 64;   // tokens of a unit of work
-constexpr int kBegin = 6;   // a block costs its tiles and this many (first loads, last sums, the join)
-constexpr int kLeast = 4;   // units that a workgroup is started for
+// A block costs its tiles and this many: first loads, last sums, the join. With 2 / 4 / 6 / 8, 22 rows of
+// 128 heads behind 32768 tokens, 257 own ones, take 337 / 242 / 227 / 226 us, and 64 rows of 16 behind
+// 16384, 1000 own, 93 / 81 / 80 / 83.
+constexpr int kBegin = 6;
+constexpr int kLeast = 2;   // units that a workgroup is started for (4: 31 us for 4 rows behind 512 tokens, 2: 25)
 constexpr int kStarts = 1024;  // groups whose starts are kept in LDS
 
 __device__ __forceinline__ int32_t positions(Args& p) {
@@ -590,7 +593,16 @@ struct Cut {
     const bool shares = max_shared > 0, owns = max_own > 0 || !shares;
     const int64_t each = ((int64_t)rows + groups - 1) / groups * heads;  // lanes of a mean group
     lanes = each <= 32 ? 32 : each <= 64 ? 64 : 128;
-    const int32_t most = heads <= 32 ? 32 : heads <= 64 ? 64 : 128;
+    // 64 lanes, two workgroups a CU, also for larger groups, where their tiles are few for each workgroup or
+    // most are single rows' of few heads, which leave waves of 32 heads idle. Measured with 64 and with
+    // 128 (us), 16 heads: 8 rows behind 2048 tokens 30 and 38, 32 behind 4096 40 and 43, behind 16384 and
+    // 1000 own ones 61 and 61, 64 behind 16384 83 and 76; 128 rows of 2000 own tokens 73 and 97; but 256 rows
+    // of 256, 128 heads, 126 and 117.
+    const double shared_tiles = (double)((max_shared + kTile - 1) / kTile) * (double)((int64_t)rows * heads / 64 + groups);
+    const double own_tiles = owns ? (double)((max_own + kTile - 1) / kTile) * rows * ((heads + 63) / 64) : 0.0;
+    if (lanes == 128 && (shared_tiles + own_tiles <= 8.0 * kPlaces || (heads <= 64 && own_tiles >= 4.0 * shared_tiles)))
+      lanes = 64;
+    const int32_t most = heads <= 32 ? 32 : heads <= 64 || lanes == 64 ? 64 : 128;
     cols = lanes == 128 && latent == Wide::kLatent ? Wide::kCols : 16;
     own_lanes = heads < most ? (heads + cols - 1) / cols * cols : most;
     own_blocks = (heads + most - 1) / most;

@@ -14,6 +14,7 @@ from tests.test_serve_shared_gpu import batch, check, picked
 pytestmark = pytest.mark.gpu
 
 DEV = "cuda"
+WIDE = dict(max_shared_len=1 << 22)  # a bound by which calls take 128 heads a workgroup (it is one, if not a near one)
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp16"])
@@ -34,13 +35,31 @@ def test_scores_that_rise_and_fall(kind, way):
     q[..., 512:] = torch.linspace(-6, 6, rows * 16, device=DEV).view(rows, 16, 1)
     cache, q = cache.to(TYPES[kind]), q.to(TYPES[kind])
     lens = shared + np.array([0, 5, 70, 1, 33, 64, 0, 2, 31])
-    for kw in (dict(), dict(max_shared_len=1, max_own_len=1), dict(max_shared_len=shared, max_own_len=70)):
+    for kw in (dict(), dict(max_shared_len=1, max_own_len=1), dict(max_shared_len=shared, max_own_len=70), WIDE):
         check(dt, q, cache, lens, table, [0, rows], [shared], 512, page, **kw)
+
+
+def test_references_outgrown_in_a_long_part():
+    """As above, with so many heads that every workgroup has several hundred tokens."""
+    import row_top_selection_amd as dt
+
+    g = torch.Generator(DEV).manual_seed(24)
+    page, rows, shared = 64, 24, 3500
+    width = -(-(shared + 9) // page)
+    table = np.arange(rows * width).reshape(rows, width)
+    cache = torch.randn(rows * width, page, 576, generator=g, device=DEV)
+    at = torch.arange(rows * width * page, device=DEV) % (width * page)
+    cache.view(-1, 576)[:, 512:] = (8.0 * at / (width * page))[:, None]
+    q = torch.zeros(rows, 128, 576, device=DEV)
+    q[..., 512:] = torch.linspace(-9, 9, rows * 128, device=DEV)[torch.randperm(rows * 128, generator=g, device=DEV)].view(rows, 128, 1)
+    lens = np.minimum(np.arange(rows) * 200 - 100, shared + 9)
+    check(dt, q.bfloat16(), cache.bfloat16(), lens, table, [0, rows], [shared], 512, page, **WIDE)
 
 
 @pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
 @pytest.mark.parametrize("where", [0, 40, 777, 1290])
-def test_an_infinite_or_absent_number(bad, where):
+@pytest.mark.parametrize("kw", [{}, WIDE], ids=["few", "wide"])
+def test_an_infinite_or_absent_number(bad, where, kw):
     """One token's first rotary element: heads whose query makes the score -inf do not see the token, others
     give NaN, and rows that end before it know nothing of it."""
     import row_top_selection_amd as dt
@@ -56,7 +75,7 @@ def test_an_infinite_or_absent_number(bad, where):
     cache.view(-1, 576)[where, 512] = bad
     lens = np.array([shared + 10, where, 0, shared, where + 1, shared + 20, 3, where + 33, shared, 1])
     sees = torch.as_tensor(lens > where, device=DEV)[:, None].expand(-1, 16)
-    out, lse = dt.attend_shared(q, cache, i32(lens), i32(table), i32([0, rows]), i32([shared]), 512, SCALE)
+    out, lse = dt.attend_shared(q, cache, i32(lens), i32(table), i32([0, rows]), i32([shared]), 512, SCALE, **kw)
     torch.cuda.synchronize()
     if math.isnan(bad):
         numbers = ~sees
@@ -86,16 +105,16 @@ def test_lanes_tiles_and_pages(kind, heads, page, rows_of, shared, own):
     rng = np.random.default_rng(heads + page)
     table, lens, starts, pages = batch(rng, rows_of, shared, own, page)
     q, cache = make(g, sum(rows_of), heads, 512, pages, page, kind)
-    for bounds in ((None, None), (1, 1), (1, 5000), (5000, 1)):
+    for bounds in ((None, None), (1, 1), (1, 5000), (5000, 1), (1 << 22, 1), (1 << 22, 1 << 20)):
         check(dt, q, cache, lens, table, starts, shared, 512, page, max_shared_len=bounds[0], max_own_len=bounds[1])
-    # what a row does not read may hold anything; pages that are not there count nothing
+    # what no row reads may hold anything
     rows = np.arange(len(lens))
     read = np.unique(np.concatenate(picked(table, rows, lens, starts, shared, page)))
-    want = dt.attend_shared(q, cache, i32(lens), i32(table), i32(starts), i32(shared), 512, SCALE)
     other = torch.full_like(cache, math.nan)
     other.view(-1, 576)[torch.as_tensor(read, device=DEV)] = cache.view(-1, 576)[torch.as_tensor(read, device=DEV)]
-    got = dt.attend_shared(q, other, i32(lens), i32(table), i32(starts), i32(shared), 512, SCALE)
-    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    for kw in ({}, WIDE):
+        want, got = (dt.attend_shared(q, c, i32(lens), i32(table), i32(starts), i32(shared), 512, SCALE, **kw) for c in (cache, other))
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
 def test_rows_by_themselves():
@@ -110,3 +129,5 @@ def test_rows_by_themselves():
     b = check(dt, q, cache, lens, table, starts, [0, 0], 512, 16, max_shared_len=0)
     assert torch.equal(a[0][lens == 0], b[0][lens == 0]) and (a[0][lens == 0] == 0).all()
     check(dt, q, cache, np.minimum(lens, 300), table, starts, [300, 300], 512, 16, max_own_len=0)
+    check(dt, q, cache, np.minimum(lens, 300), table, starts, [300, 300], 512, 16, max_own_len=0, **WIDE)
+    check(dt, q, cache, lens, table, starts, [0, 0], 512, 16, max_own_len=1 << 20, **WIDE)
