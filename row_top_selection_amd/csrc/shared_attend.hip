@@ -477,19 +477,22 @@ __global__ __launch_bounds__(PS::kBlock, (std::is_same_v<PS, Wide> ? 1 : 2)) voi
 // whole lines. What is a single part has been written as the result.
 constexpr int kPlaces = 512;  // workgroups at most, and so parts of a block but one
 constexpr int kXcds = 8;
+constexpr int kFew = 16;  // waves that join few heads' parts
 
 template <class T, int kLatent, int kSides>
 __global__ __launch_bounds__(kSides * 64) void shared_join_kernel(SharedParams) {
   Args& p = args();
-  constexpr int kPairs = kLatent / 8;
+  constexpr int kPairs = kLatent / 8, kAtOnce = 4;
   __shared__ __attribute__((aligned(16))) char space[kSides * 64 * 24];
   f32x4* vectors = reinterpret_cast<f32x4*>(space);
   float* tops = reinterpret_cast<float*>(space + kSides * 64 * 16);
   float* sums = tops + kSides * 64;
   const int tid = threadIdx.x, lane = tid & 63, side = tid >> 6;
-  // workgroups of the same heads on the same die, whose cache puts their results together
-  const uint32_t set = blockIdx.x / kXcds;
-  const int64_t heads = (int64_t)p.rows * p.heads, x0 = ((int64_t)(set / kPairs) * kXcds + blockIdx.x % kXcds) * 32;
+  // Workgroups of the same heads on the same die, whose cache puts their results together; those of few heads on
+  // all of them (32 heads of 512 parts: 13.5 us, on one die 22.9).
+  constexpr uint32_t kDies = kSides == kFew ? 1 : kXcds;
+  const uint32_t set = blockIdx.x / kDies;
+  const int64_t heads = (int64_t)p.rows * p.heads, x0 = ((int64_t)(set / kPairs) * kDies + blockIdx.x % kDies) * 32;
   const int32_t e4 = (set % kPairs) * 2 + (lane >> 5);
   if (x0 >= heads) return;
   const int64_t x = min(x0 + (lane & 31), heads - 1);
@@ -522,14 +525,16 @@ __global__ __launch_bounds__(kSides * 64) void shared_join_kernel(SharedParams) 
 
   float top = -INFINITY, sum = 0.0f;
   f32x4 o = {};
-  auto join = [&](float (&tops)[4], const float (&ns)[4], const f32x4 (&v)[4]) {
-    const float most = fmaxf(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])), top);
+  auto join = [&](const float (&tops)[kAtOnce], const float (&ns)[kAtOnce], const f32x4 (&v)[kAtOnce]) {
+    float most = top;
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) most = fmaxf(most, tops[k]);
     const float ref = most == -INFINITY ? 0.0f : most;
     const float by = exp2_fast(top - ref);
     o *= by;
     sum *= by;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < kAtOnce; ++k) {
       if (tops[k] == -INFINITY && ns[k] == 0.0f) continue;  // such a part has no vector
       const float f = exp2_fast(tops[k] - ref);
       o += v[k] * f;
@@ -537,11 +542,11 @@ __global__ __launch_bounds__(kSides * 64) void shared_join_kernel(SharedParams) 
     }
     top = most;
   };
-  for (int32_t s = side; s < parts; s += 4 * kSides) {
-    float xs[4], ns[4];
-    f32x4 v[4];
+  for (int32_t s = side; s < parts; s += kAtOnce * kSides) {
+    float xs[kAtOnce], ns[kAtOnce];
+    f32x4 v[kAtOnce];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < kAtOnce; ++k) {
       const int32_t i = s + k * kSides;
       xs[k] = -INFINITY;
       ns[k] = 0.0f;
@@ -562,11 +567,11 @@ __global__ __launch_bounds__(kSides * 64) void shared_join_kernel(SharedParams) 
   }
   __syncthreads();
   if (side || parts == 1 || x0 + (lane & 31) >= heads) return;
-  for (int s = 1; s < kSides; s += 4) {
-    float xs[4], ns[4];
-    f32x4 v[4];
+  for (int s = 1; s < kSides; s += kAtOnce) {
+    float xs[kAtOnce], ns[kAtOnce];
+    f32x4 v[kAtOnce];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < kAtOnce; ++k) {
       const bool is = s + k < kSides;
       xs[k] = is ? tops[(s + k) * 64 + lane] : -INFINITY;
       ns[k] = is ? sums[(s + k) * 64 + lane] : 0.0f;
@@ -657,12 +662,14 @@ int launch_shared(SharedParams p, const Cut& c, void* workspace, void* stream) {
   const int st = launch_cut<T, kLatent>(p, c, stream);
   if (st != DSATOPK_OK) return st;
   const int64_t tiles = ((int64_t)p.rows * p.heads + 31) / 32;
-  const dim3 grid((unsigned)((tiles + kXcds - 1) / kXcds * kXcds * (kLatent / 8)));
+  const auto grid = [&](int64_t dies) {
+    return dim3((unsigned)((tiles + dies - 1) / dies * dies * (kLatent / 8)));
+  };
   // A wave by itself for many heads (2112 heads of 16 parts: 12.6 us, 20.4 by four); few are too few waves to have
   // the memory busy (1024 heads of 33 parts: 11.7 us by four, 14.5 by eight), and may have a part of every workgroup.
-  return tiles >= 64   ? launch(shared_join_kernel<T, kLatent, 1>, grid, dim3(64), p, stream)
-         : tiles >= 16 ? launch(shared_join_kernel<T, kLatent, 4>, grid, dim3(256), p, stream)
-                       : launch(shared_join_kernel<T, kLatent, 16>, grid, dim3(1024), p, stream);
+  return tiles >= 64   ? launch(shared_join_kernel<T, kLatent, 1>, grid(kXcds), dim3(64), p, stream)
+         : tiles >= 16 ? launch(shared_join_kernel<T, kLatent, 4>, grid(kXcds), dim3(256), p, stream)
+                       : launch(shared_join_kernel<T, kLatent, kFew>, grid(1), dim3(kFew * 64), p, stream);
 }
 
 }  // namespace
