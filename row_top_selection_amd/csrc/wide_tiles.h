@@ -7,6 +7,11 @@
 // their queries (144) leave room for one wave a SIMD, which has to be kept busy by
 // itself: the scores of the next 32 tokens are computed beside the softmax of
 // the current ones, and reads go several products ahead.
+//
+// A tile of 32 tokens takes a wave 68 products of 32 cycles, 2176, and the four
+// waves' reads of it 272 KB, 2125 cycles of LDS; it is done in 2.35 us. With 16
+// heads a wave and eight waves (twice the reads) 64 rows of 16 heads behind 262144
+// tokens take 748 us, with these 638; behind 16384, up to 1000 own ones, 87 and 79.
 #ifndef DSATOPK_WIDE_TILES_H_
 #define DSATOPK_WIDE_TILES_H_
 
