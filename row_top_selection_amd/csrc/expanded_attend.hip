@@ -25,8 +25,9 @@
 // joins the parts.
 //
 // With shared keys a workgroup takes the next 32 queries a wave of those that
-// stand together and share them, whichever requests they are of, and goes over
-// segments of keys: the shared ones, once for all, then each request's own. A lane counts the keys of a segment that its query sees; waves
+// stand together, whichever requests they are of, and goes over segments of
+// keys: those that the requests share, once for all of them that stand
+// together, then each request's own. A lane counts the keys of a segment that its query sees; waves
 // none of whose queries are in a segment only copy. Prompts of 16 tokens fill
 // tiles that way, which would be nearly empty if every request had its own.
 //
@@ -411,57 +412,96 @@ struct Segment {
   }
 };
 
-// A workgroup's queries, which share their first keys: tile `index` of the runs of
-// requests with the same shared keys, each cut into tiles from its own first
-// query on. (In tiles of the batch, one that two runs meet in goes over both runs' keys,
-// twice what the others take: 2 x 4 prompts of up to 777 tokens behind 2000, 16
-// heads, took 200 us.) Threads take chunks of the requests: the last
-// beginning of a run before a chunk, and the tiles that end before it, from those of the others.
-struct Run {
-  int32_t q0, q1, first;  // queries; the run's first request
+// A workgroup's queries: tile `index` of the batch's stretches, each cut into tiles from its own
+// first query on. A stretch is a run of requests with the same shared keys. (In tiles of the
+// whole batch, one that two runs meet in goes over both runs' keys, twice what the others take:
+// 2 x 4 prompts of up to 777 tokens behind 2000, 16 heads, took 200 us and take 105.) Where
+// there are many requests for the queries (kPacked), all runs of less than half a tile that
+// stand together are one stretch, or single tokens might each need a workgroup. Threads take chunks
+// of the requests, and what is before or behind a chunk from the others.
+struct Tile {
+  int32_t q0, q1, first;  // queries; the stretch's first request
 };
-template <class S>
-__device__ __forceinline__ Run run_of(const ExpandParams& p, int32_t index, char* space, int tid, int wave, int lane) {
+template <class S, bool kPacked>
+__device__ __forceinline__ Tile tile_of(const ExpandParams& p, int32_t index, char* space, int tid, int wave,
+                                        int lane) {
   struct Room {
-    int32_t begins[S::kWaves], tiles[S::kWaves];
-    Run run;
+    int32_t last[S::kWaves], next[S::kWaves], cuts[S::kWaves], tiles[S::kWaves];
+    Tile tile;
   };
   Room& room = *reinterpret_cast<Room*>(space);
+  const int32_t chunk = p.requests / S::kBlock + 1;
+  const int32_t r0 = min(tid * chunk, p.requests), r1 = min(r0 + chunk, p.requests);
   auto start = [&](int32_t r) { return min(max(p.q_starts[r], 0), p.num_q); };
+  auto queries = [&](int32_t from, int32_t to) { return max(start(to) - start(from), 0); };
   auto begins = [&](int32_t r) {
     return r == 0 || p.shared_starts[r] != p.shared_starts[r - 1] || p.shared_lens[r] != p.shared_lens[r - 1];
   };
-  auto count = [&](int32_t from, int32_t to) { return (max(start(to) - start(from), 0) + S::kRows - 1) / S::kRows; };
-  const int32_t chunk = p.requests / S::kBlock + 1;
-  const int32_t r0 = min(tid * chunk, p.requests), r1 = min(r0 + chunk, p.requests);
-  int32_t begin = 0;
-  for (int32_t r = r0; r < r1; ++r)
-    if (begins(r)) begin = r;
-  // the largest of the threads up to this one, then of those before it
+  // the largest of the threads before this one, 0 if there is none; `all` of a wave each
+  auto before = [&](int32_t x, int32_t* all) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int32_t o = __shfl_up(x, d);
+      if (lane >= d) x = max(x, o);
+    }
+    if (lane == 63) all[wave] = x;
+    __syncthreads();
+    x = __shfl_up(x, 1);
+    if (lane == 0) x = 0;
+#pragma unroll
+    for (int w = 0; w < S::kWaves; ++w)
+      if (w < wave) x = max(x, all[w]);
+    return x;
+  };
+  // runs: where the one before the chunk begins, and the first one behind it
+  int32_t last = 0, next = p.requests;
+  for (int32_t r = r1 - 1; r >= r0; --r)
+    if (begins(r)) {
+      last = max(last, r);
+      next = r;
+    }
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const int32_t o = __shfl_up(begin, d);
-    if (lane >= d) begin = max(begin, o);
+    const int32_t o = __shfl_down(next, d);
+    if (lane + d < 64) next = min(next, o);
   }
-  if (lane == 63) room.begins[wave] = begin;
-  if (tid == 0) room.run = Run{0, 0, 0};
-  __syncthreads();
-  begin = __shfl_up(begin, 1);
-  if (lane == 0) begin = 0;
+  if (lane == 0) room.next[wave] = next;
+  if (tid == 0) room.tile = Tile{0, 0, 0};
+  last = before(last, room.last);
+  next = __shfl_down(next, 1);
+  if (lane == 63) next = p.requests;
 #pragma unroll
   for (int w = 0; w < S::kWaves; ++w)
-    if (w < wave) begin = max(begin, room.begins[w]);
-  // Runs that end in the chunk: where the next one begins, or behind the last request.
-  auto each = [&](auto&& what) {
-    int32_t from = begin;
+    if (w > wave) next = min(next, room.next[w]);
+  // Stretches begin where a run does; packed, if that or the one before it is long.
+  auto stretches = [&](auto&& what) {
+    int32_t run = last;
     for (int32_t r = r0; r < r1; ++r) {
-      if (r > 0 && begins(r)) {
-        what(from, r);
-        from = r;
+      if (!begins(r)) continue;
+      if (!kPacked) {
+        what(r);
+        continue;
       }
-      if (r + 1 == p.requests) what(from, r + 1);
+      int32_t end = r + 1;
+      while (end < r1 && !begins(end)) ++end;
+      if (end == r1) end = next;
+      if (r == 0 || 2 * queries(run, r) >= S::kRows || 2 * queries(r, end) >= S::kRows) what(r);
+      run = r;
     }
   };
+  int32_t cut = 0;
+  stretches([&](int32_t r) { cut = r; });
+  cut = before(cut, room.cuts);
+  // tiles of the stretches that end in the chunk
+  auto each = [&](auto&& what) {
+    int32_t from = cut;
+    stretches([&](int32_t r) {
+      if (r > 0) what(from, r);
+      from = r;
+    });
+    if (r0 < r1 && r1 == p.requests) what(from, r1);
+  };
+  auto count = [&](int32_t from, int32_t to) { return (queries(from, to) + S::kRows - 1) / S::kRows; };
   int32_t tiles = 0;
   each([&](int32_t from, int32_t to) { tiles += count(from, to); });
   int32_t below = tiles;
@@ -481,44 +521,70 @@ __device__ __forceinline__ Run run_of(const ExpandParams& p, int32_t index, char
       const int32_t n = count(from, to);
       if (index >= below && index < below + n) {
         const int32_t q0 = start(from) + (index - below) * S::kRows;
-        room.run = Run{q0, min(q0 + S::kRows, start(to)), from};
+        room.tile = Tile{q0, min(q0 + S::kRows, start(to)), from};
       }
       below += n;
     });
   __syncthreads();
-  const Run run{__builtin_amdgcn_readfirstlane(room.run.q0), __builtin_amdgcn_readfirstlane(room.run.q1),
-                __builtin_amdgcn_readfirstlane(room.run.first)};
-  __syncthreads();  // before the space is taken for tiles
-  return run;
+  const Tile tile{__builtin_amdgcn_readfirstlane(room.tile.q0), __builtin_amdgcn_readfirstlane(room.tile.q1),
+                  __builtin_amdgcn_readfirstlane(room.tile.first)};
+  __syncthreads();  // before the space is taken for tiles of keys
+  return tile;
 }
 
-// The segments of the queries q0 .. q1 - 1, of one run, a tile of keys at a time: the
-// shared keys, then the requests' own. The same in all lanes.
-template <class S>
+// The segments of the queries q0 .. q1 - 1, a tile of keys at a time. The same in
+// all lanes.
+template <class S, bool kPacked>
 struct Walk {
   const ExpandParams& p;
   int32_t q0, q1;
-  int32_t request;  // whose own keys come next
+  int32_t request;  // whose own keys come next, or with whom a new run begins
+  int32_t run;      // the first request behind those that share with it
   Segment at;
   int32_t j;  // first key of the tile, in the segment
   bool done;
 
   __device__ __forceinline__ Walk(const ExpandParams& params, int32_t first, int32_t last, int32_t r)
-      : p(params), q0(first), q1(last), request(r), at{}, j(0), done(false) {
+      : p(params), q0(first), q1(last), request(r), run(r), at{}, j(0), done(false) {
+    if (kPacked) {
+      next();
+    } else {  // one run: its shared keys, and then requests only
+      share(r, q0, q1);
+      if (at.len == 0) next();
+    }
+  }
+  __device__ __forceinline__ int32_t starts(int32_t r) const { return max(p.q_starts[r], 0); }
+  __device__ __forceinline__ int32_t ends(int32_t r) const { return min(p.q_starts[r + 1], p.num_q); }
+  // The keys that request r shares, for the queries from .. to - 1.
+  __device__ __forceinline__ void share(int32_t r, int32_t from, int32_t to) {
     at.base = min(max(p.shared_starts[r], 0), p.num_k);
     at.len = min(max(p.shared_lens[r], 0), p.num_k - at.base);
-    at.from = q0;
-    at.to = q1;
+    at.from = from;
+    at.to = to;
     at.diag = at.len;
-    if (at.len == 0) next();
   }
 
   __device__ __forceinline__ void next() {
     j = 0;
-    while (request < p.requests) {
+    while (true) {
+      if (kPacked && request >= run) {
+        while (request < p.requests && starts(request) >= ends(request)) ++request;
+        if (request < p.requests && starts(request) < q1) {
+          const int32_t first = p.shared_starts[request], len = p.shared_lens[request];
+          run = request + 1;
+          while (run < p.requests && starts(run) < q1 &&
+                 (starts(run) >= ends(run) || (p.shared_starts[run] == first && p.shared_lens[run] == len)))
+            ++run;
+          share(request, max(starts(request), q0), min(ends(run - 1), q1));
+          if (at.len > 0 && at.from < at.to) return;
+        }
+      }
+      if (request >= p.requests || starts(request) >= q1) {
+        done = true;
+        return;
+      }
       const int32_t r = request++;
-      const int32_t first = max(p.q_starts[r], 0), rows = min(p.q_starts[r + 1], p.num_q) - first;
-      if (first >= q1) break;
+      const int32_t first = starts(r), rows = ends(r) - first;
       at.base = min(max(p.k_starts[r], 0), p.num_k);
       const int32_t keys = max(min(p.k_starts[r + 1], p.num_k) - at.base, 0);
       at.from = max(first, q0);
@@ -528,7 +594,6 @@ struct Walk {
       at.len = min(max(at.to - 1 + at.diag, 0), keys);
       if (at.len > 0) return;
     }
-    done = true;
   }
   __device__ __forceinline__ void advance() {
     j += S::kTile;
@@ -553,7 +618,7 @@ struct Walk {
   }
 };
 
-template <class T, class S>
+template <class T, class S, bool kPacked>
 __global__ __launch_bounds__(S::kBlock, 2) void expand_shared_kernel(ExpandParams p) {
   constexpr int kRows = S::kRows, kTile = S::kTile, kRing = S::kRing, kBuffer = S::kBuffer;
   constexpr int kAheadTiles = kRing - 1, kParts = kTile / kKeys;
@@ -567,15 +632,15 @@ __global__ __launch_bounds__(S::kBlock, 2) void expand_shared_kernel(ExpandParam
   const int split = blockIdx.y;
   const int head = id / (8 * p.tiles) * 8 + id % 8;
   if (head >= p.heads) return;
-  const Run run = run_of<S>(p, p.tiles - 1 - (int32_t)(id / 8 % p.tiles), tiles, tid, wave, lane);
-  const int32_t q0 = run.q0, q1 = run.q1;
+  const Tile tile = tile_of<S, kPacked>(p, p.tiles - 1 - (int32_t)(id / 8 % p.tiles), tiles, tid, wave, lane);
+  const int32_t q0 = tile.q0, q1 = tile.q1;
   if (q0 >= q1) return;
-  const int32_t r = max(run.first, last_below(p.requests, q0, lane, [&](int32_t i) { return (int64_t)p.q_starts[i]; }));
-  const int32_t w0 = q0 + wave * 32, mine = w0 + col;
-  const int64_t at = min(mine, q1 - 1);
+  const int32_t r = max(tile.first, last_below(p.requests, q0, lane, [&](int32_t i) { return (int64_t)p.q_starts[i]; }));
+  const int32_t w0 = q0 + wave * 32;
+  const int32_t at = min(w0 + col, q1 - 1);
 
   u32x4 q[kSteps];
-  const char* qh = p.q + at * p.q_row + head * p.q_head;
+  const char* qh = p.q + (int64_t)at * p.q_row + head * p.q_head;
 #pragma unroll
   for (int i = 0; i < kSteps; ++i) q[i] = load16(qh + (2 * i + half) * 16);
 
@@ -585,15 +650,16 @@ __global__ __launch_bounds__(S::kBlock, 2) void expand_shared_kernel(ExpandParam
 #pragma unroll
   for (int b = 0; b < kBlocks; ++b) st.o[b] = f32x16{};
 
-  Walk<S> use(p, q0, q1, r);
+  using Keys = Walk<S, kPacked>;
+  Keys use(p, q0, q1, r);
   int32_t most = INT32_MAX;
   if (p.splits > 1) {
-    const int32_t all = Walk<S>(use).tiles();
+    const int32_t all = Keys(use).tiles();
     const int32_t per = (all + p.splits - 1) / p.splits;
     most = per;
     use.skip(split * per);
   }
-  Walk<S> copy(use);
+  Keys copy(use);
   const Places<S> places(p, lane);
   int32_t copied = 0;
   auto keys_at = [&](const char* base, int64_t head_bytes, int64_t row_bytes) {
@@ -616,7 +682,7 @@ __global__ __launch_bounds__(S::kBlock, 2) void expand_shared_kernel(ExpandParam
       // what the wave's queries see of the segment, at most and at least
       const int32_t top = w0 < seg.to ? seg.seen(min(w0 + 31, seg.to - 1)) : 0;
       const int32_t low = w0 + 31 < seg.to ? seg.seen(w0) : 0;
-      const int32_t sees = seg.seen((int32_t)at);  // lanes past the last query do as that does
+      const int32_t sees = seg.seen(at);  // lanes past the last query do as that does
 #pragma unroll
       for (int part = 0; part < kParts; ++part) {
         const bool last = part + 1 == kParts;
@@ -651,7 +717,8 @@ __global__ __launch_bounds__(S::kBlock, 2) void expand_shared_kernel(ExpandParam
       }
     }
   }
-  if (mine < q1) put<T>(p, st, at, head, split, half);
+  const int now = here(lane);
+  if (w0 + (now & 31) < q1) put<T>(p, st, w0 + (now & 31), head, split, now >> 5);
 }
 
 // Joins the parts of the rows' heads: 32 threads for each, 4 elements a
@@ -751,18 +818,28 @@ Cut shared_cut_of(int32_t heads, int32_t queries, int32_t max_keys) {
   if (c.wide) c.splits = 1;
   return c;
 }
-// Tiles that its runs of requests may have.
-int64_t shared_tiles(int32_t queries, int32_t requests, int rows) {
-  const int64_t n = (int64_t)queries / rows + requests;
-  return n < queries ? n : queries;
+// Tiles that its stretches may have (every one may end in a part of one): there are no more than requests,
+// nor, packed, than long runs and what lies between them. Packed where that leaves fewer. With and without (us),
+// behind 2000 shared keys, 16 heads: 64 requests of 1 query 127 and 135, 256 of 1 237 and 290, 1000 of 3 319
+// and 538, 256 of 16 157 and 188; where every run is a tile or more, packing has nothing to leave out and its
+// longer walk over the keys costs up to 5%: 2 x 4 prompts of up to 777 113 and 107.
+struct Tiles {
+  int32_t most;
+  bool packed;
+};
+Tiles shared_tiles(int32_t queries, int32_t requests, int rows) {
+  const int64_t whole = queries / rows, runs = 2 * ((int64_t)queries / (rows / 2)) + 1;
+  const int64_t n = whole + (requests < runs ? requests : runs);
+  return {(int32_t)(n < queries ? n : queries), requests > runs};
 }
 
 template <class T, class S>
 int launch_shared(ExpandParams p, const Cut& c, void* stream) {
-  p.tiles = (int32_t)shared_tiles(p.num_q, p.requests, S::kRows);
+  const Tiles tiles = shared_tiles(p.num_q, p.requests, S::kRows);
+  p.tiles = tiles.most;
   p.splits = c.splits;
-  const int st = launch(expand_shared_kernel<T, S>, dim3((unsigned)(c.pairs * p.tiles), (unsigned)c.splits),
-                        dim3(S::kBlock), p, stream);
+  const int st = launch(tiles.packed ? expand_shared_kernel<T, S, true> : expand_shared_kernel<T, S, false>,
+                        dim3((unsigned)(c.pairs * p.tiles), (unsigned)c.splits), dim3(S::kBlock), p, stream);
   if (st != DSATOPK_OK || c.splits == 1) return st;
   p.tiles = INT32_MAX / Shape<4>::kRows;  // every row of a request has been computed
   const int64_t each = (int64_t)p.num_q * p.heads;
@@ -900,7 +977,7 @@ extern "C" int dsatopk_attend_expanded_shared(
   p.shared_starts = shared_starts;
   p.shared_lens = shared_lens;
   const Cut c = shared_cut_of(num_heads, num_queries, max_keys);
-  if (c.pairs * shared_tiles(num_queries, num_requests, 128) > INT32_MAX) return DSATOPK_ERR_INVALID_ARG;
+  if (c.pairs * shared_tiles(num_queries, num_requests, 128).most > INT32_MAX) return DSATOPK_ERR_INVALID_ARG;
   st = check_room(p, c, workspace, workspace_bytes);
   if (st != DSATOPK_OK) return st;
   const bool bf16 = type == DSATOPK_BF16;

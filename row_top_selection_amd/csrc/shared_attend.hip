@@ -60,6 +60,7 @@ struct SharedParams {
   // Parts: vectors [number, lanes / cols, latent / 4, cols, 4], as the lanes of a product hold them; references
   // and sums [number, lanes, 2]; first and last part of each block [blocks, 2].
   int32_t cols;
+  int32_t shared_most, own_most;  // numbers that there are
   float* shared_part;
   float* shared_state;
   int32_t* shared_numbers;
@@ -487,6 +488,13 @@ constexpr int kPlaces = 512;  // workgroups at most, and so parts of a block but
 constexpr int kXcds = 8;
 constexpr int kFew = 16;  // waves that join few heads' parts
 
+// Parts of a block, by its first and last number. Starts that do not rise may leave blocks that nobody
+// has numbered: they have none.
+__device__ __forceinline__ int32_t parts_of(const int32_t* numbers, int32_t most) {
+  const int32_t a = numbers[0], b = numbers[1];
+  return a >= 0 && a <= b && b < most && b - a <= kPlaces ? b - a + 1 : 0;
+}
+
 template <class T, int kLatent, int kSides>
 __global__ __launch_bounds__(kSides * 64) void shared_join_kernel(SharedParams) {
   Args& p = args();
@@ -514,13 +522,13 @@ __global__ __launch_bounds__(kSides * 64) void shared_join_kernel(SharedParams) 
     const int32_t start = start_of(p, g);
     const int64_t i = x - (int64_t)start * p.heads;
     const int32_t* numbers = p.shared_numbers + (first_block(p, start, g) + i / p.lanes) * 2;
-    n = numbers[1] - numbers[0] + 1;
-    first = (int64_t)numbers[0] * p.lanes + i % p.lanes;
+    n = parts_of(numbers, p.shared_most);
+    first = (int64_t)(n ? numbers[0] : 0) * p.lanes + i % p.lanes;
   }
   if (p.owns && length_of(p, row) > shared) {
     const int32_t* numbers = p.own_numbers + ((int64_t)row * p.own_blocks + head / p.own_lanes) * 2;
-    m = numbers[1] - numbers[0] + 1;
-    own = (int64_t)numbers[0] * p.own_lanes + head % p.own_lanes;
+    m = parts_of(numbers, p.own_most);
+    own = (int64_t)(m ? numbers[0] : 0) * p.own_lanes + head % p.own_lanes;
   }
   const int32_t parts = n + m, cols = p.cols;
   // (lanes of a block are a multiple of cols)
@@ -661,6 +669,8 @@ int launch_shared(SharedParams p, const Cut& c, void* workspace, void* stream) {
   p.own_lanes = c.own_lanes;
   p.own_blocks = c.own_blocks;
   p.cols = c.cols;
+  p.shared_most = (int32_t)(c.shared_blocks + c.places);
+  p.own_most = (int32_t)(c.own + c.places);
   p.shared_part = static_cast<float*>(workspace);
   p.own_part = p.shared_part + c.shared_parts * kLatent;
   p.shared_state = p.own_part + c.own_parts * kLatent;
