@@ -678,10 +678,9 @@ int dsatopk_attend_expanded(const void* q, int64_t q_row_stride, int64_t q_head_
  * 1] - 1, which it sees as in dsatopk_attend_expanded.
  *
  *   shared_starts, shared_lens  int32 [num_requests], negative values read as
- *                 0, lengths cut at num_keys. Neighbouring requests (apart from
- *                 those without queries) with the same two values share the work
- *                 on these keys, too; equal values further apart do not. Length 0:
- *                 none are shared.
+ *                 0, lengths cut at num_keys. Neighbouring requests with the
+ *                 same two values share the work on these keys, too; equal
+ *                 values further apart do not. Length 0: none are shared.
  *   num_queries, num_keys  at most 2^30.
  *   max_keys      an upper bound on a request's keys, shared and own; it sets how
  *                 few rows of many keys are split (and the workspace's size),
