@@ -358,6 +358,7 @@ __device__ __forceinline__ bool next_job(Job& job, const Starts& starts, int tid
   int32_t e = uniform(job.entry);
   int64_t in = uniform(job.in), at = uniform(job.at);
   const int64_t end = uniform(job.end);
+  __syncthreads();  // before the next one is written
   while (at < end) {
     int32_t g = -1;
     const Entry x = entry_of(p, starts, e, g);

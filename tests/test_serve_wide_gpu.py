@@ -131,3 +131,33 @@ def test_rows_by_themselves():
     check(dt, q, cache, np.minimum(lens, 300), table, starts, [300, 300], 512, 16, max_own_len=0)
     check(dt, q, cache, np.minimum(lens, 300), table, starts, [300, 300], 512, 16, max_own_len=0, **WIDE)
     check(dt, q, cache, lens, table, starts, [0, 0], 512, 16, max_own_len=1 << 20, **WIDE)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("heads", [8, 16, 40, 64, 128])
+def test_smaller_vectors(heads, kind):
+    """Latent vectors of 256: 128 heads a workgroup, and rows of few, some and all of them."""
+    import row_top_selection_amd as dt
+
+    g = torch.Generator(DEV).manual_seed(heads)
+    rng = np.random.default_rng(heads)
+    table, lens, starts, pages = batch(rng, [17, 9], [300, 65], [70, 0, 33], 16)
+    q, cache = make(g, 26, heads, 256, pages, 16, kind)
+    for kw in (WIDE, dict(WIDE, max_own_len=1 << 18), dict(WIDE, max_own_len=0)):
+        lens_of = np.minimum(lens, [300] * 17 + [65] * 9) if kw.get("max_own_len") == 0 else lens
+        check(dt, q, cache, lens_of, table, starts, [300, 65], 256, 16, **kw)
+
+
+def test_jobs_one_after_the_other():
+    """So many short groups that every workgroup has several, by the calls with 32, 64 and 128 lanes."""
+    import row_top_selection_amd as dt
+
+    g = torch.Generator(DEV).manual_seed(25)
+    rng = np.random.default_rng(25)
+    for rows_of, heads, kw in (([1] * 900, 16, {}), ([3] * 900, 16, {}), ([1] * 700, 128, WIDE)):
+        shared = rng.integers(0, 90, len(rows_of)).tolist()
+        table, lens, starts, pages = batch(rng, rows_of, shared, [0, 3, 40, 1], 32)
+        q, cache = make(g, sum(rows_of), heads, 512, pages, 32, "bf16")
+        first = check(dt, q, cache, lens, table, starts, shared, 512, 32, **kw)
+        again = dt.attend_shared(q, cache, i32(lens), i32(table), i32(starts), i32(shared), 512, SCALE, **kw)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
