@@ -36,7 +36,7 @@
 // falls with what the matrix units switch: the same call on zeros takes 530
 // us.
 //
-// 16 x 512 queries that share 16384 keys, 16 heads: 1250 us, 1.12 PFLOP/s.
+// 16 x 512 queries that share 16384 keys, 16 heads: 1250 ... 1300 us by card, 1.1 PFLOP/s.
 //
 // Weights are rounded to the inputs' type for the second product (off by at
 // most 2^-8 of each in bfloat16; in half precision by 2^-11 of each or 2^-35

@@ -735,8 +735,8 @@ int dsatopk_attend_shared(const void* q, int64_t q_row_stride, int64_t q_head_st
   p.shares = max_shared_len > 0;
   p.owns = max_own_len > 0 || !p.shares;
   const Cut c(num_rows, num_heads, latent_dim, num_groups, max_shared_len, max_own_len);
-  // parts are numbered, and heads counted, in 32 bits
-  if ((int64_t)num_rows * num_heads * (latent_dim / 128) > INT32_MAX || c.shared_blocks + kPlaces > INT32_MAX ||
+  // parts are numbered, and the join's threads counted, in 32 bits
+  if ((int64_t)num_rows * num_heads * (latent_dim / 4) > INT32_MAX || c.shared_blocks + kPlaces > INT32_MAX ||
       c.own + kPlaces > INT32_MAX || (int64_t)num_groups + num_rows > INT32_MAX)
     return DSATOPK_ERR_INVALID_ARG;
   if (!workspace || workspace_bytes < c.bytes()) return DSATOPK_ERR_WORKSPACE_TOO_SMALL;
