@@ -15,8 +15,8 @@
 // A block is the heads of several rows, up to 32, 64 or 128, with a head of its own
 // row in each lane; a lane counts how many of the tokens its row sees
 // (drafted tokens, whose rows see one token more each). Tiles, products and
-// softmax up to 64 heads are those of one row's heads (latent_tiles.h); 128 heads
-// have a loop of their own (wide_tiles.h).
+// softmax are those of one row's heads (latent_tiles.h), but 128 heads of vectors of 512
+// have a loop of their own (wide_tiles.h): in four waves, where those of 256 take eight.
 //
 // How many tokens there are of which kind only the device knows. Each workgroup
 // adds up the tiles of all blocks (a few thousand lengths at most, from L2) and
