@@ -618,6 +618,10 @@ struct Walk {
   }
 };
 
+// Dies that one head's workgroups are on, of 8: all on one leave the others idle where heads are few (2 x 6 prompts
+// of up to 243 behind 9373, one head: 47 us, on one die 139; 8 of up to 600 behind 4000, four heads, 100 and 139).
+__host__ __device__ constexpr int dies_of(int heads) { return heads < 8 ? 8 / heads : 1; }
+
 template <class T, class S, bool kPacked>
 __global__ __launch_bounds__(S::kBlock, 2) void expand_shared_kernel(ExpandParams p) {
   constexpr int kRows = S::kRows, kTile = S::kTile, kRing = S::kRing, kBuffer = S::kBuffer;
@@ -627,12 +631,13 @@ __global__ __launch_bounds__(S::kBlock, 2) void expand_shared_kernel(ExpandParam
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 31, half = lane >> 5;
 
-  // Workgroup -> (head, queries), as above: those of one head are 8 apart.
-  const uint32_t id = blockIdx.x;
-  const int split = blockIdx.y;
-  const int head = id / (8 * p.tiles) * 8 + id % 8;
-  if (head >= p.heads) return;
-  const Tile tile = tile_of<S, kPacked>(p, p.tiles - 1 - (int32_t)(id / 8 % p.tiles), tiles, tid, wave, lane);
+  // Workgroup -> (head, queries), as above: those of one head are 8 apart. Less than 8 heads have several dies each.
+  const uint32_t id = blockIdx.x, slot = id % 8;
+  const int split = blockIdx.y, dies = dies_of(p.heads);
+  const int head = dies > 1 ? slot / dies : id / (8 * p.tiles) * 8 + slot;
+  const int index = dies > 1 ? id / 8 * dies + slot % dies : id / 8 % p.tiles;
+  if (head >= p.heads || index >= p.tiles) return;
+  const Tile tile = tile_of<S, kPacked>(p, p.tiles - 1 - index, tiles, tid, wave, lane);
   const int32_t q0 = tile.q0, q1 = tile.q1;
   if (q0 >= q1) return;
   const int32_t r = max(tile.first, last_below(p.requests, q0, lane, [&](int32_t i) { return (int64_t)p.q_starts[i]; }));
@@ -819,27 +824,32 @@ Cut shared_cut_of(int32_t heads, int32_t queries, int32_t max_keys) {
   return c;
 }
 // Tiles that its stretches may have (every one may end in a part of one): there are no more than requests,
-// nor, packed, than long runs and what lies between them. Packed where that leaves fewer. With and without (us),
-// behind 2000 shared keys, 16 heads: 64 requests of 1 query 127 and 135, 256 of 1 237 and 290, 1000 of 3 319
-// and 538, 256 of 16 157 and 188; where every run is a tile or more, packing has nothing to leave out and its
-// longer walk over the keys costs up to 5%: 2 x 4 prompts of up to 777 113 and 107.
+// nor, packed, than long runs and what lies between them. Packed where that leaves fewer, and they would be
+// several times what the card holds at once. With and without (us), behind 2000 shared keys, 16 heads: 64
+// requests of 1 query 127 and 135, 256 of 1 237 and 290, 1000 of 3 319 and 538, 256 of 16 157 and 188; but 18
+// of 1 or 2, one head, behind three sets of up to 2244 keys, 87 and 33; and where every run is a tile or more,
+// packing has nothing to leave out and its longer walk over the keys costs up to 5%: 2 x 4 prompts of up to 777
+// 113 and 107.
 struct Tiles {
   int32_t most;
   bool packed;
 };
-Tiles shared_tiles(int32_t queries, int32_t requests, int rows) {
+Tiles shared_tiles(int32_t queries, int32_t requests, int64_t each, int rows) {
   const int64_t whole = queries / rows, runs = 2 * ((int64_t)queries / (rows / 2)) + 1;
-  const int64_t n = whole + (requests < runs ? requests : runs);
-  return {(int32_t)(n < queries ? n : queries), requests > runs};
+  const bool packed = requests > runs && each * (whole + requests) > 2048;
+  const int64_t n = whole + (packed ? runs : requests);
+  return {(int32_t)(n < queries ? n : queries), packed};
 }
 
 template <class T, class S>
 int launch_shared(ExpandParams p, const Cut& c, void* stream) {
-  const Tiles tiles = shared_tiles(p.num_q, p.requests, S::kRows);
+  const Tiles tiles = shared_tiles(p.num_q, p.requests, (int64_t)p.heads * c.splits, S::kRows);
+  const int dies = dies_of(p.heads);
+  const int64_t groups = dies > 1 ? ((int64_t)tiles.most + dies - 1) / dies * 8 : c.pairs * tiles.most;
   p.tiles = tiles.most;
   p.splits = c.splits;
   const int st = launch(tiles.packed ? expand_shared_kernel<T, S, true> : expand_shared_kernel<T, S, false>,
-                        dim3((unsigned)(c.pairs * p.tiles), (unsigned)c.splits), dim3(S::kBlock), p, stream);
+                        dim3((unsigned)groups, (unsigned)c.splits), dim3(S::kBlock), p, stream);
   if (st != DSATOPK_OK || c.splits == 1) return st;
   p.tiles = INT32_MAX / Shape<4>::kRows;  // every row of a request has been computed
   const int64_t each = (int64_t)p.num_q * p.heads;
@@ -977,7 +987,7 @@ extern "C" int dsatopk_attend_expanded_shared(
   p.shared_starts = shared_starts;
   p.shared_lens = shared_lens;
   const Cut c = shared_cut_of(num_heads, num_queries, max_keys);
-  if (c.pairs * shared_tiles(num_queries, num_requests, 128).most > INT32_MAX) return DSATOPK_ERR_INVALID_ARG;
+  if (c.pairs * shared_tiles(num_queries, num_requests, (int64_t)num_heads * c.splits, 128).most > INT32_MAX) return DSATOPK_ERR_INVALID_ARG;
   st = check_room(p, c, workspace, workspace_bytes);
   if (st != DSATOPK_OK) return st;
   const bool bf16 = type == DSATOPK_BF16;
