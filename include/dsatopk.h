@@ -691,9 +691,10 @@ int dsatopk_attend_expanded(const void* q, int64_t q_row_stride, int64_t q_head_
  *
  * The other arguments, the rounding and the errors are those of
  * dsatopk_attend_expanded, but there is no max_queries: all rows are
- * computed. Values must be finite here, too, also the shared ones and the
- * neighbouring requests' own: those of a key that any of 256 queries standing
- * together sees.
+ * computed. Values must be finite here, too, those of a request's own keys
+ * and of the shared ones. Other requests' keys may hold anything: where queries
+ * of several requests stand in a tile (of up to 256) and a result is not
+ * finite, the tile is computed once more, each query from its own keys only.
  */
 size_t dsatopk_expanded_shared_bytes(int32_t num_heads, int32_t num_queries, int32_t max_keys);
 

@@ -206,8 +206,9 @@ __device__ __forceinline__ f32x16 scores_of(const char* tile, int part, const u3
 // the copies of the tile at key copy_j. The tiles are told apart so that no
 // read of one waits for the copies of another. `seen`: how many of the 32 keys
 // this lane's query sees (may be negative or above 32); `whole`: all of them, for
-// every lane of the wave.
-template <class T, class S>
+// every lane of the wave. With kApart nothing of keys that a query sees none of goes into
+// its sums, whatever their values are (a weight of 0 times an infinite one is NaN).
+template <class T, class S, bool kApart = false>
 __device__ __forceinline__ void keys_step(const ExpandParams& p, State& st, f32x16& s,
                                           const u32x4 (&q)[kSteps], const char* __restrict__ cur,
                                           int part, const char* __restrict__ after, int after_part,
@@ -242,8 +243,10 @@ __device__ __forceinline__ void keys_step(const ExpandParams& p, State& st, f32x
     return u32x4{lo[0], lo[1], hi[0], hi[1]};
   };
   u32x4 a[kAhead];
+  if constexpr (!kApart) {
 #pragma unroll
-  for (int n = 0; n < kAhead; ++n) a[n] = read(n);
+    for (int n = 0; n < kAhead; ++n) a[n] = read(n);
+  }
   if (__any(!(sum <= T::kMost) || st.top == -INFINITY)) {
     float top = s[0];
 #pragma unroll
@@ -264,10 +267,23 @@ __device__ __forceinline__ void keys_step(const ExpandParams& p, State& st, f32x
   st.sum += sum;
   s = next;
 
+  auto weights = [&](int g) {
+    return u32x4{T::pack(w[8 * g], w[8 * g + 1]), T::pack(w[8 * g + 2], w[8 * g + 3]),
+                 T::pack(w[8 * g + 4], w[8 * g + 5]), T::pack(w[8 * g + 6], w[8 * g + 7])};
+  };
+  if constexpr (kApart) {
+    const u32x4 y[2] = {weights(0), weights(1)};
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b) {
+      const f32x16 o = T::mma32(read(kBlocks + b), y[1], T::mma32(read(b), y[0], f32x16{}));
+#pragma unroll
+      for (int i = 0; i < 16; ++i) st.o[b][i] += seen > 0 ? o[i] : 0.0f;
+    }
+    return;
+  }
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
-    const u32x4 y = {T::pack(w[8 * g], w[8 * g + 1]), T::pack(w[8 * g + 2], w[8 * g + 3]),
-                     T::pack(w[8 * g + 4], w[8 * g + 5]), T::pack(w[8 * g + 6], w[8 * g + 7])};
+    const u32x4 y = weights(g);
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b) {
       const int n = g * kBlocks + b;
@@ -622,25 +638,13 @@ struct Walk {
 // of up to 243 behind 9373, one head: 47 us, on one die 139; 8 of up to 600 behind 4000, four heads, 100 and 139).
 __host__ __device__ constexpr int dies_of(int heads) { return heads < 8 ? 8 / heads : 1; }
 
-template <class T, class S, bool kPacked>
-__global__ __launch_bounds__(S::kBlock, 2) void expand_shared_kernel(ExpandParams p) {
-  constexpr int kRows = S::kRows, kTile = S::kTile, kRing = S::kRing, kBuffer = S::kBuffer;
+// The sums of the queries q0 .. q1 - 1, the first of which are of request r, over part `split` of their keys.
+template <class T, class S, bool kPacked, bool kApart>
+__device__ __forceinline__ void attend_segments(const ExpandParams& p, State& st, char* tiles, int32_t q0, int32_t q1,
+                                                int32_t r, int head, int split, int wave, int lane) {
+  constexpr int kTile = S::kTile, kRing = S::kRing, kBuffer = S::kBuffer;
   constexpr int kAheadTiles = kRing - 1, kParts = kTile / kKeys;
-  __shared__ __attribute__((aligned(1024))) char tiles[kRing * kBuffer];
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 31, half = lane >> 5;
-
-  // Workgroup -> (head, queries), as above: those of one head are 8 apart. Less than 8 heads have several dies each.
-  const uint32_t id = blockIdx.x, slot = id % 8;
-  const int split = blockIdx.y, dies = dies_of(p.heads);
-  const int head = dies > 1 ? slot / dies : id / (8 * p.tiles) * 8 + slot;
-  const int index = dies > 1 ? id / 8 * dies + slot % dies : id / 8 % p.tiles;
-  if (head >= p.heads || index >= p.tiles) return;
-  const Tile tile = tile_of<S, kPacked>(p, p.tiles - 1 - index, tiles, tid, wave, lane);
-  const int32_t q0 = tile.q0, q1 = tile.q1;
-  if (q0 >= q1) return;
-  const int32_t r = max(tile.first, last_below(p.requests, q0, lane, [&](int32_t i) { return (int64_t)p.q_starts[i]; }));
   const int32_t w0 = q0 + wave * 32;
   const int32_t at = min(w0 + col, q1 - 1);
 
@@ -649,7 +653,6 @@ __global__ __launch_bounds__(S::kBlock, 2) void expand_shared_kernel(ExpandParam
 #pragma unroll
   for (int i = 0; i < kSteps; ++i) q[i] = load16(qh + (2 * i + half) * 16);
 
-  State st;
   st.top = -INFINITY;
   st.sum = 0.0f;
 #pragma unroll
@@ -709,7 +712,7 @@ __global__ __launch_bounds__(S::kBlock, 2) void expand_shared_kernel(ExpandParam
         if (j < top) {
           if (!have)
             s = scores_of<T, S>(cur, part, q, places, nullptr, 0.0f, 0.0f, nullptr, nullptr);
-          keys_step<T, S>(p, st, s, q, cur, part, tiles + (n + last) % kRing * kBuffer, last ? 0 : part + 1, to,
+          keys_step<T, S, kApart>(p, st, s, q, cur, part, tiles + (n + last) % kRing * kBuffer, last ? 0 : part + 1, to,
                           k, v, rope, more, copy.j, copy.at.len, sees - j, low >= j + kKeys, places, wave, lane);
         } else if (more) {
           copy_tile<S>(p, to, k, v, rope, copy.j, copy.at.len, places, wave, lane);
@@ -722,7 +725,49 @@ __global__ __launch_bounds__(S::kBlock, 2) void expand_shared_kernel(ExpandParam
       }
     }
   }
-  const int now = here(lane);
+}
+
+template <class T, class S, bool kPacked>
+__global__ __launch_bounds__(S::kBlock, 2) void expand_shared_kernel(ExpandParams p) {
+  __shared__ __attribute__((aligned(1024))) char tiles[S::kRing * S::kBuffer];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+
+  // Workgroup -> (head, queries), as above: those of one head are 8 apart. Less than 8 heads have several dies each.
+  const uint32_t id = blockIdx.x, slot = id % 8;
+  const int split = blockIdx.y, dies = dies_of(p.heads);
+  const int head = dies > 1 ? slot / dies : id / (8 * p.tiles) * 8 + slot;
+  const int index = dies > 1 ? id / 8 * dies + slot % dies : id / 8 % p.tiles;
+  if (head >= p.heads || index >= p.tiles) return;
+  const Tile tile = tile_of<S, kPacked>(p, p.tiles - 1 - index, tiles, tid, wave, lane);
+  const int32_t q0 = tile.q0, q1 = tile.q1;
+  if (q0 >= q1) return;
+  const int32_t r = max(tile.first, last_below(p.requests, q0, lane, [&](int32_t i) { return (int64_t)p.q_starts[i]; }));
+  State st;
+  attend_segments<T, S, kPacked, false>(p, st, tiles, q0, q1, r, head, split, wave, lane);
+  if (min(p.q_starts[r + 1], p.num_q) < q1) {
+    // Queries of several requests: infinite values or NaN of one request's keys have made NaN of them all, by
+    // weights of 0. If any result is not finite, all are computed once more, each of what it sees only. (The
+    // lane's number is asked for anew: the sums leave no register to keep it in.)
+    float odd = 0.0f;
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) odd = fmaf(st.o[b][i], 0.0f, odd);
+    int32_t* odds = reinterpret_cast<int32_t*>(tiles);
+    const bool mine = __any(odd != 0.0f);
+    __syncthreads();  // nobody reads the tiles any more
+    if (__lane_id() == 0) odds[wave] = mine;
+    __syncthreads();
+    int32_t any = 0;
+#pragma unroll
+    for (int w = 0; w < S::kWaves; ++w) any |= odds[w];
+    any = __builtin_amdgcn_readfirstlane(any);
+    __syncthreads();  // before the space is taken for tiles
+    if (any) attend_segments<T, S, kPacked, true>(p, st, tiles, q0, q1, r, head, split, wave, __lane_id());
+  }
+  const int32_t w0 = q0 + wave * 32;
+  const int now = here(__lane_id());
   if (w0 + (now & 31) < q1) put<T>(p, st, w0 + (now & 31), head, split, now >> 5);
 }
 
