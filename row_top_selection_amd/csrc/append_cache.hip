@@ -144,18 +144,20 @@ __device__ __forceinline__ float max_lanes(float x) {
 
 // Cosines and sines that lane `chunk` of a rotary part's 8 needs: of its four
 // pairs if they are neighbours, else of the eight that it has one side of.
-// Without a position, those that change nothing.
+// Without a position elements stay as they are (turned by nothing, one beside an infinite one
+// would be NaN).
 template <bool kNear>
 struct Turn {
   static constexpr int kN = kNear ? 4 : 8;
+  bool there;
   float cos[kN], sin[kN];
 
-  __device__ __forceinline__ Turn(const Tokens& t, int32_t position, int chunk) {
-    const bool there = position >= 0 && position < t.positions;
+  __device__ __forceinline__ Turn(const Tokens& t, int32_t position, int chunk)
+      : there(position >= 0 && position < t.positions) {
     const float* at = t.angles + (there ? position : 0) * t.angle_row + (kNear ? 4 * chunk : 8 * (chunk & 3));
 #pragma unroll
     for (int i = 0; i < kN; i += 4) {
-      f32x4 c = {1.0f, 1.0f, 1.0f, 1.0f}, s = {};
+      f32x4 c = {}, s = {};
       if (there) {
         c = *reinterpret_cast<const f32x4*>(at + i);
         s = *reinterpret_cast<const f32x4*>(at + kRope / 2 + i);
@@ -178,15 +180,15 @@ struct Turn {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float a = e.v[2 * i], b = e.v[2 * i + 1];
-        e.v[2 * i] = a * cos[i] - b * sin[i];
-        e.v[2 * i + 1] = a * sin[i] + b * cos[i];
+        e.v[2 * i] = there ? a * cos[i] - b * sin[i] : a;
+        e.v[2 * i + 1] = there ? a * sin[i] + b * cos[i] : b;
       }
     } else {
       // the other side of the pairs is four lanes away: mirrored in 8, then in 4
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float other = from_lane<kReverse4>(from_lane<kMirror8>(e.v[i]));
-        e.v[i] = e.v[i] * cos[i] + other * sin[i];
+        e.v[i] = there ? e.v[i] * cos[i] + other * sin[i] : e.v[i];
       }
     }
   }
