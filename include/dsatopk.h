@@ -574,6 +574,8 @@ int dsatopk_attend_paged(const void* q, int64_t q_row_stride, int64_t q_head_str
  *                 group_starts[g] .. group_starts[g + 1] - 1. The first entry is
  *                 taken as 0 and the last as num_rows, so that every row is in a
  *                 group. A group may be a single row, or empty.
+ *                 (Where they do not rise, results of the rows concerned mean
+ *                 nothing; no memory but the arguments' is touched.)
  *   shared_lens   int32 [num_groups]: positions 0 .. shared_lens[g] - 1 of a
  *                 group's rows are those of its first row's page table (what
  *                 other rows' tables have there is not looked at). Row b reads

@@ -519,8 +519,9 @@ __global__ __launch_bounds__(kSides * 64) void shared_join_kernel(SharedParams) 
   const int32_t shared = shared_of(p, g);
   int32_t n = 0, m = 0;  // shared parts, own parts
   int64_t first = 0, own = 0;
-  if (shared > 0) {
-    const int32_t start = start_of(p, g);
+  const int32_t start = start_of(p, g);
+  // (where starts do not rise a row may be before its group: no part is its own then)
+  if (shared > 0 && start <= row) {
     const int64_t i = x - (int64_t)start * p.heads;
     const int32_t* numbers = p.shared_numbers + (first_block(p, start, g) + i / p.lanes) * 2;
     n = parts_of(numbers, p.shared_most);
