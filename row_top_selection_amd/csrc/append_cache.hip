@@ -474,6 +474,12 @@ extern "C" int dsatopk_append_latent(
     int64_t q_head_stride, void* q_out, int64_t q_out_row_stride, int64_t q_out_head_stride,
     int32_t num_heads, void* stream) {
   LatentParams p{};
+  // what the call has no use for is not looked at
+  if (!out) out_stride = 0;
+  if (num_heads == 0) {
+    q_rope = q_out = nullptr;
+    q_row_stride = q_head_stride = q_out_row_stride = q_out_head_stride = 0;
+  }
   if ((latent_dim != 256 && latent_dim != 512) || num_heads < 0 || num_heads > 1024 ||
       bad_strides({latent_stride, out_stride, q_row_stride, q_head_stride, q_out_row_stride,
                    q_out_head_stride}))
@@ -527,6 +533,19 @@ extern "C" int dsatopk_append_index(
     void* stream) {
   IndexParams p{};
   const bool eight = index_type == DSATOPK_FP8;
+  // what the call has no use for is not looked at
+  if (num_heads == 0) {
+    q = q_out = nullptr;
+    q_row_stride = q_head_stride = q_out_row_stride = q_out_head_stride = 0;
+  }
+  if (!eight) {
+    key_scales = nullptr;
+    scale_page_stride = 0;
+  }
+  if (!eight || num_heads == 0) {
+    weights = weights_out = nullptr;
+    weight_stride = weight_out_stride = 0;
+  }
   if ((head_dim != 64 && head_dim != 128) || num_heads < 0 || num_heads > 128 ||
       (!eight && index_type != type) || (weight == nullptr) != (bias == nullptr) ||
       bad_strides({key_stride, scale_page_stride, q_row_stride, q_head_stride, q_out_row_stride,
