@@ -285,6 +285,8 @@ __device__ __forceinline__ void attend_wide(char* tiles, uint32_t (*masks)[Wide:
   int32_t t = first;
 #pragma unroll 1
   for (bool some = false;; some = true) {
+    // A segment: the tiles from here on that one reference holds for.
+    const int32_t begin = t;
     const int now = here(lane);
     const WidePlaces places(now);
     WideState st;
@@ -302,11 +304,11 @@ __device__ __forceinline__ void attend_wide(char* tiles, uint32_t (*masks)[Wide:
       {
         f32x16 s = wide_scores<T>(tiles + (t - first) % kRing * kBuffer, q, places);
         wide_mask(s, joined(valid_of(t - first)), mine - t * kTile, now);
-        // The reference is 2^kLift below the largest score; a head that sees none of the tokens needs none.
+        // The reference is 2^kLift below the largest score; a head that sees none of the segment's tokens needs none.
         float top = s[0];
 #pragma unroll
         for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
-        st.top = fmaxf(fmaxf(top, other_half(top)) * scale2 - T::kLift, mine <= first * kTile ? 0.0f : -INFINITY);
+        st.top = fmaxf(fmaxf(top, other_half(top)) * scale2 - T::kLift, mine <= begin * kTile ? 0.0f : -INFINITY);
 #pragma unroll
         for (int i = 0; i < 8; ++i) w.take<T>(s, i, scale2, st.top == -INFINITY ? 0.0f : st.top);
       }
@@ -334,7 +336,7 @@ __device__ __forceinline__ void attend_wide(char* tiles, uint32_t (*masks)[Wide:
       // what is done with the sums next is no reason to have them elsewhere in the loop
 #pragma unroll
       for (int b = 0; b < Wide::kBlocks; ++b) asm volatile("" : "+a"(st.o[b]));
-      if (mine <= first * kTile) st.top = -INFINITY;
+      if (mine <= begin * kTile) st.top = -INFINITY;
     } else {
       st.top = -INFINITY;
     }

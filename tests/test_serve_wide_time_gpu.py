@@ -1,0 +1,56 @@
+"""Attention behind shared tokens, 128 heads a workgroup: rows that end early cost
+nothing once a reference has been outgrown."""
+import math
+
+import pytest
+import torch
+
+from tests.test_serve_attend_gpu import SCALE, TYPES, i32
+
+pytestmark = pytest.mark.gpu
+
+
+def microseconds(call):
+    """The median of five times a call, among others."""
+    begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    for _ in range(3):
+        call()
+    times = []
+    for _ in range(5):
+        begin.record()
+        for _ in range(10):
+            call()
+        end.record()
+        torch.cuda.synchronize()
+        times.append(begin.elapsed_time(end) * 100)
+    return sorted(times)[2]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+def test_rows_that_end_before_a_new_reference(kind):
+    """Scores grow by 20 at token 128 of 1024. Every second row ends before that, in the same waves as those
+    that see all: less work than if all see all, and no other result for these."""
+    import row_top_selection_amd as dt
+
+    g = torch.Generator("cuda").manual_seed(1)
+    rows, shared, page = 2048, 1024, 64
+    cache = torch.randn(shared // page, page, 576, generator=g, device="cuda")
+    cache.view(-1, 576)[:, 512] = torch.arange(shared, device="cuda") >= 128
+    q = 0.1 * torch.randn(rows, 16, 576, generator=g, device="cuda")
+    q[..., 512] = 20 / SCALE
+    cache, q = cache.to(TYPES[kind]), q.to(TYPES[kind])
+    table = torch.arange(shared // page, device="cuda", dtype=torch.int32).expand(rows, -1).contiguous()
+    whole = torch.full((rows,), shared, dtype=torch.int32, device="cuda")
+    uneven = whole.clone()
+    uneven[::2] = 40
+
+    def call(lens):
+        return dt.attend_shared(q, cache, lens, table, i32_starts, i32_shared, 512, SCALE, max_shared_len=shared, max_own_len=0)
+
+    i32_starts, i32_shared = i32([0, rows]), i32([shared])
+    (out, lse), (want, want_lse) = call(uneven), call(whole)
+    torch.cuda.synchronize()
+    assert torch.isfinite(out).all() and not math.isinf(float(lse.min()))
+    assert torch.equal(out[1::2], want[1::2]) and torch.equal(lse[1::2], want_lse[1::2])
+    of_uneven, of_whole = microseconds(lambda: call(uneven)), microseconds(lambda: call(whole))
+    assert of_uneven < 1.5 * of_whole, (of_uneven, of_whole)
