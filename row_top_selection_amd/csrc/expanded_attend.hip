@@ -225,7 +225,8 @@ __device__ __forceinline__ void keys_step(const ExpandParams& p, State& st, f32x
   }
   // The weights are taken by the reference in use, which only has to
   // be near enough: a lane's sum over kMost (or not a number) tells that it
-  // is not, and the scores' maximum is looked for.
+  // is not, and the scores' maximum is looked for. A query that sees none of
+  // these keys needs no reference for them.
   f32x16 w;
   float sum = 0.0f;
   const f32x16 next = scores_of<T, S>(after, after_part, q, places, &s, p.scale2,
@@ -247,7 +248,7 @@ __device__ __forceinline__ void keys_step(const ExpandParams& p, State& st, f32x
 #pragma unroll
     for (int n = 0; n < kAhead; ++n) a[n] = read(n);
   }
-  if (__any(!(sum <= T::kMost) || st.top == -INFINITY)) {
+  if (__any(!(sum <= T::kMost) || (st.top == -INFINITY && seen > 0))) {
     float top = s[0];
 #pragma unroll
     for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
