@@ -227,6 +227,7 @@ __device__ __forceinline__ void keys_step(const ExpandParams& p, State& st, f32x
   // be near enough: a lane's sum over kMost (or not a number) tells that it
   // is not, and the scores' maximum is looked for. A query that sees none of
   // these keys needs no reference for them.
+  const bool wants = st.top == -INFINITY && seen > 0;
   f32x16 w;
   float sum = 0.0f;
   const f32x16 next = scores_of<T, S>(after, after_part, q, places, &s, p.scale2,
@@ -248,7 +249,7 @@ __device__ __forceinline__ void keys_step(const ExpandParams& p, State& st, f32x
 #pragma unroll
     for (int n = 0; n < kAhead; ++n) a[n] = read(n);
   }
-  if (__any(!(sum <= T::kMost) || (st.top == -INFINITY && seen > 0))) {
+  if (__any(!(sum <= T::kMost) || wants)) {
     float top = s[0];
 #pragma unroll
     for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
@@ -728,6 +729,18 @@ __device__ __forceinline__ void attend_segments(const ExpandParams& p, State& st
   }
 }
 
+// Uniform values, and the arguments as they are in memory, from which what follows is computed anew: nothing of it is kept
+// from before, in registers that a loop in between is short of.
+__device__ __forceinline__ int32_t anew(int32_t x) {
+  asm volatile("" : "+s"(x));
+  return x;
+}
+__device__ __forceinline__ const ExpandParams& params_anew() {
+  auto* p = (const __attribute__((address_space(4))) ExpandParams*)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return *(const ExpandParams*)p;
+}
+
 template <class T, class S, bool kPacked>
 __global__ __launch_bounds__(S::kBlock, 2) void expand_shared_kernel(ExpandParams p) {
   __shared__ __attribute__((aligned(1024))) char tiles[S::kRing * S::kBuffer];
@@ -765,7 +778,9 @@ __global__ __launch_bounds__(S::kBlock, 2) void expand_shared_kernel(ExpandParam
     for (int w = 0; w < S::kWaves; ++w) any |= odds[w];
     any = __builtin_amdgcn_readfirstlane(any);
     __syncthreads();  // before the space is taken for tiles
-    if (any) attend_segments<T, S, kPacked, true>(p, st, tiles, q0, q1, r, head, split, wave, __lane_id());
+    if (any)
+      attend_segments<T, S, kPacked, true>(params_anew(), st, tiles, anew(q0), anew(q1), anew(r), anew(head), anew(split),
+                                           wave, __lane_id());
   }
   const int32_t w0 = q0 + wave * 32;
   const int now = here(__lane_id());
