@@ -34,6 +34,7 @@
 // tokens: a chain of loads). 33 groups of 4 drafts behind 2500 ... 5000 tokens: 70 us,
 // where reading the tokens takes 23.
 
+#include <cstddef>
 #include <type_traits>
 
 #include "wide_tiles.h"
@@ -411,8 +412,9 @@ __global__ __launch_bounds__(PS::kBlock, (std::is_same_v<PS, Wide> ? 1 : 2)) voi
     int64_t sums[kWaves];
     float joined[2][kWaves][16];
     int32_t kept[kStarts];
-    uint32_t masks[Wide::kRing][kWaves];
+    alignas(16) uint32_t masks[Wide::kRing][kWaves];  // (read 16 bytes at a time)
   };
+  static_assert(kSpace % 16 == 0 && offsetof(Rest, masks) % 16 == 0, "masks are aligned as they are read");
   __shared__ __attribute__((aligned(1024))) char tiles[kSpace + sizeof(Rest)];
   Rest& rest = *reinterpret_cast<Rest*>(tiles + kSpace);
   auto& job = rest.job;
