@@ -326,8 +326,8 @@ __device__ __forceinline__ void attend_job(const Job& job, char* tiles, uint32_t
     clear<P>(st);
     {
       const int32_t i = wave % P::kWH * 16 + (lane & 15);
-      // a lane that sees nothing of these tokens must not ask for a reference at every tile
-      if (!kOwn && mine(i) <= first * P::kTile) st.top = 0.0f;
+      // a lane that sees none of the wave's tokens must not ask for a reference at every tile
+      if (!kOwn && mine(i) <= first * P::kTile + wave / P::kWH * P::kTokens) st.top = 0.0f;
       Args& p = args();
       const Places<P> places(wave, lane);
       attend_range<T, P, true, !kOwn>(st, tiles, masks, cache_of(p), pages_of(p, uniform(job.row0)), base, len,
@@ -335,7 +335,7 @@ __device__ __forceinline__ void attend_job(const Job& job, char* tiles, uint32_t
     }
     const int32_t now = here(lane), i = wave % P::kWH * 16 + (now & 15);
     float sum = head_sum(st.sum);
-    float top = !kOwn && mine(i) <= job.first * kTile ? -INFINITY : st.top;
+    float top = !kOwn && mine(i) <= job.first * kTile + wave / P::kWH * P::kTokens ? -INFINITY : st.top;
     if constexpr (P::kWT > 1) join_groups<P>(st, top, sum, tiles, joined, wave, now);
     const Block block(args(), job, kLanes);
     if (wave / P::kWH == 0 && i < block.count)
