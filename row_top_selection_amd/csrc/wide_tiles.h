@@ -317,8 +317,9 @@ __device__ __forceinline__ void attend_wide(char* tiles, uint32_t (*masks)[Wide:
       bool again = true;
 #pragma unroll 1
       for (; t < last; ++t) {
-        // a head without a reference has to get one, weights that have outgrown it another
-        if (!again && __any(!(w.sum <= T::kMost) || st.top == -INFINITY)) break;
+        // a head without a reference has to get one, weights that have outgrown it another (no other one helps
+        // a sum that is no number)
+        if (!again && __any((!(w.sum <= T::kMost) || st.top == -INFINITY) && st.sum == st.sum)) break;
         again = false;
         st.sum += w.sum;
         const int n = t - first;

@@ -54,3 +54,29 @@ def test_rows_that_end_before_a_new_reference(kind):
     assert torch.equal(out[1::2], want[1::2]) and torch.equal(lse[1::2], want_lse[1::2])
     of_uneven, of_whole = microseconds(lambda: call(uneven)), microseconds(lambda: call(whole))
     assert of_uneven < 1.5 * of_whole, (of_uneven, of_whole)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+def test_a_row_that_is_no_number(kind):
+    """The queries of one row in eight are NaN: the others get what they get without them, in the same time."""
+    import row_top_selection_amd as dt
+
+    g = torch.Generator("cuda").manual_seed(2)
+    rows, shared, page = 2048, 1024, 64
+    cache = torch.randn(shared // page, page, 576, generator=g, device="cuda").to(TYPES[kind])
+    q = (0.1 * torch.randn(rows, 16, 576, generator=g, device="cuda")).to(TYPES[kind])  # (references hold for all tokens)
+    odd = q.clone()
+    odd[::8] = math.nan
+    table = torch.arange(shared // page, device="cuda", dtype=torch.int32).expand(rows, -1).contiguous()
+    at = (i32([shared] * rows), table, i32([0, rows]), i32([shared]), 512, SCALE)
+
+    def call(queries):
+        return dt.attend_shared(queries, cache, *at, max_shared_len=shared, max_own_len=0)
+
+    (out, lse), (want, want_lse) = call(odd), call(q)
+    torch.cuda.synchronize()
+    numbers = torch.arange(rows, device="cuda") % 8 != 0
+    assert torch.equal(out[numbers], want[numbers]) and torch.equal(lse[numbers], want_lse[numbers])
+    assert torch.isnan(out[~numbers]).all() and torch.isnan(lse[~numbers]).all()
+    of_odd, of_all = microseconds(lambda: call(odd)), microseconds(lambda: call(q))
+    assert of_odd < 1.5 * of_all, (of_odd, of_all)
