@@ -180,49 +180,32 @@ __device__ __forceinline__ void put_part(Args& p, const State<P>& st, float top,
 }
 
 // The same for 32 heads a wave, where register i of block b holds element 32 * b + 8 * (i / 4) + 4 *
-// (lane / 32) + i % 4. `more`: the sums go on by another reference, and these are put to their place until then;
-// `some`: some have been put there before.
+// (lane / 32) + i % 4.
 template <class T>
-__device__ __forceinline__ void put_wide(Args& p, WideState& st, bool more, bool some, bool whole, int64_t row,
-                                         int32_t head, const Slot& to, int lane) {
+__device__ __forceinline__ void put_wide(Args& p, const WideState& st, bool whole, int64_t row, int32_t head,
+                                         const Slot& to, int lane) {
   const int half = lane >> 5;
-  float top = st.top, sum = st.sum, by = 1.0f, before = 0.0f;
-  float* part = to.part + half * to.step;
-  bool kept = false;
-  if (some) {
-    const float x = to.state[0], n = to.state[1];
-    kept = !(x == -INFINITY && n == 0.0f);
-    const float ref = fmaxf(x, top);
-    before = kept ? exp2_fast(x - (ref == -INFINITY ? 0.0f : ref)) : 0.0f;
-    by = top == -INFINITY ? 0.0f : exp2_fast(top - ref);
-    sum = sum * by + n * before;
-    top = ref;
-  }
-  const bool result = whole && !more;
-  if (result) by *= sum == 0.0f ? 0.0f : 1.0f / sum, before *= sum == 0.0f ? 0.0f : 1.0f / sum;
+  const float by = !whole ? 1.0f : st.sum == 0.0f ? 0.0f : 1.0f / st.sum;
   char* out = p.out + ((row * p.heads + head) * Wide::kLatent + 4 * half) * 2;
-  if (result) {
-    if (p.lse && half == 0) p.lse[row * p.heads + head] = (top + log2f(sum)) * kLn2;
+  float* part = to.part + half * to.step;
+  if (whole) {
+    if (p.lse && half == 0) p.lse[row * p.heads + head] = (st.top + log2f(st.sum)) * kLn2;
   } else {
-    // (both halves have read the state before one writes it)
     if (half == 0) {
-      to.state[0] = top;
-      to.state[1] = sum;
+      to.state[0] = st.top;
+      to.state[1] = st.sum;
     }
-    if (top == -INFINITY && sum == 0.0f) return;  // nothing seen: the join skips it
+    if (st.top == -INFINITY && st.sum == 0.0f) return;  // nothing seen: the join skips it
   }
 #pragma unroll
   for (int b = 0; b < Wide::kBlocks; ++b)
 #pragma unroll
     for (int i = 0; i < 16; i += 4) {
-      f32x4 v = {st.o[b][i], st.o[b][i + 1], st.o[b][i + 2], st.o[b][i + 3]};
-      float* at = part + (8 * b + i / 2) * to.step;
-      v *= by;
-      if (kept) v += *reinterpret_cast<const f32x4*>(at) * before;
-      if (result)
+      const f32x4 v = f32x4{st.o[b][i], st.o[b][i + 1], st.o[b][i + 2], st.o[b][i + 3]} * by;
+      if (whole)
         *reinterpret_cast<u32x2*>(out + (b * 32 + 2 * i) * 2) = u32x2{T::pack(v[0], v[1]), T::pack(v[2], v[3])};
       else
-        *reinterpret_cast<f32x4*>(at) = v;
+        *reinterpret_cast<f32x4*>(part + (8 * b + i / 2) * to.step) = v;
     }
 }
 
@@ -309,11 +292,11 @@ __device__ __forceinline__ void attend_job(const Job& job, char* tiles, uint32_t
     return i < block.count ? block.sees(i) : INT32_MAX;
   };
   if constexpr (std::is_same_v<P, Wide>) {
-    auto done = [&](WideState& st, bool more, bool some) {
+    auto done = [&](const WideState& st) {
       const Block block(args(), job, kLanes);
       const int32_t now = here(lane), i = wave * 32 + now % 32;
       if (i < block.count)
-        put_wide<T>(block.p, st, more, some, job.whole && block.alone(i), block.row_of(i), block.head_of(i),
+        put_wide<T>(block.p, st, job.whole && block.alone(i), block.row_of(i), block.head_of(i),
                     block.slot<P>(job, i), now);
     };
     Args& p = args();

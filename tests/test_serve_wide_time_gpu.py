@@ -80,3 +80,25 @@ def test_a_row_that_is_no_number(kind):
     assert torch.isnan(out[~numbers]).all() and torch.isnan(lse[~numbers]).all()
     of_odd, of_all = microseconds(lambda: call(odd)), microseconds(lambda: call(q))
     assert of_odd < 1.5 * of_all, (of_odd, of_all)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("spread", [1.7, 3.5, 7.0])
+def test_scores_that_spread_far(kind, spread):
+    """Random scores that spread by 1.7 to 7 outgrow references again and again. Whatever that costs, it is less
+    than the call took with scores that never do."""
+    import row_top_selection_amd as dt
+
+    g = torch.Generator("cuda").manual_seed(3)
+    rows, shared, page = 64, 16384, 64
+    cache = torch.randn(shared // page, page, 576, generator=g, device="cuda").to(TYPES[kind])
+    q = torch.randn(rows, 16, 576, generator=g, device="cuda") / (SCALE * 24)  # scores of size 1
+    table = torch.arange(shared // page, device="cuda", dtype=torch.int32).expand(rows, -1).contiguous()
+    at = (i32([shared] * rows), table, i32([0, rows]), i32([shared]), 512, SCALE)
+
+    def call(queries):
+        return dt.attend_shared(queries, cache, *at, max_shared_len=shared, max_own_len=0)
+
+    near, far = (0.4 * q).to(TYPES[kind]), (spread * q).to(TYPES[kind])
+    of_near, of_far = microseconds(lambda: call(near)), microseconds(lambda: call(far))
+    assert of_far < 2 * of_near, (of_far, of_near)
