@@ -361,8 +361,9 @@ def expanded_shared_bytes(num_heads: int, num_queries: int, max_keys: int) -> in
 
 
 # The serving operators' calls (csrc/serve_binding.cpp), loaded at first use.
-_SERVE = ("page_maps", "append_latent", "append_index", "scores_paged", "scores_ragged", "attend_selected", "attend_paged",
-          "attend_shared", "attend_expanded", "attend_expanded_shared")
+_SERVE = ("page_maps", "append_latent", "append_index", "scores_paged", "scores_ragged",
+          "attend_selected", "attend_paged", "attend_shared", "attend_expanded",
+          "attend_expanded_shared")
 
 
 def __getattr__(name):

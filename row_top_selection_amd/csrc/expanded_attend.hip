@@ -17,9 +17,9 @@
 // registers, which are, rounded, the B operand of O' = V' P'; V's columns
 // come from LDS column reads. Queries stay in registers throughout.
 //
-// The scores of 32 keys are computed beside the softmax of the 32 before
-// them, one product between every few other instructions, so that the matrix
-// units work while exponentials are taken.
+// A wave takes the softmax of 32 keys between the reads for the scores of the
+// next 32 and their products. Two waves a SIMD fill each other's pauses, one's
+// products beside the other's exponentials.
 //
 // Few rows of many keys are split over workgroups by keys; a second kernel
 // joins the parts.
@@ -36,7 +36,7 @@
 // falls with what the matrix units switch: the same call on zeros takes 530
 // us.
 //
-// 16 x 512 queries that share 16384 keys, 16 heads: 1250 ... 1300 us by card, 1.1 PFLOP/s.
+// 16 x 512 queries that share 16384 keys, 16 heads: 1250 ... 1320 us by card, 1.1 PFLOP/s.
 //
 // Weights are rounded to the inputs' type for the second product (off by at
 // most 2^-8 of each in bfloat16; in half precision by 2^-11 of each or 2^-35
@@ -164,11 +164,12 @@ __device__ __forceinline__ float weight_of(const f32x16& s, int i, float scale2,
   return exp2_fast(fmaf(s[i], scale2, -ref));
 }
 
-// The scores of the 32 keys `part` of a tile for the wave's 32 queries, and beside them
-// the weights of `s` (if there is one), a few after each product. Reads go
-// kAhead steps before their products. The order is kept as written: left
-// alone, the compiler puts each read right before its product, waits for it
-// there, and takes the weights after all products.
+// The scores of the 32 keys `part` of a tile for the wave's 32 queries, and with them
+// the weights of `s` (if there is one). Reads are issued at least kAhead steps before
+// their products: left alone, the compiler puts each read right before its product,
+// waits for it there, and takes the weights after all products. Written as here, a few
+// weights behind each product, it issues all reads and takes the weights first, and
+// the products run through behind them.
 template <class T, class S>
 __device__ __forceinline__ f32x16 scores_of(const char* tile, int part, const u32x4 (&q)[kSteps],
                                             const Places<S>& places, const f32x16* s, float scale2,

@@ -154,8 +154,9 @@ __device__ __forceinline__ void attend_tokens(State<P>& st, const u32x4 (&q)[P::
     const char* ropes = cur + from * kRopeBytes;
 #pragma unroll
     for (int x = 0; x < kGo; ++x) s[x] = f32x4{};
-    // Reads go kAhead steps before the products that take them, and no
-    // further: registers are what a wave has least of.
+    // Reads are issued kAhead steps before the products that take them, and no
+    // further: registers are what a wave has least of. (While the next tile's copies
+    // are under way they are waited for together, every few products: copy_to_lds.)
     constexpr int kAhead = 3, kAll = P::kSteps + P::kRopeSteps;
     auto read = [&](int i, int x) {
       if (i < P::kSteps)

@@ -28,7 +28,8 @@ using global_u32 = const __attribute__((address_space(1))) uint32_t;
 
 // How attention scales its softmax's weights before it rounds them to a 16-bit
 // type: by a reference 2^kLift below a maximum of the row's scores, which is
-// kept until a lane's weights add up to more than kMost. bfloat16 has fp32's
+// kept until a lane's weights add up to more than kMost (in wide_tiles.h, to more
+// than a bound of its own). bfloat16 has fp32's
 // exponents, so that every weight is off by at most 2^-8 of itself wherever
 // it lies. Half precision ends 14 (with fewer bits: 24) binary orders below 1
 // and 16 above: weights up to kMost, its largest number, stay finite, and one is
@@ -97,7 +98,9 @@ struct Fp16 {
 
 // 16 bytes a lane from memory straight into LDS: lane l's bytes go to
 // lds + 16 * l (lds is the wave's, the global address each lane's own).
-// Completion is counted with the vector loads (wait_copies).
+// Completion is counted with the vector loads (wait_copies). The compiler takes
+// it for an access of LDS as well: while one is under way, each of its waits for
+// an LDS read is a wait for all that have been issued.
 __device__ __forceinline__ void copy_to_lds(const void* global, char* lds) {
   __builtin_amdgcn_global_load_lds((global_u32*)(uintptr_t)global, (lds_u32*)lds, 16, 0, 0);
 }

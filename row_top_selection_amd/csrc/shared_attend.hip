@@ -19,20 +19,27 @@
 // have a loop of their own (wide_tiles.h): in four waves, where those of 256 take eight.
 //
 // How many tokens there are of which kind only the device knows. Each workgroup
-// adds up the tiles of all blocks (a few thousand lengths at most, from L2) and
+// adds up the tiles of all blocks and
 // takes its equal share of them, in their order: the end of one block,
 // blocks as a whole, the beginning of the last one. So the card is full from
 // the first to the last tile whatever the lengths are, and a block has as
 // many parts as workgroups worked on it. What one workgroup did alone it
 // writes as the result.
 //
-// 64 rows of 16 heads behind 262144 tokens take 635 us, 920 TFLOP/s (a large
+// 64 rows of 16 heads behind 262144 tokens take 620 ... 645 us, 920 TFLOP/s (a large
 // library product reaches 1370): the matrix units are busy two fifths of the
-// time, in turn with LDS, of whose bandwidth the tiles' reads take as much. What
+// time, and the reads of LDS, which would fit beside them, are waited for
+// (wide_tiles.h). What
 // comes on top for shorter work is the parts: 256 workgroups of 128 heads write
 // and read 64 MB, 25 us; and 12 us until the first tile is there (share, pages,
 // tokens: a chain of loads). 33 groups of 4 drafts behind 2500 ... 5000 tokens: 70 us,
-// where reading the tokens takes 23.
+// where reading the tokens takes 23. Every workgroup looks at all groups and rows:
+// 20 us for each thousand groups (1000 of one empty row 25 us, 10000 222), 9 for each
+// thousand rows of one group (10000: 90 us).
+//
+// Where little is shared dsatopk_attend_paged, which reads the shared tokens for every row, is
+// faster, by 4 to 10 us: up to about 300000 rows times shared tokens of 16 heads (4 rows
+// behind 65536 48 and 47 us, 64 behind 4096 48 and 42, 32 behind 16384 58 and 83).
 
 #include <cstddef>
 #include <type_traits>
@@ -603,9 +610,10 @@ struct Cut {
     lanes = each <= 32 ? 32 : each <= 64 ? 64 : 128;
     // 64 lanes, two workgroups a CU, also for larger groups, where their tiles are few for each workgroup or
     // most are single rows' of few heads, which leave waves of 32 heads idle. Measured with 64 and with
-    // 128 (us), 16 heads: 8 rows behind 2048 tokens 30 and 38, 32 behind 4096 40 and 43, behind 16384 and
-    // 1000 own ones 61 and 61, 64 behind 16384 83 and 76; 128 rows of 2000 own tokens 73 and 97; but 256 rows
-    // of 256, 128 heads, 126 and 117.
+    // 128 (us), 16 heads: 8 rows behind 2048 tokens and 200 own ones 26 and 33, 32 behind 4096 38 and 39, behind
+    // 16384 and 1000 own ones 59 and 59, 64 behind 16384 83 and 74, behind 65536 220 and 173; 128 rows of 2000 own
+    // tokens 73 and 97. With vectors of 256, in the same order: 22 and 24, 30 and 31, 40 and 41, 51 and 49, 122 and
+    // 109; 22 rows of 128 heads behind 32768 159 and 141; but 64 of 16 behind 16384 and 1000 own ones 54 and 58.
     const double shared_tiles = (double)((max_shared + kTile - 1) / kTile) * (double)((int64_t)rows * heads / 64 + groups);
     const double own_tiles = owns ? (double)((max_own + kTile - 1) / kTile) * rows * ((heads + 63) / 64) : 0.0;
     if (lanes == 128 && (shared_tiles + own_tiles <= 8.0 * kPlaces || (heads <= 64 && own_tiles >= 4.0 * shared_tiles)))

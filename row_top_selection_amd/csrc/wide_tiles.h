@@ -5,13 +5,17 @@
 // instructions of 32 x 32: a vector that is read from LDS feeds twice as many
 // products as with 16 heads a wave. The sums of 32 heads (256 registers) and
 // their queries (144) leave room for one wave a SIMD, which has to be kept busy by
-// itself: the scores of the next 32 tokens are computed beside the softmax of
-// the current ones, and reads go several products ahead.
+// itself: the scores of the next 32 tokens are computed before the sums of the
+// current ones, and reads are issued up to eight products ahead.
 //
 // A tile of 32 tokens takes a wave 68 products of 32 cycles, 2176, and the four
-// waves' reads of it 272 KB, 2125 cycles of LDS; it is done in 2.35 us. With 16
+// waves' reads of it (278528 bytes) as many cycles of LDS; it is done in 2.35 us,
+// about 5600. Between these lie the waits: with copies under way (copy_to_lds) all
+// reads are waited for at every eighth product, the last of which has only been
+// issued, nine times a tile; and the compiler takes all weights behind the last
+// product, not between them. With 16
 // heads a wave and eight waves (twice the reads) 64 rows of 16 heads behind 262144
-// tokens take 748 us, with these 638; behind 16384, up to 1000 own ones, 87 and 79.
+// tokens take 748 us, with these 620 ... 645; behind 16384, up to 1000 own ones, 87 and 79.
 #ifndef DSATOPK_WIDE_TILES_H_
 #define DSATOPK_WIDE_TILES_H_
 
@@ -32,7 +36,7 @@ struct Wide {
   static constexpr int kBlocks = kLatent / 32;
   // What a lane's weights of a tile may add up to before they need another reference, which costs 2.7 us here, a
   // tile 2.35. bfloat16's weights are as exact far from theirs as near it: up to 2^24 (sums stay finite for values up
-  // to 2^80). 64 rows of 16 heads behind 16384 tokens, up to 1000 own ones, with scores that spread by 0.9 / 1.7 /
+  // to 2^80). 64 rows of 16 heads behind 16384 tokens and 1000 own ones with scores that spread by 0.9 / 1.7 /
   // 3.5 / 6.9: 85 / 86 / 86 / 96 us, in half precision 86 / 96 / 131 / 147 (64 heads a workgroup 101 ... 106).
   template <class T>
   static constexpr float most() {
@@ -194,11 +198,12 @@ struct Weights {
 };
 
 // One tile, `cur`, the weights of which are there: a copy of a later one, the scores of the one after it, and the
-// sums, beside which those scores become weights. The tiles are told apart so that no read of one
+// sums, and those scores become weights. The tiles are told apart so that no read of one
 // waits for the copies of another. `valid`, `seen`: as for wide_mask, of the tile after it.
-// One wave a SIMD has nobody to fill its pauses: reads go kAhead products ahead, also from the scores into the
-// sums, and the copy's addresses and instructions stand between the scores' products. The order is kept as
-// written.
+// One wave a SIMD has nobody to fill its pauses: reads are issued kAhead products ahead, also from the scores into
+// the sums, and the copy's addresses and instructions stand between the scores' products. That order holds, but the
+// reads are waited for all at once, every kAhead products (copy_to_lds); and the weights, written between the sums'
+// products, end up behind them.
 template <class T>
 __device__ __forceinline__ void wide_step(f32x16 (&o)[Wide::kBlocks], Weights& w, const u32x4 (&q)[Wide::kAll],
                                           const char* __restrict__ cur, const char* __restrict__ after,
