@@ -5,7 +5,7 @@ import pytest
 
 from tests.test_serve_attend_gpu import SCALE, i32
 from tests.test_serve_behind_gpu import inputs
-from tests.test_serve_wide_time_gpu import microseconds
+from tests.test_serve_wide_time_gpu import times
 
 import torch
 
@@ -17,7 +17,7 @@ pytestmark = pytest.mark.gpu
 def test_one_shared_key_less(kind, heads, new, own):
     """Without any shared keys, queries of later requests have seen nothing yet while a tile goes over those of
     the first ones; with one shared key in front all have. The latter is more work, and the former has to take
-    no more time than it (and a tenth of it, for what a measurement is off by)."""
+    no more time than it (and 7%, for what a measurement is off by; looking for references took 14 to 20)."""
     import row_top_selection_amd as dt
 
     g = torch.Generator("cuda").manual_seed(1)
@@ -30,5 +30,5 @@ def test_one_shared_key_less(kind, heads, new, own):
     def call(lens):
         return dt.attend_expanded_shared(q, k, v, rope, starts, k_starts, zero, lens, SCALE, max_keys=0)
 
-    without, with_one = microseconds(lambda: call(none)), microseconds(lambda: call(one))
-    assert without < 1.1 * with_one, (without, with_one)
+    without, with_one = times(lambda: call(none), lambda: call(one))
+    assert without < 1.07 * with_one, (without, with_one)

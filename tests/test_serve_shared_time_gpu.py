@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from tests.test_serve_attend_gpu import SCALE, TYPES, i32
-from tests.test_serve_wide_time_gpu import microseconds
+from tests.test_serve_wide_time_gpu import times
 
 pytestmark = pytest.mark.gpu
 
@@ -12,7 +12,7 @@ pytestmark = pytest.mark.gpu
 @pytest.mark.parametrize("kind", ["bf16", "fp16"])
 def test_rows_that_end_in_the_first_tile(kind):
     """Groups of two rows, of which one ends after 5 tokens of 2048: no other result for the other one, and no
-    more time than if both see all (but for the hiding of what the short one does not see)."""
+    more time than if both see all."""
     import row_top_selection_amd as dt
 
     g = torch.Generator("cuda").manual_seed(1)
@@ -36,6 +36,6 @@ def test_rows_that_end_in_the_first_tile(kind):
     assert torch.equal(out[::2], want[::2]) and torch.equal(lse[::2], want_lse[::2])
     assert ((out[1::2].float() - short[1::2].float()).abs() <= 4 * torch.finfo(TYPES[kind]).eps * size).all()
     assert ((lse[1::2] - short_lse[1::2]).abs() <= 1e-4).all()
-    of_uneven, of_whole = microseconds(lambda: call(uneven)), microseconds(lambda: call(whole))
-    # hiding the tokens that a row does not see is 3 to 6% of a tile; looking for references was 17
-    assert of_uneven < 1.12 * of_whole, (of_uneven, of_whole)
+    of_uneven, of_whole = times(lambda: call(uneven), lambda: call(whole))
+    # looking for references takes 12% of a tile
+    assert of_uneven < 1.07 * of_whole, (of_uneven, of_whole)
