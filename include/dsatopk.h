@@ -370,7 +370,8 @@ int dsatopk_page_maps(const int32_t* seq_lens, const int32_t* new_lens, int32_t 
  *                 page_stride, token_stride, as dsatopk_attend_paged reads it.
  *   out           type [num_tokens, latent_dim + rope_dim] or NULL: also
  *                 receives y, of every token (for a prompt's keys and values).
- *                 May be latent itself.
+ *                 May be latent itself (with its stride), and must not overlap
+ *                 it otherwise.
  *   q_rope        type [num_tokens, num_heads, rope_dim], the rotary parts of
  *                 the queries, strides q_row_stride, q_head_stride;
  *   q_out         type, of the same shape, receives them turned. May be q_rope

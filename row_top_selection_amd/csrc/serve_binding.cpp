@@ -17,6 +17,7 @@
 #include <exception>
 #include <initializer_list>
 #include <string>
+#include <utility>
 
 #include "dsatopk.h"
 
@@ -346,11 +347,21 @@ at::Tensor result_like(const On& on, PyObject* o, const at::Tensor& x, at::Scala
   return t;
 }
 
-// A written tensor's rows must not share memory.
+// A written tensor's rows must not share memory: from the closest ones on, every
+// dimension steps over all of those inside it.
 void apart(const at::Tensor& t, const char* name) {
-  for (int64_t d = 0; d + 1 < t.dim(); ++d)
-    if (t.size(d) > 1 && t.stride(d) < t.size(t.dim() - 1))
-      refuse(std::string(name) + " must not be expanded: it is written");
+  if (!t.numel()) return;
+  std::pair<int64_t, int64_t> outer[2];  // strides and sizes of the others than the last
+  int n = 0;
+  for (int64_t d = 0; d + 1 < t.dim() && n < 2; ++d)
+    if (t.size(d) > 1) outer[n++] = {t.stride(d), t.size(d)};
+  std::sort(outer, outer + n);
+  int64_t extent = t.size(t.dim() - 1);
+  for (int i = 0; i < n; ++i) {
+    if (outer[i].first < extent)
+      refuse(std::string(name) + " must not be expanded, nor its rows overlap: it is written");
+    extent += outer[i].first * (outer[i].second - 1);
+  }
 }
 
 PyObject* append_latent(PyObject* const* args, Py_ssize_t n, PyObject* kw) {
