@@ -600,8 +600,9 @@ int dsatopk_attend_paged(const void* q, int64_t q_row_stride, int64_t q_head_str
  * The other arguments are those of dsatopk_attend_paged, as are the rounding
  * and the errors. A shared position that some but not all rows of its group see
  * has to hold finite values (its weight is 0 in the others, which infinities
- * and NaN turn into NaN); what no row sees may hold anything. num_groups 0 is
- * refused unless num_rows is 0.
+ * and NaN turn into NaN; rows that see nothing at all get zeros all the same);
+ * what no row sees may hold anything. num_groups 0 is refused unless num_rows
+ * is 0.
  */
 size_t dsatopk_shared_bytes(int32_t num_rows, int32_t num_heads, int32_t latent_dim,
                             int32_t num_groups, int64_t max_shared_len, int64_t max_own_len);

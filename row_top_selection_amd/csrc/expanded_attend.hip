@@ -318,15 +318,17 @@ __device__ __forceinline__ void put(const ExpandParams& p, const State& st, int6
             f32x4{st.o[b][i], st.o[b][i + 1], st.o[b][i + 2], st.o[b][i + 3]};
     return;
   }
-  const float by = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const float by = 1.0f / sum;
   char* to = p.out + ((at * p.heads + head) * kValue + 4 * half) * 2;
 #pragma unroll
   for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
-    for (int i = 0; i < 16; i += 4)
-      *reinterpret_cast<u32x2*>(to + (b * 32 + 2 * i) * 2) =
-          u32x2{T::pack(st.o[b][i] * by, st.o[b][i + 1] * by),
-                T::pack(st.o[b][i + 2] * by, st.o[b][i + 3] * by)};
+    for (int i = 0; i < 16; i += 4) {
+      const u32x2 v = {T::pack(st.o[b][i] * by, st.o[b][i + 1] * by),
+                       T::pack(st.o[b][i + 2] * by, st.o[b][i + 3] * by)};
+      // (zeros where nothing was seen: the sums may not be, by infinite values that others saw)
+      *reinterpret_cast<u32x2*>(to + (b * 32 + 2 * i) * 2) = sum == 0.0f ? u32x2{} : v;
+    }
   if (p.lse && half == 0) p.lse[at * p.heads + head] = (st.top + log2f(sum)) * kLn2;
 }
 

@@ -394,12 +394,14 @@ __device__ __forceinline__ void put(const State<P>& st, float top, float sum, co
   const int group = lane >> 4;
   // register i of block b: element b * 16 + 4 * group + i of the head's vector
   if (to.splits == 1) {
-    const float by = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const float by = 1.0f / sum;
     char* out = to.out + ((row * to.heads + head) * P::kLatent + 4 * group) * 2;
 #pragma unroll
-    for (int b = 0; b < P::kBlocks; ++b)
-      *reinterpret_cast<u32x2*>(out + b * 32) = u32x2{T::pack(st.o[b][0] * by, st.o[b][1] * by),
-                                                     T::pack(st.o[b][2] * by, st.o[b][3] * by)};
+    for (int b = 0; b < P::kBlocks; ++b) {
+      const u32x2 v = {T::pack(st.o[b][0] * by, st.o[b][1] * by), T::pack(st.o[b][2] * by, st.o[b][3] * by)};
+      // (zeros where nothing was seen: the sums may not be, by infinite numbers that others saw)
+      *reinterpret_cast<u32x2*>(out + b * 32) = sum == 0.0f ? u32x2{} : v;
+    }
     if (to.lse && group == 0) to.lse[row * to.heads + head] = (top + log2f(sum)) * kLn2;
   } else {
     const int64_t at = (row * to.splits + split) * to.heads + head;

@@ -192,7 +192,7 @@ template <class T>
 __device__ __forceinline__ void put_wide(Args& p, const WideState& st, bool whole, int64_t row, int32_t head,
                                          const Slot& to, int lane) {
   const int half = lane >> 5;
-  const float by = !whole ? 1.0f : st.sum == 0.0f ? 0.0f : 1.0f / st.sum;
+  const float by = whole ? 1.0f / st.sum : 1.0f;
   char* out = p.out + ((row * p.heads + head) * Wide::kLatent + 4 * half) * 2;
   float* part = to.part + half * to.step;
   if (whole) {
@@ -209,8 +209,9 @@ __device__ __forceinline__ void put_wide(Args& p, const WideState& st, bool whol
 #pragma unroll
     for (int i = 0; i < 16; i += 4) {
       const f32x4 v = f32x4{st.o[b][i], st.o[b][i + 1], st.o[b][i + 2], st.o[b][i + 3]} * by;
-      if (whole)
-        *reinterpret_cast<u32x2*>(out + (b * 32 + 2 * i) * 2) = u32x2{T::pack(v[0], v[1]), T::pack(v[2], v[3])};
+      const u32x2 y = {T::pack(v[0], v[1]), T::pack(v[2], v[3])};
+      if (whole)  // (zeros where nothing was seen, whatever others saw)
+        *reinterpret_cast<u32x2*>(out + (b * 32 + 2 * i) * 2) = st.sum == 0.0f ? u32x2{} : y;
       else
         *reinterpret_cast<f32x4*>(part + (8 * b + i / 2) * to.step) = v;
     }
